@@ -1,5 +1,6 @@
 """Python binding of libnvfp4moe.so, the NVFP4 weight-only MoE library for
-B200 (sm_100a).
+B200 (sm_100a), and of libnvfp4dense.so, the dense feed-forward operators next
+to it.
 
 Two layers:
   * the C ABI under its own names (`nvfp4_quantize`, `moe_route`,
@@ -7,7 +8,9 @@ Two layers:
     device pointers and sizes, returning the status code;
   * torch conveniences (`quantize`, `dequantize`, `route`, `permute`,
     `MoeLayer`, `residual_rmsnorm`): they allocate outputs and workspaces with torch and
-    pass pointers to the same C calls on torch's current stream.
+    pass pointers to the same C calls on torch's current stream;
+  * the dense operators in the same two layers (`dense_capi`; `mxfp4_quantize`,
+    `mxfp4_linear`, `mxfp4_linear_a4`, `gated_ffn`, ...).
 
 Every computation runs in the library's CUDA kernels; there is no fallback.
 The shared library is loaded on first use of anything but `build`; that use
@@ -20,14 +23,18 @@ import importlib
 
 _API = {"MoeLayer", "MoeBlock", "DenseParts", "Aff4Experts", "Aff4Layer", "W4A4Layer", "Router", "Experts", "quantize", "dequantize", "route", "permute", "residual_rmsnorm",
         "device_status", "forward_views", "unscaled_hidden"}
+_DENSE = {"Mxfp4Weight", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_linear_a4", "gated_ffn",
+          "gated_ffn_forward", "gated_ffn_backward"}
 _CAPI = {"NVFP4Error", "check", "status_string"}
 
-__all__ = sorted(_API | _CAPI | {"capi", "build"})
+__all__ = sorted(_API | _DENSE | _CAPI | {"capi", "dense_capi", "build"})
 
 
 def __getattr__(name):
-    if name == "capi":
-        return importlib.import_module(".capi", __name__)
+    if name in ("capi", "dense_capi"):
+        return importlib.import_module("." + name, __name__)
+    if name in _DENSE:
+        return getattr(importlib.import_module(".dense", __name__), name)
     if name in _CAPI:
         return getattr(importlib.import_module(".capi", __name__), name)
     if name in _API:

@@ -441,4 +441,7 @@ def residual_rmsnorm(res: torch.Tensor, y: torch.Tensor | None, x_out: torch.Ten
 
 
 def device_status(stream=None) -> int:
-    return capi.nvfp4_get_device_status(_stream(stream))
+    """The first recorded device error of either library (0 if none), cleared."""
+    from . import dense_capi
+    first = capi.nvfp4_get_device_status(_stream(stream))
+    return dense_capi.nvfp4dense_get_device_status(_stream(stream)) or first

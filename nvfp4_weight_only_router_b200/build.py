@@ -1,10 +1,12 @@
-"""Build the in-tree shared library libnvfp4moe.so for sm_100a with nvcc.
+"""Build the in-tree shared libraries libnvfp4moe.so (csrc/*.cu) and
+libnvfp4dense.so (csrc/dense/*.cu and the host helpers it shares) for sm_100a
+with nvcc.
 
     python -m nvfp4_weight_only_router_b200.build [--force] [--verbose]
 
-Each csrc/*.cu is compiled to an object under _build/ and linked into
-nvfp4_weight_only_router_b200/libnvfp4moe.so.  Sources are rebuilt when they
-or any header is newer than their object.
+Each source is compiled to an object under _build/ and linked into its
+library in nvfp4_weight_only_router_b200/.  Sources are rebuilt when they or
+any header is newer than their object.
 """
 from __future__ import annotations
 
@@ -13,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
+DENSE_LIB = os.path.join(PKG, "libnvfp4dense.so")
+DENSE_SHARED = ("host_util", "tma_map")  # csrc/*.cu that the dense library links too
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden", "--expt-relaxed-constexpr",
@@ -33,35 +38,44 @@ def nvcc() -> str:
 
 
 def _headers() -> list[str]:
-    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h"))
+    return [h for d in (CSRC, os.path.join(CSRC, "dense")) for e in ("*.cuh", "*.h")
+            for h in glob.glob(os.path.join(d, e))] + glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    hdr_mtime = max([os.path.getmtime(h) for h in _headers()] + [0.0])
-    objs = []
     flags = NVCC_FLAGS + (extra_flags or [])
-    for src in srcs:
-        obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        objs.append(obj)
-        if (not force and os.path.exists(obj) and os.path.getmtime(obj) >= os.path.getmtime(src)
-                and os.path.getmtime(obj) >= hdr_mtime):
-            continue
-        cmd = [nvcc()] + ARCH + flags + ["-c", src, "-o", obj]
-        if verbose:
-            cmd.insert(1, "-Xptxas=-v")
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-    if force or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
-        tmp = LIB + ".tmp"
-        cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
-        os.replace(tmp, LIB)
+    hdr_mtime = max([os.path.getmtime(h) for h in _headers()] + [0.0])
+    main = {src: _object(src) for src in sorted(glob.glob(os.path.join(CSRC, "*.cu")))}
+    dense = {src: _object(src, "dense_") for src in sorted(glob.glob(os.path.join(CSRC, "dense", "*.cu")))}
+    stale = [(src, obj) for src, obj in {**main, **dense}.items()
+             if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr_mtime)]
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        list(pool.map(lambda so: _compile(*so, flags, verbose), stale))
+    _link(LIB, list(main.values()), force, verbose)
+    _link(DENSE_LIB, list(dense.values()) + [_object(os.path.join(CSRC, n + ".cu")) for n in DENSE_SHARED], force, verbose)
     return LIB
+
+
+def _object(src: str, prefix: str = "") -> str:
+    return os.path.join(BUILD, prefix + os.path.basename(src)[:-3] + ".o")
+
+
+def _run(cmd: list[str], verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+
+
+def _compile(src: str, obj: str, flags: list[str], verbose: bool) -> None:
+    _run([nvcc()] + (["-Xptxas=-v"] if verbose else []) + ARCH + flags + ["-c", src, "-o", obj], verbose)
+
+
+def _link(lib: str, objs: list[str], force: bool, verbose: bool) -> None:
+    if force or not os.path.exists(lib) or any(os.path.getmtime(o) > os.path.getmtime(lib) for o in objs):
+        tmp = lib + ".tmp"
+        _run([nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs, verbose)
+        os.replace(tmp, lib)
 
 
 if __name__ == "__main__":

@@ -135,11 +135,11 @@ for _name, (_res, _args) in SIGNATURES.items():
 
 
 class NVFP4Error(RuntimeError):
-    def __init__(self, status: int, what: str = ""):
+    def __init__(self, status: int, what: str = "", cuda_error: str | None = None):
         self.status = status
         msg = f"{what}: {STATUS.get(status, status)} ({status_string(status)})"
         if status == NVFP4_ERR_CUDA:
-            msg += f": {lib.nvfp4_last_cuda_error().decode()}"
+            msg += f": {cuda_error or lib.nvfp4_last_cuda_error().decode()}"
         super().__init__(msg)
 
 

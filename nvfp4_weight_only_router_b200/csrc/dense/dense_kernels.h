@@ -1,0 +1,121 @@
+// Internal launch interface between the dense C ABI (api_dense.cu) and its
+// kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../kernels.h"
+
+namespace nvfp4moe {
+
+// element types and activations, as in nvfp4dense.h
+constexpr int kBf16 = 0, kF16 = 1, kF32 = 2;
+constexpr int kActNone = 0, kActGelu = 1, kActSilu = 2;
+
+constexpr int kMxBlock = 32;    // elements per E8M0 scale
+constexpr int kSfChunkB = 512;  // block scales of 128 rows x 4 blocks in the tensor core's order
+
+inline int64_t mx_blocks(int64_t K) { return (K + kMxBlock - 1) / kMxBlock; }
+inline int64_t mx_pitch(int64_t K) { return mx_blocks(K) * (kMxBlock / 2); }
+// 512-byte scale chunks along K: whole stages of 256 elements
+inline int mx_sf_chunks(int K) { return (K + 255) / 256 * 2; }
+
+// ------------------------------------------------------------ mxfp4_quant.cu
+cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ldx, uint8_t* codes,
+                                  uint8_t* scales, cudaStream_t st);
+cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out,
+                                    int dtype, cudaStream_t st);
+// x [T, K] -> codes [T, K/2] and scale chunks; and the weight's row-major
+// scales -> the chunks of each bn-row tile of the product (one launch)
+struct MxPrepArgs {
+  const void* x;
+  int dtype;
+  int T, K;
+  int64_t ldx;
+  uint8_t* xq;           // [T, K/2]
+  uint8_t* xsf;          // [ceil(T/128)][chunks][512]
+  const uint8_t* wscales;  // [N (gated: 2 N), K/32]
+  int N;                 // output columns
+  bool gated;            // a tile: bn/2 gate rows, then their bn/2 up rows
+  int bn;
+  uint8_t* wsf;          // [mx_wsf_blocks][chunks][512]
+};
+// 128-row scale blocks of the weight: max(1, bn/128) for each tile
+inline int64_t mx_wsf_blocks(int N, bool gated, int bn) {
+  const int tn = gated ? bn / 2 : bn;
+  return (int64_t)((N + tn - 1) / tn) * (bn >= 256 ? 2 : 1);
+}
+cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- skinny.cu
+constexpr int kSkinnyMaxTokens = 32;
+struct SkinnyArgs {
+  const void* x;      // [T, K]
+  int64_t ldx;        // elements
+  const void* w0;     // 16-bit: [N, K] (gate); MXFP4: codes
+  const void* w1;     // 16-bit gated: up [N, K]
+  const uint8_t* scales;  // MXFP4
+  void* y;            // [T, N]
+  int T, N, K;        // N: output columns
+  int act;            // kActNone: plain; else gated
+  int dtype;          // of x and y
+  bool mx;            // MXFP4 weights
+  bool quant_x;       // x through MXFP4 first
+  bool after_producer;  // x is written by the kernel launched just before on the stream
+};
+cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st);
+
+// ------------------------------------------------------------- pair_gemm.cu
+// A stage of the operands of one product: A [M, K] and B [N, K] by pointer and
+// row pitch in elements; *_mn: stored with K outermost ([K, M], [K, N]).
+struct PairOperand {
+  const void* p;
+  int64_t ld;
+  bool mn;
+};
+struct PairSegment {
+  PairOperand a, b;
+  int K;
+};
+struct PairGemm {
+  PairSegment seg[2];
+  int nseg;
+  int M, N;       // output rows and columns
+  void* out;      // [M, N], 16-bit, pitch N
+};
+constexpr int kPairMaxProblems = 4;
+// plain products, one launch for all (at most kPairMaxProblems); out = sum over segments A B^T
+cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st);
+// h = act(x gate^T) * (x up^T); g, u (16-bit, may be null) kept for the backward pass
+struct PairGated {
+  const void *x, *gate, *up;
+  int64_t ldx;
+  int64_t ldw;
+  int T, I, K;
+  int act, dtype;
+  void *h, *g, *u;
+};
+cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st);
+// dh = dy down with dg = dh u act'(g), du = dh act(g) written in its place
+struct PairGatedBwd {
+  const void* dy;         // [T, H]
+  int64_t lddy;
+  const void* down;       // [H, I]
+  int T, H, I;
+  int act, dtype;
+  const void *g, *u;
+  void *dg, *du;
+};
+cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
+// MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns)
+struct PairMx {
+  const uint8_t *xq, *xsf, *wq, *wsf;
+  int T, N, K;
+  int act, dtype, bn;  // bn: pair_mx_tile of the same product
+  void* y;
+};
+int pair_mx_tile(int T, int N, int act);
+cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st);
+
+}  // namespace nvfp4moe

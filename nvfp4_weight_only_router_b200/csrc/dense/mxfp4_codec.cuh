@@ -1,0 +1,123 @@
+// MXFP4 (E2M1 codes, one power-of-two scale byte per 32 elements): block
+// encoding and decoding shared by the quantiser, the products' operand
+// loads and the dequantiser.
+#pragma once
+
+#include "../common.cuh"
+#include "../nvfp4_encode.cuh"
+#include "dense_kernels.h"
+
+namespace nvfp4moe {
+
+// Scale byte X + 127 of a block whose largest magnitude is amax >= 0, with
+// X = floor(log2 amax) - 2 clamped to [-127, 127] (2 is the exponent of the
+// largest E2M1 value, 6 = 1.5 * 2^2).  The exponent field of a normal fp32 is
+// floor(log2) + 127; every subnormal amax and zero clamp to X = -127, and the
+// largest finite amax gives X = 125.  255 (NaN) for an infinity or a NaN,
+// which the caller leaves in amax's exponent field.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 23);
+  return e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+}
+
+// 2^-X as fp32 for a scale byte 0..252 (X = -127 gives 2^127, X = 125 gives 2^-125).
+__device__ __forceinline__ float mx_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// 2^X as fp32: subnormal at byte 0, NaN at byte 255.
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : (byte == 0u ? 0x00400000u : byte << 23));
+}
+
+// Bits of the largest |v| with NaN above infinity above every finite value.
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Eight E2M1 codes of v * inv (element i in nibble i).  The product is exact
+// unless it is subnormal, far below the grid's first threshold.
+__device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t byte) {
+  if (byte == 255u) return 0u;
+  const float inv = mx_inv_scale(byte);
+  float s[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = v[k] * inv;
+  return e2m1x8_rne(s);
+}
+
+// The two factors that turn a code's bits placed at a bf16's sign, two low
+// exponent bits and top mantissa bit (v 2^-126, subnormal codes included)
+// into v 2^X: 2^(126 + X) for X <= 1, and 2^127 followed by 2^(X - 1) above.
+struct MxFactor {
+  uint32_t f0, f1;  // bf16x2; f1 applies where big
+  bool big;
+};
+__device__ __forceinline__ MxFactor mx_factor(uint32_t byte) {
+  MxFactor m;
+  const uint32_t h = byte == 255u ? 0x7FFFu : (min(byte, 128u) + 126u) << 7;
+  m.f0 = h | (h << 16);
+  m.big = byte > 128u && byte != 255u;
+  const uint32_t b = (byte - 1u) << 7;
+  m.f1 = b | (b << 16);
+  return m;
+}
+
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t o;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+  return o;
+}
+
+// Eight codes (a 32-bit word) -> four bf16x2 of elements (j, j + 4), j = 0..3,
+// scaled by 2^X (exact: E2M1 times a power of two is a bf16 unless it
+// overflows or lies below 2^-133).
+__device__ __forceinline__ void mx_decode8(uint32_t w, const MxFactor& m, uint32_t (&o)[4]) {
+  constexpr uint32_t M = 0x01C001C0u, S = 0x80008000u;
+  o[0] = ((w << 6) & M) | ((w << 12) & S);
+  o[1] = ((w << 2) & M) | ((w << 8) & S);
+  o[2] = ((w >> 2) & M) | ((w << 4) & S);
+  o[3] = ((w >> 6) & M) | (w & S);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = bmul2(o[j], m.f0);
+  if (m.big) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = bmul2(o[j], m.f1);
+  }
+}
+
+// ------------------------------------------------------------ 16-bit elements
+__device__ __forceinline__ uint32_t pack16x2(float lo, float hi, bool f16) {
+  uint32_t o;
+  if (f16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+  return o;
+}
+__device__ __forceinline__ void unpack16x2(uint32_t v, bool f16, float& lo, float& hi) {
+  if (f16) {
+    lo = __half2float(__ushort_as_half((unsigned short)(v & 0xFFFFu)));
+    hi = __half2float(__ushort_as_half((unsigned short)(v >> 16)));
+  } else {
+    lo = __uint_as_float(v << 16);
+    hi = __uint_as_float(v & 0xFFFF0000u);
+  }
+}
+
+// ---------------------------------------------------------------- activations
+// gelu_tanh (common.cuh) and silu, with their derivatives, in fp32.  With
+// s = 1 / (1 + exp(-z)), silu: z = g, gelu_tanh: z = 2 sqrt(2/pi) (g + 0.044715 g^3):
+// act = g s, act' = s + g s (1 - s) dz/dg.
+__device__ __forceinline__ float act_fwd(float g, int act) {
+  return act == kActSilu ? g / (1.0f + __expf(-g)) : gelu_tanh(g);
+}
+__device__ __forceinline__ void act_fwd_grad(float g, int act, float& a, float& da) {
+  a = act_fwd(g, act);
+  // s (1 - s) is 0 in fp32 beyond |z| ~ 104, reached before |g| = 128 by both;
+  // the clamp keeps g^2 finite there and lets a NaN through
+  const float c = fabsf(g) > 128.0f ? copysignf(128.0f, g) : g;
+  const float k0 = 1.5957691216057308f, k1 = 0.044715f;  // 2 sqrt(2 / pi)
+  const float z = act == kActSilu ? c : k0 * (c + k1 * c * c * c);
+  const float dz = act == kActSilu ? 1.0f : k0 * (1.0f + 3.0f * k1 * c * c);
+  const float s = 1.0f / (1.0f + __expf(-z));
+  // 1 - s as s(-z) keeps its relative accuracy for large z
+  const float r = 1.0f / (1.0f + __expf(z));
+  da = s + c * s * r * dz;
+}
+
+}  // namespace nvfp4moe

@@ -1,0 +1,682 @@
+// Dense products on the 5th-generation tensor cores, two SMs per tile
+// (cta_group::2): D[256 rows, BN columns] += A[256, k] B[BN, k]^T with fp32
+// accumulators in tensor memory.  16-bit operands (kind::f16, 64 elements of K
+// per stage) or MXFP4 operands (kind::mxf4, E2M1 with an E8M0 scale per 32,
+// 256 elements per stage).
+//
+// Bound by the tensor pipe, and for MXFP4 by the bytes an SM can draw from L2:
+// a stage's operands are read once per tile, so a pair of SMs shares one
+// 256-column B tile (each loads half of it) and every byte of A and B feeds
+// 256 columns or rows.
+//
+// Forms:
+//   plain   out = sum over K segments A B^T, 16-bit; several products in one
+//           launch (their tiles in one list, so that the last wave of one is
+//           filled by the next).  An operand may be stored with K outermost
+//           (the transposes of a backward pass); TMA then brings 64 x 64
+//           boxes and the descriptors say M- or N-major.
+//   gated   B's halves are gate rows and up rows of the same hidden units (SM 0
+//           loads the gate half, SM 1 the up half); each accumulator row then
+//           holds both, and the epilogue writes act(g) u, and g and u if kept.
+//   gated backward   the accumulators are dh; the epilogue reads g and u and
+//           writes dg = dh u act'(g) and du = dh act(g), so dh never leaves
+//           the chip.
+//
+// Warps: 0 TMA producer (in both SMs), 1 MMA issuer (in SM 0 of the pair; the
+// whole warp runs the loop and one elected lane issues), 4-11 epilogue: a warp
+// per tensor-memory lane quarter and column half.  With two accumulators a
+// tile's epilogue overlaps the next tile's products; the 256-column MXFP4 tile
+// has one (scales need the other columns).  Every wait is bounded in wall
+// time; one that gives up records a timeout and the pair tears down.
+#include <algorithm>
+#include <cstring>
+
+#include "../tc_common.cuh"
+#include "mxfp4_codec.cuh"
+
+namespace nvfp4moe {
+
+namespace {
+
+constexpr int kPThreads = 384;
+constexpr int kPProd = 0, kPMma = 1, kPEpi0 = 4, kPEpiWarps = 8;
+constexpr int kPTmem = 512;
+constexpr int kKind16 = 0, kKindMx = 1;
+constexpr int kEpiPlain = 0, kEpiGated = 1, kEpiGatedBwd = 2;
+
+template <int KIND, int BN>
+struct PCfg {
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = BN / 2 * 128;
+  static constexpr int SFB_BLK = BN >= 256 ? 2 : 1;                 // 128-row scale blocks of B
+  static constexpr int SFA_BYTES = KIND == kKindMx ? 2 * kSfChunkB : 0;
+  static constexpr int SFB_BYTES = KIND == kKindMx ? SFB_BLK * 2 * kSfChunkB : 0;
+  static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int NS_RAW = (225 * 1024) / STAGE;
+  static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
+  static constexpr int NACC = (KIND == kKindMx && BN == 256) ? 1 : 2;
+  static constexpr int SF_COL0 = NACC * BN;
+  static constexpr int SF_COLS = 8 + 8 * SFB_BLK;                   // per stage
+  static_assert(KIND == kKind16 ? NACC * BN <= kPTmem : SF_COL0 + NS * SF_COLS <= kPTmem, "tensor memory");
+};
+
+template <int KIND, int BN>
+struct alignas(1024) PSmem {
+  using C = PCfg<KIND, BN>;
+  uint8_t a[C::NS][C::A_BYTES];
+  uint8_t b[C::NS][C::B_BYTES];
+  uint8_t sfa[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::SFA_BYTES : 16];
+  uint8_t sfb[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::SFB_BYTES : 16];
+  uint64_t full[C::NS], empty[C::NS];  // full: SM 0's barrier counts both SMs' bytes
+  uint64_t d_full[2], d_empty[2];      // d_empty: SM 0's, arrivals of both SMs' epilogues
+  uint64_t fin;
+  uint32_t taddr;
+  int abort_flag;
+  int issued;
+};
+
+struct alignas(64) PProb {
+  CUtensorMap a[2], b[2];  // by K segment; gated: b[0] gate rows, b[1] up rows
+  void* out;
+  int M, N;                // output rows and columns
+  int kc0, kc;             // K stages of segment 0 and in all
+  int tm, t0;              // tiles along M; first tile in the list
+  int a_mn, b_mn;
+};
+
+struct PEpi {
+  void *g, *u;             // gated: kept g and u (or null); backward: dg and du
+  const void *gi, *ui;     // backward: g and u
+  int act, f16;
+  int ksteps;              // MXFP4: MMA steps of 64 along K
+};
+
+template <int NP>
+struct alignas(64) PParams {
+  PProb p[NP];
+  CUtensorMap sfa, sfb;    // MXFP4 scale chunks
+  PEpi e;
+  int np, n_tiles;
+  int* status;
+};
+
+// ------------------------------------------------------------------ PTX forms
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of `p` in SM 0 of the pair
+__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t n) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t n) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(n) : "memory");
+}
+// into this SM's shared memory, completing on SM 0's barrier
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {  // arrives in both SMs
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns = kWaitTimeoutNs) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > timeout_ns) return false;
+  }
+}
+__device__ __forceinline__ void mma16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                            uint32_t sfb, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// a 512-byte scale chunk of each SM's shared memory into its tensor memory
+__device__ __forceinline__ void cp_sf_pair(uint32_t taddr, uint32_t smem_addr) {
+  uint64_t d = (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)1u << 16;
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(d)
+      : "memory");
+}
+
+// Descriptor of an operand stored with K outermost: boxes of 64 (M or N) x 64
+// (K), 128-byte swizzled rows.  8-row atoms 1024 bytes apart along K (stride
+// offset), boxes 8192 bytes apart along M or N (leading offset).
+__device__ __forceinline__ uint64_t make_mn_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(8192u >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
+template <int KIND, int BN>
+__device__ __forceinline__ bool pwait(PSmem<KIND, BN>& sm, uint64_t* bar, uint32_t parity, int* status) {
+  if (wait_cluster(bar, parity)) return true;
+  atomicExch(&sm.abort_flag, 1);
+  record_status(status, kStatusTimeout);
+  return false;
+}
+
+struct PTile {
+  int prob, m, n;
+};
+template <int NP>
+__device__ __forceinline__ PTile ptile(const PParams<NP>& p, int t) {
+  PTile r;
+  r.prob = 0;
+#pragma unroll
+  for (int i = 1; i < NP; ++i)
+    if (i < p.np && t >= p.p[i].t0) r.prob = i;
+  const int l = t - p.p[r.prob].t0, tm = p.p[r.prob].tm;
+  r.m = l % tm;
+  r.n = l / tm;
+  return r;
+}
+
+// 8 consecutive 16-bit values
+__device__ __forceinline__ uint4 pack8(const float* v, bool f16) {
+  return make_uint4(pack16x2(v[0], v[1], f16), pack16x2(v[2], v[3], f16), pack16x2(v[4], v[5], f16),
+                    pack16x2(v[6], v[7], f16));
+}
+
+template <int KIND, int BN, int EPI, int NP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ PParams<NP> p) {
+  using C = PCfg<KIND, BN>;
+  using Smem = PSmem<KIND, BN>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.d_full[b], 1);
+      mbar_init(&sm.d_empty[b], 2 * kPEpiWarps);
+    }
+    mbar_init(&sm.fin, 1);
+    sm.abort_flag = 0;
+    sm.issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == kPMma) {
+    tmem_alloc2(&sm.taddr, kPTmem);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t taddr = sm.taddr;
+
+  if (warp == kPProd) {
+    // -------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      uint32_t kiter = 0;
+      bool ok = true;
+      for (int t = cluster; t < p.n_tiles && ok; t += clusters) {
+        const PTile d = ptile<NP>(p, t);
+        const PProb& q = p.p[d.prob];
+        const int arow = d.m * 256 + (int)rank * 128;
+        const int brow = EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
+        for (int kc = 0; kc < q.kc; ++kc, ++kiter) {
+          const int s = kiter % C::NS, use = kiter / C::NS;
+          if (use > 0 && !pwait(sm, &sm.empty[s], (use - 1) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = leader_addr(&sm.full[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
+          const int seg = kc >= q.kc0, kk = seg ? kc - q.kc0 : kc;
+          const uint32_t da = smem_u32(sm.a[s]), db = smem_u32(sm.b[s]);
+          if constexpr (KIND == kKind16) {
+            const CUtensorMap* ma = &q.a[seg];
+            const CUtensorMap* mb = &q.b[EPI == kEpiGated ? rank : seg];
+            if (q.a_mn) {
+              tma_load_pair(da, ma, arow, kk * 64, bar);
+              tma_load_pair(da + 8192, ma, arow + 64, kk * 64, bar);
+            } else {
+              tma_load_pair(da, ma, kk * 64, arow, bar);
+            }
+            if (BN >= 128 && q.b_mn) {
+#pragma unroll
+              for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + 8192 * j, mb, brow + 64 * j, kk * 64, bar);
+            } else {
+              tma_load_pair(db, mb, kk * 64, brow, bar);
+            }
+          } else {
+            tma_load_pair(da, &q.a[0], kk * 128, arow, bar);
+            tma_load_pair(db, &q.b[EPI == kEpiGated ? rank : 0], kk * 128, brow, bar);
+            tma_load_pair(smem_u32(sm.sfa[s]), &p.sfa, kk * 256, arow >> 7, bar);
+            tma_load_pair(smem_u32(sm.sfb[s]), &p.sfb, kk * 256, d.n * C::SFB_BLK, bar);
+          }
+          sm.issued = (int)kiter + 1;
+        }
+      }
+    }
+  } else if (warp == kPMma) {
+    // ---------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      uint32_t kiter = 0, titer = 0;
+      bool ok = true;
+      for (int t = cluster; t < p.n_tiles && ok; t += clusters, ++titer) {
+        const PTile d = ptile<NP>(p, t);
+        const PProb& q = p.p[d.prob];
+        const int db = titer % C::NACC, duse = titer / C::NACC;
+        if (duse > 0) ok = pwait(sm, &sm.d_empty[db], (duse - 1) & 1, p.status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t dcol = taddr + (uint32_t)(db * BN);
+        // D fp32 (kind::f16), M = 256, N = BN
+        uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+        if (KIND == kKind16) {
+          idesc |= 1u << 4;
+          if (!p.e.f16) idesc |= (1u << 7) | (1u << 10);
+          idesc |= (uint32_t)q.a_mn << 15 | (uint32_t)q.b_mn << 16;
+        } else {
+          idesc |= (1u << 7) | (1u << 10) | (1u << 23);  // E2M1 x E2M1, E8M0 scales
+        }
+        const uint32_t astep = KIND == kKind16 && q.a_mn ? 2048u >> 4 : 2u;
+        const uint32_t bstep = KIND == kKind16 && q.b_mn ? 2048u >> 4 : 2u;
+        for (int kc = 0; kc < q.kc; ++kc, ++kiter) {
+          const int s = kiter % C::NS, use = kiter / C::NS;
+          ok = __shfl_sync(0xffffffffu, pwait(sm, &sm.full[s], use & 1, p.status), 0);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(sm.a[s]), sb = smem_u32(sm.b[s]);
+          const uint64_t ad = KIND == kKind16 && q.a_mn ? make_mn_desc(sa) : make_sw128_desc(sa);
+          const uint64_t bd = KIND == kKind16 && q.b_mn ? make_mn_desc(sb) : make_sw128_desc(sb);
+          if constexpr (KIND == kKind16) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma16_pair(dcol, ad + (uint64_t)(kk * astep), bd + (uint64_t)(kk * bstep), idesc, kc > 0 || kk > 0);
+          } else {
+            const uint32_t ta = taddr + (uint32_t)(C::SF_COL0 + s * C::SF_COLS), tb = ta + 8;
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              cp_sf_pair(ta + 4 * ch, smem_u32(sm.sfa[s]) + ch * kSfChunkB);
+#pragma unroll
+              for (int bb = 0; bb < C::SFB_BLK; ++bb)
+                cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), smem_u32(sm.sfb[s]) + (bb * 2 + ch) * kSfChunkB);
+            }
+            const int nks = min(4, p.e.ksteps - 4 * kc);
+            for (int k = 0; k < nks; ++k) {
+              // steps 2 ch and 2 ch + 1 use scale bytes 0-1 and 2-3 of chunk ch
+              const uint32_t id = idesc | ((uint32_t)(k & 1) * 2u) << 4 | ((uint32_t)(k & 1) * 2u) << 29;
+              mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), id, ta + 4 * (k >> 1),
+                          tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+            }
+          }
+          commit_pair(&sm.empty[s]);
+        }
+        if (!ok) break;
+        commit_pair(&sm.d_full[db]);
+      }
+      // every MMA issued has completed before the tear-down
+      commit_pair(&sm.fin);
+      wait_cluster(&sm.fin, 0);
+      __syncwarp();
+    }
+  } else if (warp >= kPEpi0) {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - kPEpi0, quarter = warp & 3, half = ew >> 2;
+    const bool f16 = p.e.f16;
+    uint32_t titer = 0;
+    for (int t = cluster; t < p.n_tiles; t += clusters, ++titer) {
+      const PTile d = ptile<NP>(p, t);
+      const PProb& q = p.p[d.prob];
+      const int db = titer % C::NACC, duse = titer / C::NACC;
+      if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
+      tc_fence_after();
+      const int row = d.m * 256 + (int)rank * 128 + quarter * 32 + lane;
+      const bool rok = row < q.M;
+      const uint32_t trow = taddr + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(db * BN);
+      if constexpr (EPI == kEpiGated) {
+        constexpr int HU = BN / 4;  // hidden units of this warp
+        constexpr int CW = 16;
+        const size_t base = (size_t)row * q.N;
+#pragma unroll
+        for (int cc = 0; cc < HU / CW; ++cc) {
+          const int col = half * HU + cc * CW;
+          float g[CW], u[CW];
+          tmem_ld16(trow + col, g);
+          tmem_ld16(trow + BN / 2 + col, u);
+          const int n = d.n * (BN / 2) + col;
+#pragma unroll
+          for (int k = 0; k < CW; k += 8) {
+            if (rok && n + k < q.N) {
+              if (p.e.g) {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.g) + base + n + k) = pack8(g + k, f16);
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.u) + base + n + k) = pack8(u + k, f16);
+              }
+              float h[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) h[i] = act_fwd(g[k + i], p.e.act) * u[k + i];
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(q.out) + base + n + k) = pack8(h, f16);
+            }
+          }
+        }
+      } else {
+        constexpr int HC = BN / 2, CW = 32;
+        const size_t base = (size_t)row * q.N;
+#pragma unroll
+        for (int cc = 0; cc < HC / CW; ++cc) {
+          const int col = half * HC + cc * CW;
+          const int n = d.n * BN + col;
+          uint4 gi[EPI == kEpiGatedBwd ? 4 : 1], ui[EPI == kEpiGatedBwd ? 4 : 1];
+          if constexpr (EPI == kEpiGatedBwd) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              gi[k] = ui[k] = make_uint4(0u, 0u, 0u, 0u);
+              if (rok && n + 8 * k < q.N) {
+                gi[k] = ldg_nc_v4(static_cast<const uint16_t*>(p.e.gi) + base + n + 8 * k);
+                ui[k] = ldg_nc_v4(static_cast<const uint16_t*>(p.e.ui) + base + n + 8 * k);
+              }
+            }
+          }
+          float v[CW];
+          tmem_ld32(trow + col, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (!rok || n + 8 * k >= q.N) continue;
+            if constexpr (EPI == kEpiPlain) {
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(q.out) + base + n + 8 * k) = pack8(v + 8 * k, f16);
+            } else {
+              const uint32_t gw[4] = {gi[k].x, gi[k].y, gi[k].z, gi[k].w};
+              const uint32_t uw[4] = {ui[k].x, ui[k].y, ui[k].z, ui[k].w};
+              float dg[8], du[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float g2[2], u2[2];
+                unpack16x2(gw[i], f16, g2[0], g2[1]);
+                unpack16x2(uw[i], f16, u2[0], u2[1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float a, da;
+                  act_fwd_grad(g2[j], p.e.act, a, da);
+                  const float dh = v[8 * k + 2 * i + j];
+                  dg[2 * i + j] = dh * u2[j] * da;
+                  du[2 * i + j] = dh * a;
+                }
+              }
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.g) + base + n + 8 * k) = pack8(dg, f16);
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.u) + base + n + 8 * k) = pack8(du, f16);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(leader_addr(&sm.d_empty[db]));
+    }
+  }
+
+  // ------------------------------------------------------------- tear-down
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && sm.abort_flag) {
+    // copies in flight land before the pair leaves (SM 1's complete on SM 0's barriers)
+    for (int it = max(0, sm.issued - C::NS); it < sm.issued; ++it)
+      wait_cluster(&sm.full[it % C::NS], (it / C::NS) & 1, kAbortDrainNs);
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == kPMma) {
+    tc_fence_after();
+    tmem_dealloc2(taddr, kPTmem);
+  }
+  cluster_sync();
+}
+
+// ---------------------------------------------------------------------- host
+template <int KIND, int BN, int EPI, int NP>
+cudaError_t launch_pair(const PParams<NP>& p, cudaStream_t st) {
+  constexpr int smem = (int)sizeof(PSmem<KIND, BN>) + 1024;
+  static_assert(smem <= 232448, "shared memory budget");
+  auto fn = pair_gemm_kernel<KIND, BN, EPI, NP>;
+  cudaError_t err = configure_kernel_once((const void*)fn, smem);
+  if (err != cudaSuccess) return err;
+  int sms = 0;
+  err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  const int clusters = std::max(1, std::min(p.n_tiles, sms / 2));
+  fn<<<2 * clusters, kPThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+bool map16(CUtensorMap* m, const PairOperand& o, int rows, int K, int dtype, int box_rows) {
+  const CUtensorMapDataType dt = dtype == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  if (o.mn) return encode_tma_2d(m, dt, o.p, rows, K, o.ld * 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  return encode_tma_2d(m, dt, o.p, K, rows, o.ld * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Relative time of one tile by its column count, from the tensor pipe's share
+// at each width; the width whose whole list takes the fewest tile times wins.
+int pick_bn(int64_t tiles256, int64_t tiles128, int64_t tiles64, int clusters) {
+  auto waves = [&](int64_t t) { return (double)((t + clusters - 1) / clusters); };
+  const double c256 = waves(tiles256) * 1.0, c128 = waves(tiles128) * 0.6, c64 = tiles64 ? waves(tiles64) * 0.4 : 1e30;
+  if (c64 < c128 && c64 < c256) return 64;
+  return c128 < c256 ? 128 : 256;
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st) {
+  if (n < 1 || n > kPairMaxProblems) return cudaErrorInvalidValue;
+  int sms = 0;
+  cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  int64_t tiles[3] = {0, 0, 0};
+  bool mn = false;
+  for (int i = 0; i < n; ++i) {
+    for (int b = 0; b < 3; ++b) tiles[b] += cdiv(g[i].M, 256) * cdiv(g[i].N, 256 >> b);
+    for (int s = 0; s < g[i].nseg; ++s) mn |= g[i].seg[s].b.mn;
+  }
+  const int bn = pick_bn(tiles[0], tiles[1], mn ? 0 : tiles[2], sms / 2);
+  PParams<kPairMaxProblems> p;
+  std::memset(&p, 0, sizeof(p));
+  int t0 = 0;
+  for (int i = 0; i < n; ++i) {
+    PProb& q = p.p[i];
+    for (int s = 0; s < 2; ++s) {
+      const PairSegment& sg = g[i].seg[s < g[i].nseg ? s : 0];
+      if (!map16(&q.a[s], sg.a, g[i].M, sg.K, dtype, 128) || !map16(&q.b[s], sg.b, g[i].N, sg.K, dtype, bn / 2))
+        return cudaErrorInvalidValue;
+    }
+    q.out = g[i].out;
+    q.M = g[i].M;
+    q.N = g[i].N;
+    q.kc0 = (int)cdiv(g[i].seg[0].K, 64);
+    q.kc = q.kc0 + (g[i].nseg > 1 ? (int)cdiv(g[i].seg[1].K, 64) : 0);
+    q.tm = (int)cdiv(q.M, 256);
+    q.t0 = t0;
+    q.a_mn = g[i].seg[0].a.mn;
+    q.b_mn = g[i].seg[0].b.mn;
+    t0 += q.tm * (int)cdiv(q.N, bn);
+  }
+  p.e.f16 = dtype == kF16;
+  p.np = n;
+  p.n_tiles = t0;
+  p.status = status;
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, st);
+  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, st);
+}
+
+cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  const int64_t tm = cdiv(a.T, 256);
+  const int bn = pick_bn(tm * cdiv(a.I, 128), tm * cdiv(a.I, 64), tm * cdiv(a.I, 32), sms / 2);
+  PParams<1> p;
+  std::memset(&p, 0, sizeof(p));
+  PProb& q = p.p[0];
+  const PairOperand x{a.x, a.ldx, false}, wg{a.gate, a.ldw, false}, wu{a.up, a.ldw, false};
+  if (!map16(&q.a[0], x, a.T, a.K, a.dtype, 128) || !map16(&q.b[0], wg, a.I, a.K, a.dtype, bn / 2) ||
+      !map16(&q.b[1], wu, a.I, a.K, a.dtype, bn / 2))
+    return cudaErrorInvalidValue;
+  q.out = a.h;
+  q.M = a.T;
+  q.N = a.I;
+  q.kc0 = q.kc = (int)cdiv(a.K, 64);
+  q.tm = (int)tm;
+  p.e.g = a.g;
+  p.e.u = a.u;
+  p.e.act = a.act;
+  p.e.f16 = a.dtype == kF16;
+  p.np = 1;
+  p.n_tiles = (int)(tm * cdiv(a.I, bn / 2));
+  p.status = status;
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, st);
+  return launch_pair<kKind16, 256, kEpiGated, 1>(p, st);
+}
+
+cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  const int64_t tm = cdiv(a.T, 256);
+  const int bn = pick_bn(tm * cdiv(a.I, 256), tm * cdiv(a.I, 128), 0, sms / 2);
+  PParams<1> p;
+  std::memset(&p, 0, sizeof(p));
+  PProb& q = p.p[0];
+  const PairOperand dy{a.dy, a.lddy, false}, wd{a.down, a.I, true};
+  if (!map16(&q.a[0], dy, a.T, a.H, a.dtype, 128) || !map16(&q.b[0], wd, a.I, a.H, a.dtype, bn / 2))
+    return cudaErrorInvalidValue;
+  q.M = a.T;
+  q.N = a.I;
+  q.kc0 = q.kc = (int)cdiv(a.H, 64);
+  q.tm = (int)tm;
+  q.b_mn = 1;
+  p.e.g = a.dg;
+  p.e.u = a.du;
+  p.e.gi = a.g;
+  p.e.ui = a.u;
+  p.e.act = a.act;
+  p.e.f16 = a.dtype == kF16;
+  p.np = 1;
+  p.n_tiles = (int)(tm * cdiv(a.I, bn));
+  p.status = status;
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, st);
+  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, st);
+}
+
+int pair_mx_tile(int T, int N, int act) {
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) sms = 148;
+  const int64_t tm = cdiv(T, 256), cols = act != kActNone ? 2 * (int64_t)N : N;
+  return pick_bn(tm * cdiv(cols, 256), tm * cdiv(cols, 128), tm * cdiv(cols, 64), sms / 2);
+}
+
+cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
+  const bool gated = a.act != kActNone;
+  const int bn = a.bn, tn = gated ? bn / 2 : bn;  // output columns per tile
+  const int64_t pitch = mx_pitch(a.K), tm = cdiv(a.T, 256), tiles_n = cdiv(a.N, tn);
+  const int chunks = mx_sf_chunks(a.K), blks = bn >= 256 ? 2 : 1;
+  PParams<1> p;
+  std::memset(&p, 0, sizeof(p));
+  PProb& q = p.p[0];
+  const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, ns = CU_TENSOR_MAP_SWIZZLE_NONE;
+  if (!encode_tma_2d(&q.a[0], u8, a.xq, a.K / 2, a.T, pitch, 128, 128, sw) ||
+      !encode_tma_2d(&q.b[0], u8, a.wq, a.K / 2, a.N, pitch, 128, bn / 2, sw) ||
+      !encode_tma_2d(&q.b[1], u8, a.wq + (gated ? a.N * pitch : 0), a.K / 2, a.N, pitch, 128, bn / 2, sw) ||
+      !encode_tma_2d(&p.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.xsf, (uint64_t)chunks * 128, cdiv(a.T, 128),
+                     (uint64_t)chunks * kSfChunkB, 256, 1, ns) ||
+      !encode_tma_2d(&p.sfb, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.wsf, (uint64_t)chunks * 128, tiles_n * blks,
+                     (uint64_t)chunks * kSfChunkB, 256, blks, ns))
+    return cudaErrorInvalidValue;
+  q.out = a.y;
+  q.M = a.T;
+  q.N = a.N;
+  q.kc0 = q.kc = (int)cdiv(a.K, 256);
+  q.tm = (int)tm;
+  p.e.act = a.act;
+  p.e.f16 = a.dtype == kF16;
+  p.e.ksteps = (int)cdiv(a.K, 64);
+  p.np = 1;
+  p.n_tiles = (int)(tm * tiles_n);
+  p.status = status;
+  if (gated) {
+    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, st);
+    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, st);
+    return launch_pair<kKindMx, 256, kEpiGated, 1>(p, st);
+  }
+  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, st);
+  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, st);
+  return launch_pair<kKindMx, 256, kEpiPlain, 1>(p, st);
+}
+
+}  // namespace nvfp4moe

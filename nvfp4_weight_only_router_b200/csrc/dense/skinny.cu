@@ -1,0 +1,250 @@
+// Products of up to 32 tokens with a weight matrix: y[t, n] = sum_k x[t, k]
+// w[n, k], optionally gated (y[t, i] = act(gate_i) up_i), with 16-bit or MXFP4
+// weights.
+//
+// Bound by the weight stream (T = 1, MXFP4 4224 x 2816: 6.3 MB) and, at these
+// sizes, by the latency of a few dependent loads, so the kernel is one wave of
+// small CTAs that put their whole share of the weights in flight at once: a
+// CTA owns 16 rows (gated: 8 gate rows and their 8 up rows), its 8 warps take
+// interleaved steps of K, and the 8 partial tiles meet in shared memory.  The
+// products run on the warp-level tensor instruction m16n8k16 (the memory pipe
+// is the limit, not the tensor pipe).  Its K order is free as long as both
+// operands agree, so each lane loads 16 consecutive bytes of its two rows and
+// the matching elements of x:
+//   16-bit:  8 elements, two instructions;
+//   MXFP4:   32 codes = one block with one scale, eight instructions; the
+//            codes become bf16 in registers (exact), pairing elements j and
+//            j + 4 of every 8.
+// Gated tiles put gate row i and up row i into rows r and r + 8 of the tile,
+// which one lane holds both of.  With quant_x a lane holds a whole 32-element
+// block of x per token: it quantises it to MXFP4 and back in registers (the
+// values are bf16 exactly), so the W4A4 product of few tokens is this kernel too.
+//
+// after_producer: the launch may start while the kernel before it on the
+// stream still runs (programmatic dependent launch); weights are loaded
+// first, x only after that kernel's results are visible.
+#include "mxfp4_codec.cuh"
+
+namespace nvfp4moe {
+
+namespace {
+
+constexpr int kSkThreads = 256, kSkWarps = 8;
+
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  const uint32_t a[4] = {a0, a1, a2, a3};
+  if (F16) mma_f16_16816(d, a, b0, b1);
+  else mma_bf16_16816(d, a, b0, b1);
+}
+
+struct SkinnyParams {
+  const uint8_t *x, *w0, *w1, *s0, *s1;
+  uint16_t* y;
+  int64_t ldx_bytes;
+  int T, N, units;   // units: 16-byte pieces of a weight row
+  int act;
+  bool f16;          // type of y (and of x)
+};
+
+// CODEC 0: 16-bit weights (bf16, or f16 with F16); 1: MXFP4 (bf16 products;
+// QX quantises x, of either 16-bit type).
+template <int CODEC, int NT8, bool GATED, bool OPT>
+__global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
+  constexpr bool F16 = CODEC == 0 && OPT, QX = CODEC == 1 && OPT;
+  constexpr int U = CODEC == 1 ? 3 : 6;   // steps of K in flight per warp
+  constexpr int XW = CODEC == 1 ? 4 : 1;  // 16-byte pieces of x per step and token
+  __shared__ float4 red[kSkWarps][NT8][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = lane >> 2, c = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int row_a = GATED ? blockIdx.x * 8 + r : blockIdx.x * 16 + r;
+  const int row_b = GATED ? row_a : row_a + 8;
+  const bool ok_a = row_a < p.N, ok_b = row_b < p.N;
+  const size_t pitch = (size_t)p.units * 16;
+  const uint8_t* wa = p.w0 + (ok_a ? row_a : 0) * pitch;
+  const uint8_t* wb = (GATED ? p.w1 : p.w0) + (ok_b ? row_b : 0) * pitch;
+  const uint8_t* sa = CODEC == 1 ? p.s0 + (size_t)(ok_a ? row_a : 0) * p.units : nullptr;
+  const uint8_t* sb = CODEC == 1 ? (GATED ? p.s1 : p.s0) + (size_t)(ok_b ? row_b : 0) * p.units : nullptr;
+
+  float acc[NT8][4];
+#pragma unroll
+  for (int j = 0; j < NT8; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+
+  const int steps = (p.units + 3) / 4;
+  bool first = true;
+  for (int s0 = warp; s0 < steps; s0 += kSkWarps * U) {
+    uint4 va[U], vb[U];
+    uint32_t ca[U], cb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int unit = 4 * (s0 + u * kSkWarps) + c;
+      va[u] = vb[u] = make_uint4(0u, 0u, 0u, 0u);
+      ca[u] = cb[u] = 0u;
+      if (unit < p.units) {
+        va[u] = ldg_nc_v4(wa + (size_t)unit * 16);
+        vb[u] = ldg_nc_v4(wb + (size_t)unit * 16);
+        if (CODEC == 1) {
+          ca[u] = __ldg(sa + unit);
+          cb[u] = __ldg(sb + unit);
+        }
+      }
+    }
+    if (first) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      first = false;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int unit = 4 * (s0 + u * kSkWarps) + c;
+      if (4 * (s0 + u * kSkWarps) >= p.units) break;  // the same for the whole warp
+      uint4 xv[NT8][XW];
+#pragma unroll
+      for (int j = 0; j < NT8; ++j) {
+        const int t = j * 8 + r;
+#pragma unroll
+        for (int i = 0; i < XW; ++i) {
+          xv[j][i] = make_uint4(0u, 0u, 0u, 0u);
+          // plain loads: x may have been written by the kernel before
+          if (t < p.T && unit < p.units)
+            xv[j][i] = *reinterpret_cast<const uint4*>(p.x + (size_t)t * p.ldx_bytes + ((size_t)unit * XW + i) * 16);
+        }
+      }
+      if constexpr (CODEC == 0) {
+#pragma unroll
+        for (int j = 0; j < NT8; ++j) {
+          mma16<F16>(acc[j], va[u].x, vb[u].x, va[u].y, vb[u].y, xv[j][0].x, xv[j][0].y);
+          mma16<F16>(acc[j], va[u].z, vb[u].z, va[u].w, vb[u].w, xv[j][0].z, xv[j][0].w);
+        }
+      } else {
+        const MxFactor fa = mx_factor(ca[u]), fb = mx_factor(cb[u]);
+        MxFactor fx[NT8];
+        uint32_t xq[NT8][4];
+        if constexpr (QX) {
+#pragma unroll
+          for (int j = 0; j < NT8; ++j) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&xv[j][0]);
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+            float lo, hi;
+            unpack16x2(m2, p.f16, lo, hi);
+            const uint32_t byte = mx_scale_byte(max(abs_bits(lo), abs_bits(hi)));
+            fx[j] = mx_factor(byte);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) unpack16x2(w[4 * q + k], p.f16, v[2 * k], v[2 * k + 1]);
+              xq[j][q] = mx_encode8(v, byte);
+            }
+          }
+        }
+        const uint32_t wav[4] = {va[u].x, va[u].y, va[u].z, va[u].w}, wbv[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[4], b[4];
+          mx_decode8(wav[q], fa, a);
+          mx_decode8(wbv[q], fb, b);
+#pragma unroll
+          for (int j = 0; j < NT8; ++j) {
+            uint32_t o[4];
+            if constexpr (QX) {
+              mx_decode8(xq[j][q], fx[j], o);
+            } else {
+              const uint4 xw = xv[j][q];
+              o[0] = __byte_perm(xw.x, xw.z, 0x5410);
+              o[1] = __byte_perm(xw.x, xw.z, 0x7632);
+              o[2] = __byte_perm(xw.y, xw.w, 0x5410);
+              o[3] = __byte_perm(xw.y, xw.w, 0x7632);
+            }
+            mma16<false>(acc[j], a[0], b[0], a[1], b[1], o[0], o[1]);
+            mma16<false>(acc[j], a[2], b[2], a[3], b[3], o[2], o[3]);
+          }
+        }
+      }
+    }
+  }
+  // y may still be read by the kernel before (a user's buffer): no store ahead of it
+  if (first) asm volatile("griddepcontrol.wait;" ::: "memory");
+
+#pragma unroll
+  for (int j = 0; j < NT8; ++j) red[warp][j][lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+  __syncthreads();
+  if (threadIdx.x < 32 * NT8) {
+    const int j = threadIdx.x >> 5;
+    float4 d = red[0][j][lane];
+#pragma unroll
+    for (int w = 1; w < kSkWarps; ++w) {
+      const float4 e = red[w][j][lane];
+      d.x += e.x; d.y += e.y; d.z += e.z; d.w += e.w;
+    }
+    const int t0 = j * 8 + 2 * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + i;
+      if (t >= p.T) break;
+      const float v0 = i ? d.y : d.x, v1 = i ? d.w : d.z;
+      uint16_t* y = p.y + (size_t)t * p.N;
+      if (GATED) {
+        if (ok_a) y[row_a] = (uint16_t)pack16x2(act_fwd(v0, p.act) * v1, 0.f, p.f16);
+      } else {
+        const uint32_t v = pack16x2(v0, v1, p.f16);
+        if (ok_a) y[row_a] = (uint16_t)v;
+        if (ok_b) y[row_b] = (uint16_t)(v >> 16);
+      }
+    }
+  }
+}
+
+template <int CODEC, bool GATED, bool OPT>
+cudaError_t launch_nt(const SkinnyParams& p, int T, bool after, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  const int rows = GATED ? 8 : 16;
+  cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows));
+  cfg.blockDim = dim3(kSkThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  if (T <= 8) return cudaLaunchKernelEx(&cfg, skinny_kernel<CODEC, 1, GATED, OPT>, p);
+  if (T <= 16) return cudaLaunchKernelEx(&cfg, skinny_kernel<CODEC, 2, GATED, OPT>, p);
+  return cudaLaunchKernelEx(&cfg, skinny_kernel<CODEC, 4, GATED, OPT>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
+  const bool gated = a.act != kActNone;
+  SkinnyParams p{};
+  p.x = static_cast<const uint8_t*>(a.x);
+  p.w0 = static_cast<const uint8_t*>(a.w0);
+  p.w1 = static_cast<const uint8_t*>(a.w1);
+  p.units = a.mx ? a.K / 32 : a.K / 8;
+  p.s0 = a.scales;
+  if (a.mx && gated) {
+    p.w1 = p.w0 + (size_t)a.N * p.units * 16;
+    p.s1 = p.s0 + (size_t)a.N * p.units;
+  }
+  p.y = static_cast<uint16_t*>(a.y);
+  p.ldx_bytes = a.ldx * 2;
+  p.T = a.T;
+  p.N = a.N;
+  p.act = a.act;
+  p.f16 = a.dtype == kF16;
+  const bool opt = a.mx ? a.quant_x : p.f16;
+  if (a.mx) {
+    if (gated) return opt ? launch_nt<1, true, true>(p, a.T, a.after_producer, st) : launch_nt<1, true, false>(p, a.T, a.after_producer, st);
+    return opt ? launch_nt<1, false, true>(p, a.T, a.after_producer, st) : launch_nt<1, false, false>(p, a.T, a.after_producer, st);
+  }
+  if (gated) return opt ? launch_nt<0, true, true>(p, a.T, a.after_producer, st) : launch_nt<0, true, false>(p, a.T, a.after_producer, st);
+  return opt ? launch_nt<0, false, true>(p, a.T, a.after_producer, st) : launch_nt<0, false, false>(p, a.T, a.after_producer, st);
+}
+
+}  // namespace nvfp4moe

@@ -1,0 +1,270 @@
+"""torch conveniences over the dense feed-forward C ABI (include/nvfp4dense.h):
+MXFP4 quantisation, products with MXFP4 weights, and the gated feed-forward
+block with its backward pass.
+
+Every function runs on torch's current stream of the tensors' device, or on
+`stream`; outputs and workspaces are allocated on that stream, per call, so
+that calls may overlap and be captured freely.  Tensors are [rows, features]
+with contiguous features; x (and dy) may be row-strided views.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import dataclasses
+
+import torch
+
+from . import dense_capi as dc
+from .dense_capi import check
+
+_DTYPE = {torch.bfloat16: dc.BF16, torch.float16: dc.F16, torch.float32: dc.F32}
+_ACT = {None: dc.ACT_NONE, "gelu_tanh": dc.ACT_GELU_TANH, "silu": dc.ACT_SILU}
+_byref = ctypes.byref
+_HERE = contextlib.nullcontext()
+
+
+def _act(name, gated: bool = False) -> int:
+    if name not in _ACT or (gated and name is None):
+        raise ValueError(f"activation must be 'gelu_tanh' or 'silu'{'' if gated else ' or None'}, not {name!r}")
+    return _ACT[name]
+
+
+def _rows(t: torch.Tensor, what: str, features: int | None = None) -> int:
+    """Checks a [rows, features] device tensor; its row stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a CUDA device")
+    if t.dim() != 2 or (features is not None and t.shape[1] != features):
+        raise ValueError(f"{what} must be a tensor [rows, {'features' if features is None else features}], "
+                         f"not {list(t.shape)}")
+    n, f = t.shape
+    if f > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous features")
+    if n <= 1:
+        return f
+    if t.stride(0) < f:
+        raise ValueError(f"{what} has overlapping rows")
+    return t.stride(0)
+
+
+def _same(what: str, *tensors: torch.Tensor) -> None:
+    a = tensors[0]
+    for t in tensors[1:]:
+        if t.dtype != a.dtype or t.device != a.device:
+            raise ValueError(f"{what} must have one dtype and one device")
+
+
+def _contiguous(what: str, *tensors: torch.Tensor) -> None:
+    for t in tensors:
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+
+
+def _on(stream, *tensors: torch.Tensor):
+    """Context in which the call allocates and launches: the tensors' device,
+    and `stream` if given (the tensors are then also held for it)."""
+    dev = tensors[0].device
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("stream and tensors are on different devices")
+        for t in tensors:
+            t.record_stream(stream)
+        return torch.cuda.stream(stream)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_ptr(t: torch.Tensor) -> int:
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+# ------------------------------------------------------------------- MXFP4
+def mxfp4_quantize(x: torch.Tensor, stream=None):
+    """bf16, f16 or f32 [R, K] -> (codes uint8 [R, 16 ceil(K/32)], scales uint8
+    [R, ceil(K/32)]): E2M1 codes under one power-of-two scale per 32 elements."""
+    if x.dtype not in _DTYPE:
+        raise ValueError("x must be bf16, f16 or f32")
+    ld = _rows(x, "x")
+    R, K = x.shape
+    nb = (K + 31) // 32
+    with _on(stream, x):
+        codes = torch.empty((R, 16 * nb), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((R, nb), dtype=torch.uint8, device=x.device)
+        check(dc.mxfp4_quantize(x.data_ptr(), _DTYPE[x.dtype], R, K, ld, codes.data_ptr(), scales.data_ptr(),
+                                _stream_ptr(x)), "mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, K: int | None = None, dtype=torch.float32,
+                     stream=None) -> torch.Tensor:
+    """The values [R, K] of codes and scales, in f32 or bf16 (K defaults to the
+    whole blocks)."""
+    _check_codes(codes, scales)
+    R, nb = scales.shape
+    K = 32 * nb if K is None else int(K)
+    if (K + 31) // 32 != nb:
+        raise ValueError(f"K = {K} does not have {nb} blocks of 32")
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("dtype must be float32 or bfloat16")
+    with _on(stream, codes, scales):
+        out = torch.empty((R, K), dtype=dtype, device=codes.device)
+        check(dc.mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), R, K, out.data_ptr(), _DTYPE[dtype],
+                                  _stream_ptr(codes)), "mxfp4_dequantize")
+    return out
+
+
+def _check_codes(codes: torch.Tensor, scales: torch.Tensor) -> None:
+    _rows(codes, "codes")
+    _rows(scales, "scales")
+    if codes.dtype != torch.uint8 or codes.shape != (scales.shape[0], 16 * scales.shape[1]):
+        raise ValueError("codes must be uint8 [R, 16 B] for scales [R, B]")
+    _same("codes and scales", codes, scales)
+    _contiguous("codes and scales", codes, scales)
+
+
+@dataclasses.dataclass(frozen=True)
+class Mxfp4Weight:
+    """An MXFP4 weight matrix [N, K] on the device: codes uint8 [N, K/2] and
+    scales uint8 [N, K/32] (K a multiple of 32).  For a gated product the
+    first half of the rows is the gate, the second the up projection."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    K: int
+
+    def __post_init__(self):
+        _check_codes(self.codes, self.scales)
+        if self.K != 32 * self.scales.shape[1]:
+            raise ValueError(f"K = {self.K} must be a multiple of 32 and match the scales")
+        object.__setattr__(self, "_c", dc.mxfp4_weight(self.codes.data_ptr(), self.scales.data_ptr(),
+                                                       self.codes.shape[0], self.K))
+
+    @property
+    def N(self) -> int:
+        return self.codes.shape[0]
+
+    @staticmethod
+    def quantize(w: torch.Tensor, stream=None) -> "Mxfp4Weight":
+        """From a weight matrix [N, K] in bf16, f16 or f32."""
+        codes, scales = mxfp4_quantize(w, stream)
+        return Mxfp4Weight(codes, scales, w.shape[1])
+
+    def dequantize(self, dtype=torch.float32, stream=None) -> torch.Tensor:
+        return mxfp4_dequantize(self.codes, self.scales, self.K, dtype, stream)
+
+
+def _linear(name, x, weight, activation, stream):
+    act = _act(activation)
+    ld = _rows(x, "x", weight.K)
+    if x.dtype not in _DTYPE:
+        raise ValueError("x must be bf16 (mxfp4_linear_a4: or f16)")
+    if x.device != weight.codes.device:
+        raise ValueError("x and the weight are on different devices")
+    T = x.shape[0]
+    c = _byref(weight._c)
+    with _on(stream, x, weight.codes, weight.scales):
+        y = torch.empty((T, weight.N // 2 if act else weight.N), dtype=x.dtype, device=x.device)
+        # 0 bytes: arguments that the call below refuses
+        ws = torch.empty(max(getattr(dc, name + "_workspace_bytes")(T, c, act), 256), dtype=torch.uint8,
+                         device=x.device)
+        check(getattr(dc, name)(x.data_ptr(), _DTYPE[x.dtype], ld, T, c, act, y.data_ptr(), ws.data_ptr(), ws.numel(),
+                                _stream_ptr(x)), name)
+    return y
+
+
+def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
+    """W4A16: y [T, N] = x weight^T for bf16 x [T, K]; with an activation the
+    gated form y [T, N/2] = act(x Wg^T) * (x Wu^T)."""
+    return _linear("mxfp4_linear", x, weight, activation, stream)
+
+
+def mxfp4_linear_a4(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
+    """W4A4: mxfp4_linear with x (bf16 or f16) quantised to MXFP4 on the way in."""
+    return _linear("mxfp4_linear_a4", x, weight, activation, stream)
+
+
+# ------------------------------------------------------------- feed-forward
+def _ffn_weights(gate, up, down, activation) -> dc.gated_ffn_weights:
+    act = _act(activation, gated=True)
+    if gate.dim() != 2 or gate.shape != up.shape or down.shape != gate.shape[::-1]:
+        raise ValueError("weights must be gate, up [I, H] and down [H, I]")
+    if not gate.is_cuda:
+        raise ValueError("weights must be on a CUDA device")
+    _same("gate, up and down", gate, up, down)
+    _contiguous("gate, up and down", gate, up, down)
+    if gate.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("weights must be bf16 or f16")
+    I, H = gate.shape
+    return dc.gated_ffn_weights(gate.data_ptr(), up.data_ptr(), down.data_ptr(), H, I, act, _DTYPE[gate.dtype])
+
+
+def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
+                      activation: str = "gelu_tanh", save: bool = False, stream=None):
+    """y [T, H] = (act(x gate^T) * (x up^T)) down^T, for bf16 or f16 x [T, H],
+    gate, up [I, H], down [H, I]; with save, (y, saved) where saved [3, T, I]
+    is what gated_ffn_backward takes."""
+    f = _ffn_weights(gate, up, down, activation)
+    ld = _rows(x, "x", f.H)
+    _same("x and the weights", x, gate)
+    T = x.shape[0]
+    with _on(stream, x, gate, up, down):
+        y = torch.empty((T, f.H), dtype=x.dtype, device=x.device)
+        if save:
+            saved = torch.empty((3, T, f.I), dtype=x.dtype, device=x.device)
+            check(dc.gated_ffn_forward(x.data_ptr(), ld, T, _byref(f), y.data_ptr(), saved.data_ptr() or None, None, 0,
+                                       _stream_ptr(x)) if T else 0, "gated_ffn_forward")
+            return y, saved
+        ws = torch.empty(max(dc.gated_ffn_forward_workspace_bytes(T, _byref(f)), 256), dtype=torch.uint8,
+                         device=x.device)
+        check(dc.gated_ffn_forward(x.data_ptr(), ld, T, _byref(f), y.data_ptr(), None, ws.data_ptr(), ws.numel(),
+                                   _stream_ptr(x)), "gated_ffn_forward")
+    return y
+
+
+def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
+                       saved: torch.Tensor, activation: str = "gelu_tanh", needs=(True, True, True, True),
+                       stream=None):
+    """(dx, dgate, dup, ddown) of gated_ffn_forward for dy [T, H], given its x
+    and saved; None where `needs` is false."""
+    f = _ffn_weights(gate, up, down, activation)
+    ld, lddy = _rows(x, "x", f.H), _rows(dy, "dy", f.H)
+    T = x.shape[0]
+    _same("dy, x, saved and the weights", dy, x, saved, gate)
+    if dy.shape[0] != T or saved.shape != (3, T, f.I):
+        raise ValueError("dy and saved must be those of x's forward pass")
+    _contiguous("saved", saved)
+    with _on(stream, dy, x, gate, up, down, saved):
+        outs = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need else None
+                for w, need in zip((x, gate, up, down), needs)]
+        ws = torch.empty(max(dc.gated_ffn_backward_workspace_bytes(T, _byref(f)), 256), dtype=torch.uint8,
+                         device=x.device)
+        check(dc.gated_ffn_backward(dy.data_ptr(), lddy, x.data_ptr(), ld, saved.data_ptr(), T, _byref(f),
+                                    *(None if o is None else o.data_ptr() for o in outs), ws.data_ptr(), ws.numel(),
+                                    _stream_ptr(x)), "gated_ffn_backward")
+    return tuple(outs)
+
+
+class _GatedFfn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, up, down, activation):
+        if not any(ctx.needs_input_grad[:4]):
+            return gated_ffn_forward(x, gate, up, down, activation)
+        y, saved = gated_ffn_forward(x, gate, up, down, activation, save=True)
+        ctx.save_for_backward(x, gate, up, down, saved)
+        ctx.activation = activation
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, gate, up, down, saved = ctx.saved_tensors
+        # an expanded gradient (of a sum) has no rows of its own
+        grads = gated_ffn_backward(dy.contiguous(), x, gate, up, down, saved, ctx.activation,
+                                   ctx.needs_input_grad[:4])
+        return (*grads, None)
+
+
+def gated_ffn(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
+              activation: str = "gelu_tanh") -> torch.Tensor:
+    """gated_ffn_forward as a differentiable torch operation, for x [..., H].
+    First derivatives only."""
+    y = _GatedFfn.apply(x.reshape(-1, x.shape[-1]).contiguous(), gate, up, down, activation)
+    return y.view(x.shape)

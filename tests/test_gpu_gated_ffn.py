@@ -1,0 +1,161 @@
+"""The gated feed-forward block on the GPU, forward and backward, against its
+64-bit form (bounds of dense_ref), and the path train -> quantise -> serve."""
+import pytest
+import torch
+
+import nvfp4_weight_only_router_b200 as lib
+from tests import dense_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F16 = torch.bfloat16, torch.float16
+
+
+def _make(seed, T, H, I, dtype, dev):
+    gen = torch.Generator(device=dev).manual_seed(seed)
+
+    def rn(*s, k=1.0):
+        return (torch.randn(s, generator=gen, device=dev) * k).to(dtype)
+    return rn(T, H), rn(I, H, k=H ** -0.5), rn(I, H, k=H ** -0.5), rn(H, I, k=I ** -0.5), rn(T, H)
+
+
+def _reference(x, gate, up, down, dy, act):
+    return R.ffn64(x.double(), gate.double(), up.double(), down.double(), None if dy is None else dy.double(), act,
+                   x.dtype)
+
+
+def _check_step(x, gate, up, down, dy, act):
+    y, saved = lib.gated_ffn_forward(x, gate, up, down, act, save=True)
+    grads = lib.gated_ffn_backward(dy, x, gate, up, down, saved, act)
+    ref = _reference(x, gate, up, down, dy, act)
+    assert lib.device_status() == 0
+    for name, got in zip(("y", "dx", "dgate", "dup", "ddown"), (y, *grads)):
+        R.assert_within(got, *ref[name], f"{name} {list(x.shape)} {list(gate.shape)} {act} {x.dtype}")
+    return y, saved, grads
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("T,H,I", [(1, 64, 64), (7, 8, 8), (9, 72, 136), (32, 256, 200), (33, 256, 200), (100, 520, 264),
+                                   (129, 128, 1000), (255, 640, 64), (300, 2816, 704)])
+def test_forward(dev, T, H, I, dtype):
+    x, gate, up, down, _ = _make(T, T, H, I, dtype, dev)
+    for act in ("gelu_tanh", "silu"):
+        y = lib.gated_ffn_forward(x, gate, up, down, act)
+        assert lib.device_status() == 0
+        R.assert_within(y, *_reference(x, gate, up, down, None, act)["y"], f"y {T} {H} {I} {act}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("T,H,I", [(1, 64, 64), (5, 8, 8), (31, 72, 136), (64, 256, 256), (65, 264, 200), (130, 520, 264),
+                                   (257, 128, 1000), (1000, 640, 64), (513, 1024, 768)])
+def test_step(dev, T, H, I, dtype):
+    for act in ("gelu_tanh", "silu"):
+        _check_step(*_make(T + I, T, H, I, dtype, dev), act)
+
+
+@pytest.mark.parametrize("T,H,I,act,dtype", [(1001, 2008, 1000, "silu", F16), (4096, 2816, 2112, "gelu_tanh", BF)])
+def test_step_large(dev, T, H, I, act, dtype):
+    _check_step(*_make(3, T, H, I, dtype, dev), act)
+
+
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_large_gates(dev, act):
+    """Gate values far outside the activation's curved range: finite gradients."""
+    x, gate, up, down, dy = _make(5, 40, 64, 64, BF, dev)
+    gate = gate * 64
+    _check_step(x, gate, up, down, dy, act)
+
+
+def test_partial_gradients_and_empty_batch(dev):
+    x, gate, up, down, dy = _make(6, 70, 136, 72, BF, dev)
+    y, saved, full = _check_step(x, gate, up, down, dy, "gelu_tanh")
+    for needs in ((True, False, False, False), (False, True, False, True), (False, False, False, True),
+                  (False, False, True, False), (False,) * 4):
+        part = lib.gated_ffn_backward(dy, x, gate, up, down, saved, needs=needs)
+        for p, f, n in zip(part, full, needs):
+            assert (p is None) if not n else torch.equal(p, f)
+    y0, s0 = lib.gated_ffn_forward(x[:0], gate, up, down, save=True)
+    g0 = lib.gated_ffn_backward(dy[:0], x[:0], gate, up, down, s0)
+    assert y0.shape == (0, 136) and g0[0].shape == (0, 136)
+    assert all((g == 0).all() for g in g0[1:])
+    assert lib.gated_ffn_forward(x[:0], gate, up, down).shape == (0, 136)
+
+
+@pytest.mark.parametrize("T", [4, 90])
+def test_strides_streams_and_graphs(dev, T):
+    x, gate, up, down, dy = _make(7, T, 136, 72, BF, dev)
+    wide = torch.zeros((T, 400), dtype=BF, device=dev)
+    wide[:, 8:144], wide[:, 200:336] = x, dy
+    xs, ds = wide[:, 8:144], wide[:, 200:336]
+    y, saved = lib.gated_ffn_forward(x, gate, up, down, save=True)
+    grads = lib.gated_ffn_backward(dy, x, gate, up, down, saved)
+    serve = lib.gated_ffn_forward(x, gate, up, down)
+
+    def same(a, b):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+    ys, ss = lib.gated_ffn_forward(xs, gate, up, down, save=True)
+    same((ys, *lib.gated_ffn_backward(ds, xs, gate, up, down, ss)), (y, *grads))
+    same((lib.gated_ffn_forward(xs, gate, up, down),), (serve,))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y2, s2 = lib.gated_ffn_forward(x, gate, up, down, save=True, stream=s)
+    g2 = lib.gated_ffn_backward(dy, x, gate, up, down, s2, stream=s)
+    s.synchronize()
+    same((y2, *g2), (y, *grads))
+    # two captured graphs and eager calls between their replays
+    static, outs, graphs = x.clone(), [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            yc, sc = lib.gated_ffn_forward(static, gate, up, down, save=True)
+            outs.append((yc, *lib.gated_ffn_backward(dy, static, gate, up, down, sc),
+                         lib.gated_ffn_forward(static, gate, up, down)))
+        graphs.append(g)
+    static.copy_(x.flip(0))
+    for g in graphs:
+        g.replay()
+    lib.gated_ffn_forward(x, gate, up, down)
+    yf, sf = lib.gated_ffn_forward(x.flip(0), gate, up, down, save=True)
+    ref = (yf, *lib.gated_ffn_backward(dy, x.flip(0), gate, up, down, sf), lib.gated_ffn_forward(x.flip(0), gate, up, down))
+    torch.cuda.synchronize()
+    for o in outs:
+        same(o, ref)
+
+
+def test_autograd(dev):
+    x, gate, up, down, _ = _make(8, 60, 136, 72, BF, dev)
+    leaves = [t.clone().requires_grad_() for t in (x.view(3, 20, 136), gate, up, down)]
+    y = lib.gated_ffn(*leaves, "silu")
+    assert y.shape == (3, 20, 136)
+    y.sum().backward()                       # an expanded gradient
+    yf, saved = lib.gated_ffn_forward(x, gate, up, down, "silu", save=True)
+    ref = lib.gated_ffn_backward(torch.ones_like(x), x, gate, up, down, saved, "silu")
+    assert torch.equal(y.view(60, 136), yf)
+    for leaf, g in zip(leaves, ref):
+        assert torch.equal(leaf.grad.view(g.shape), g)
+    # frozen weights: the input's gradient alone
+    xi = x.clone().requires_grad_()
+    lib.gated_ffn(xi, gate, up, down, "silu").sum().backward()
+    assert torch.equal(xi.grad, ref[0])
+    with torch.no_grad():
+        assert not lib.gated_ffn(xi, gate, up, down, "silu").requires_grad
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_train_quantise_serve(dev, T):
+    """A step of training in bf16, the stepped weights quantised to MXFP4, and
+    the block served from them in both forms."""
+    x, gate, up, down, dy = _make(9, T, 256, 192, BF, dev)
+    leaves = [t.clone().requires_grad_() for t in (gate, up, down)]
+    lib.gated_ffn(x, *leaves).backward(dy)
+    gate, up, down = ((t - 0.05 * t.grad).detach() for t in leaves)
+    gu, dn = lib.Mxfp4Weight.quantize(torch.cat((gate, up))), lib.Mxfp4Weight.quantize(down)
+    for a4, f in ((False, lib.mxfp4_linear), (True, lib.mxfp4_linear_a4)):
+        h = f(x, gu, "gelu_tanh")
+        y = f(h, dn)
+        q = R.mx_round if a4 else torch.Tensor.double
+        href, hb = R.linear64(q(x), gu.dequantize().double(), "gelu_tanh", BF)
+        R.assert_within(h, href, hb, "h")
+        yref, yb = R.linear64(q(h), dn.dequantize().double(), None, BF)   # from the served h
+        R.assert_within(y, yref, yb, "y")
+    assert lib.device_status() == 0
