@@ -82,7 +82,8 @@ typedef struct {
  * dtype: BF16.  T <= 2^20.
  * mxfp4_linear_a4 (W4A4): x (bf16 or f16, y alike) is first quantised as by
  * mxfp4_quantize; the E2M1 products are exact and summed in fp32.
- * The workspace queries return 0 for arguments the call would refuse.
+ * The workspace queries return 0 for arguments the call would refuse; at 256
+ * bytes the call uses no workspace and takes NULL.
  * ------------------------------------------------------------------------- */
 NVFP4DENSE_API size_t mxfp4_linear_workspace_bytes(int32_t T, const mxfp4_weight* w, int32_t act);
 NVFP4DENSE_API nvfp4_status mxfp4_linear(const void* x_dev, int32_t dtype, int64_t ldx, int32_t T,
@@ -107,11 +108,13 @@ typedef struct {
 /* ---------------------------------------------------------------------------
  * gated_ffn_forward: g = x gate^T, u = x up^T, h = act(g) u, y = h down^T.
  *   x [T, H] (row stride ldx), y [T, H]
- *   saved [3, T, I] (g, u, h) for gated_ffn_backward, or NULL
- * fp32 accumulation; g, u (fp32 in the gate) and h are rounded to the 16-bit
- * type where they are stored.  T <= 2^20.  With `saved` the workspace is not
- * used.
+ *   saved gated_ffn_saved_bytes bytes, 256-byte aligned, for
+ *         gated_ffn_backward (h in 16 bits, act(g) and u act'(g) in 24: 8 bytes
+ *         per token and hidden unit), or NULL
+ * fp32 accumulation; h is rounded to the 16-bit type.  T <= 2^20.  With `saved`
+ * the workspace is not used.
  * ------------------------------------------------------------------------- */
+NVFP4DENSE_API size_t gated_ffn_saved_bytes(int32_t T, const gated_ffn_weights* f);
 NVFP4DENSE_API size_t gated_ffn_forward_workspace_bytes(int32_t T, const gated_ffn_weights* f);
 NVFP4DENSE_API nvfp4_status gated_ffn_forward(const void* x_dev, int64_t ldx, int32_t T, const gated_ffn_weights* f,
                                               void* y_dev, void* saved_dev, void* ws_dev, size_t ws_bytes,

@@ -90,16 +90,15 @@ LinearLayout a4_layout(int32_t T, const mxfp4_weight* w, int32_t act) {
   return L;
 }
 
-nvfp4_status linear_checks(const void* x, int32_t dtype, int64_t ldx, int32_t T, const mxfp4_weight* w, int32_t act,
+nvfp4_status linear_checks(const void* x, int32_t dtype, int64_t ldx, int32_t T, const mxfp4_weight* w,
                            const void* y, const void* ws, size_t ws_bytes, size_t need, bool a4) {
   if (T > 0 && (!x || !y)) return NVFP4_ERR_INVALID_ARG;
   if (dtype < kBf16 || dtype > kF32) return NVFP4_ERR_INVALID_ARG;
   if (dtype == kF32 || (!a4 && dtype != kBf16)) return NVFP4_ERR_UNSUPPORTED;
   if (!row_stride_ok(ldx, w->K, T)) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(y, 16) || (T > 1 && ldx % 8 != 0)) return NVFP4_ERR_ALIGNMENT;
-  if (!ws || ws_bytes < need) return NVFP4_ERR_WORKSPACE;
+  if (need > 256 && (!ws || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return NVFP4_ERR_ALIGNMENT;
-  (void)act;
   return NVFP4_OK;
 }
 
@@ -158,7 +157,7 @@ nvfp4_status nvfp4dense_get_device_status(void* stream) {
 // ---------------------------------------------------------------- quantise
 static nvfp4_status check_mx_dims(int64_t rows, int64_t K) {
   if (rows < 0 || K < 1) return NVFP4_ERR_INVALID_ARG;
-  if (rows > 0x7FFFFFFF || K >= (int64_t(1) << 24) || rows * mx_blocks(K) >= (int64_t(1) << 35))
+  if (rows > 0x7FFFFFFF || K >= (int64_t(1) << 24) || rows * K >= (int64_t(1) << 40))
     return NVFP4_ERR_UNSUPPORTED;
   return NVFP4_OK;
 }
@@ -199,7 +198,7 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
   NvtxRange nv("mxfp4_linear");
   nvfp4_status st = check_linear(T, w, act);
   if (st != NVFP4_OK) return st;
-  st = linear_checks(x, dtype, ldx, T, w, act, y, ws, ws_bytes, linear_bytes(T, w), false);
+  st = linear_checks(x, dtype, ldx, T, w, y, ws, ws_bytes, linear_bytes(T, w), false);
   if (st != NVFP4_OK || T == 0) return st;
   if (T == 1) ldx = w->K;
   cudaStream_t s = as_stream(stream);
@@ -240,7 +239,7 @@ nvfp4_status mxfp4_linear_a4(const void* x, int32_t dtype, int64_t ldx, int32_t 
   nvfp4_status st = check_linear(T, w, act);
   if (st != NVFP4_OK) return st;
   const LinearLayout L = a4_layout(T, w, act);
-  st = linear_checks(x, dtype, ldx, T, w, act, y, ws, ws_bytes, L.total, true);
+  st = linear_checks(x, dtype, ldx, T, w, y, ws, ws_bytes, L.total, true);
   if (st != NVFP4_OK || T == 0) return st;
   if (T == 1) ldx = w->K;
   cudaStream_t s = as_stream(stream);
@@ -277,6 +276,11 @@ nvfp4_status mxfp4_linear_a4(const void* x, int32_t dtype, int64_t ldx, int32_t 
 }
 
 // -------------------------------------------------------------- feed-forward
+size_t gated_ffn_saved_bytes(int32_t T, const gated_ffn_weights* f) {
+  if (check_ffn(T, f) != NVFP4_OK) return 0;
+  return T == 0 ? 256 : pair_kept(nullptr, T, f->I).bytes;
+}
+
 size_t gated_ffn_forward_workspace_bytes(int32_t T, const gated_ffn_weights* f) {
   return check_ffn(T, f) == NVFP4_OK ? round_up((size_t)T * f->I * 2 + 1, 256) : 0;
 }
@@ -287,7 +291,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   nvfp4_status st = check_ffn(T, f);
   if (st != NVFP4_OK) return st;
   if ((T > 0 && (!x || !y)) || !row_stride_ok(ldx, f->H, T)) return NVFP4_ERR_INVALID_ARG;
-  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(saved, 16) || (T > 1 && ldx % 8 != 0)) return NVFP4_ERR_ALIGNMENT;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(saved, 256) || (T > 1 && ldx % 8 != 0)) return NVFP4_ERR_ALIGNMENT;
   if (!saved) {
     if (!ws || ws_bytes < gated_ffn_forward_workspace_bytes(T, f)) return NVFP4_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return NVFP4_ERR_ALIGNMENT;
@@ -295,7 +299,6 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   if (T == 0) return NVFP4_OK;
   if (T == 1) ldx = f->H;
   cudaStream_t s = as_stream(stream);
-  const size_t plane = (size_t)T * f->I;
   if (!saved && T <= kSkinnyMaxTokens) {
     SkinnyArgs a{};
     a.x = x;
@@ -321,7 +324,6 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
     a.after_producer = true;
     return cuda_status(launch_skinny(a, s));
   }
-  uint16_t* sv = static_cast<uint16_t*>(saved);
   PairGated a{};
   a.x = x;
   a.ldx = ldx;
@@ -333,9 +335,9 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   a.K = f->H;
   a.act = f->act;
   a.dtype = f->dtype;
-  a.g = sv;
-  a.u = sv ? sv + plane : nullptr;
-  a.h = sv ? sv + 2 * plane : ws;
+  a.keep = saved != nullptr;
+  a.kept = pair_kept(saved, T, f->I);
+  a.h = saved ? saved : ws;
   int* status = device_status_ptr();
   cudaError_t e = launch_pair_gated(a, status, s);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -360,9 +362,10 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
   if (st != NVFP4_OK) return st;
   if (T > 0 && (!dy || !x || !saved)) return NVFP4_ERR_INVALID_ARG;
   if (!row_stride_ok(lddy, f->H, T) || !row_stride_ok(ldx, f->H, T)) return NVFP4_ERR_INVALID_ARG;
-  const void* ps[] = {dy, x, saved, dx, dgate, dup, ddown};
+  const void* ps[] = {dy, x, dx, dgate, dup, ddown};
   for (const void* p : ps)
     if (!aligned(p, 16)) return NVFP4_ERR_ALIGNMENT;
+  if (!aligned(saved, 256)) return NVFP4_ERR_ALIGNMENT;
   if (T > 1 && (ldx % 8 != 0 || lddy % 8 != 0)) return NVFP4_ERR_ALIGNMENT;
   if (!ws || ws_bytes < gated_ffn_backward_workspace_bytes(T, f)) return NVFP4_ERR_WORKSPACE;
   if (!aligned(ws, 256)) return NVFP4_ERR_ALIGNMENT;
@@ -378,7 +381,7 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
   }
   if (T == 1) ldx = lddy = H;
   const size_t plane = (size_t)T * I;
-  const uint16_t* g = static_cast<const uint16_t*>(saved);
+  const PairKept kept = pair_kept(const_cast<void*>(saved), T, I);
   uint16_t* dg = static_cast<uint16_t*>(ws);
   uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + round_up(plane * 2, 256));
   int* status = device_status_ptr();
@@ -390,10 +393,8 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
     a.T = T;
     a.H = H;
     a.I = I;
-    a.act = f->act;
     a.dtype = f->dtype;
-    a.g = g;
-    a.u = g + plane;
+    a.kept = kept;
     a.dg = dg;
     a.du = du;
     const cudaError_t e = launch_pair_gated_bwd(a, status, s);
@@ -420,7 +421,7 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
   };
   if (dgate) weight_grad(dg, I, x, ldx, I, H, dgate);
   if (dup) weight_grad(du, I, x, ldx, I, H, dup);
-  if (ddown) weight_grad(dy, lddy, g + 2 * plane, I, H, I, ddown);
+  if (ddown) weight_grad(dy, lddy, kept.h, I, H, I, ddown);
   if (n == 0) return NVFP4_OK;
   return cuda_status(launch_pair_gemm(q, n, f->dtype, status, s));
 }

@@ -87,24 +87,37 @@ struct PairGemm {
 constexpr int kPairMaxProblems = 4;
 // plain products, one launch for all (at most kPairMaxProblems); out = sum over segments A B^T
 cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st);
-// h = act(x gate^T) * (x up^T); g, u (16-bit, may be null) kept for the backward pass
+// What the forward pass keeps for the backward one: h, and p = u act'(g) and
+// a = act(g) in 24 bits (a 16-bit and an 8-bit plane each), [T, I] all
+struct PairKept {
+  uint8_t *h, *p_hi, *a_hi, *p_lo, *a_lo;
+  size_t bytes;
+};
+inline PairKept pair_kept(void* base, int64_t T, int64_t I) {
+  const size_t p2 = ((size_t)(T * I) * 2 + 255) / 256 * 256, p1 = ((size_t)(T * I) + 255) / 256 * 256;
+  uint8_t* b = static_cast<uint8_t*>(base);
+  return PairKept{b, b + p2, b + 2 * p2, b + 3 * p2, b + 3 * p2 + p1, 3 * p2 + 2 * p1};
+}
+// h = act(x gate^T) * (x up^T)
 struct PairGated {
   const void *x, *gate, *up;
   int64_t ldx;
   int64_t ldw;
   int T, I, K;
   int act, dtype;
-  void *h, *g, *u;
+  void* h;
+  bool keep;       // kept.h == h
+  PairKept kept;
 };
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st);
-// dh = dy down with dg = dh u act'(g), du = dh act(g) written in its place
+// dh = dy down with dg = dh p, du = dh a written in its place
 struct PairGatedBwd {
   const void* dy;         // [T, H]
   int64_t lddy;
   const void* down;       // [H, I]
   int T, H, I;
-  int act, dtype;
-  const void *g, *u;
+  int dtype;
+  PairKept kept;
   void *dg, *du;
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);

@@ -100,24 +100,56 @@ __device__ __forceinline__ void unpack16x2(uint32_t v, bool f16, float& lo, floa
 }
 
 // ---------------------------------------------------------------- activations
-// gelu_tanh (common.cuh) and silu, with their derivatives, in fp32.  With
-// s = 1 / (1 + exp(-z)), silu: z = g, gelu_tanh: z = 2 sqrt(2/pi) (g + 0.044715 g^3):
-// act = g s, act' = s + g s (1 - s) dz/dg.
+// gelu_tanh and silu with their derivatives, in fp32.  With s = 1 / (1 + exp(-z)),
+// silu: z = g, gelu_tanh: z = 2 sqrt(2/pi) (g + 0.044715 g^3) (0.5 (1 + tanh(z / 2)) = s):
+// act = g s, act' = s + g s (1 - s) dz/dg.  The fast exponential and division
+// (2^-21 relative together) run once per hidden unit in epilogues that must not
+// outlast the products; exp overflow gives the limit s = 0.
+constexpr float kGeluK0 = 1.5957691216057308f, kGeluK1 = 0.044715f;  // 2 sqrt(2 / pi)
 __device__ __forceinline__ float act_fwd(float g, int act) {
-  return act == kActSilu ? g / (1.0f + __expf(-g)) : gelu_tanh(g);
+  const float z = act == kActSilu ? g : kGeluK0 * (g + kGeluK1 * g * g * g);
+  return __fdividef(g, 1.0f + __expf(-z));
 }
 __device__ __forceinline__ void act_fwd_grad(float g, int act, float& a, float& da) {
-  a = act_fwd(g, act);
-  // s (1 - s) is 0 in fp32 beyond |z| ~ 104, reached before |g| = 128 by both;
-  // the clamp keeps g^2 finite there and lets a NaN through
+  // s (1 - s) is 0 in fp32 well before |g| = 128 for both; the clamp keeps
+  // dz finite beyond and lets a NaN through
   const float c = fabsf(g) > 128.0f ? copysignf(128.0f, g) : g;
-  const float k0 = 1.5957691216057308f, k1 = 0.044715f;  // 2 sqrt(2 / pi)
-  const float z = act == kActSilu ? c : k0 * (c + k1 * c * c * c);
-  const float dz = act == kActSilu ? 1.0f : k0 * (1.0f + 3.0f * k1 * c * c);
-  const float s = 1.0f / (1.0f + __expf(-z));
-  // 1 - s as s(-z) keeps its relative accuracy for large z
-  const float r = 1.0f / (1.0f + __expf(z));
-  da = s + c * s * r * dz;
+  const float z = act == kActSilu ? c : kGeluK0 * (c + kGeluK1 * c * c * c);
+  const float dz = act == kActSilu ? 1.0f : kGeluK0 * (1.0f + 3.0f * kGeluK1 * c * c);
+  const float s = __fdividef(1.0f, 1.0f + __expf(-z));
+  a = g * s;
+  da = s + c * s * (1.0f - s) * dz;
+}
+
+// ------------------------------------------------ 24-bit kept values, wide access
+// What the forward pass keeps for the backward one (act(g) and u act'(g)) is
+// stored as the top 24 bits of its fp32: 16 bits in one plane and 8 in
+// another.  Rounded to 16 bits they would add an error as large as the
+// gradients' own rounding; 24 bits (2^-15) add none that shows, and 8 bytes
+// per hidden unit with h in 16 bits is what four 16-bit tensors would take.
+__device__ __forceinline__ uint32_t keep_hi2(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ uint32_t keep_lo4(float a, float b, float c, float d) {
+  return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0051),
+                     __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0051), 0x5410);
+}
+// value i (0..3) of two hi words (values 0, 1 and 2, 3) and one lo word
+__device__ __forceinline__ float kept(uint32_t hi01, uint32_t hi23, uint32_t lo, int i) {
+  const uint32_t hi = (i & 2) ? hi23 : hi01;
+  const uint32_t h = (i & 1) ? (hi & 0xFFFF0000u) : (hi << 16);
+  return __uint_as_float(h | (__byte_perm(lo, 0u, 0x4440 + i) << 8));
+}
+
+__device__ __forceinline__ void ld_nc_v8(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 }  // namespace nvfp4moe

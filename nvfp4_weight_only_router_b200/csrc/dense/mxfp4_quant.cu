@@ -6,11 +6,13 @@
 //   value = E2M1 2^X.  A block with a NaN or an infinity gets scale 255 (NaN)
 //   and codes 0; a ragged last block is filled up with zeros.
 //
-// Bound by memory: K (2 + 1/2 + 1/32) bytes per bf16 row.  A thread holds 8
-// consecutive elements (one or two 16-byte loads, one 4-byte store of codes),
-// four neighbouring lanes form a block and share its maximum through two
-// shuffles, so loads and stores of a warp are contiguous.  Four groups per
-// thread keep four loads in flight.
+// Bound by memory: K (2 + 1/2 + 1/32) bytes per bf16 row.  A thread holds one
+// block: 64 bytes of a 16-bit row by two 32-byte loads, its maximum by packed
+// integer comparisons, its codes by one 16-byte store, so that a block costs
+// no shuffles and neighbouring threads write neighbouring codes and scales.
+// Rows off the 16-byte grid (and ragged last blocks) read the aligned 16-byte
+// pieces that hold the block and shift them into place in registers; only
+// pieces that hold an element of the block are read.
 #include <type_traits>
 
 #include "mxfp4_codec.cuh"
@@ -20,123 +22,157 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kQT = 256;  // threads
-constexpr int kQU = 4;    // groups of 8 elements per thread
-constexpr int kQGroups = kQT * kQU;
-
-// The bits of 8 elements; loaded first for all of a thread's groups.
-template <typename T>
-struct Raw {
-  uint4 v[sizeof(T) == 4 ? 2 : 1];
-};
-
-template <typename T>
-__device__ __forceinline__ void raw_to_f32(const Raw<T>& r, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
-  } else {
-    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) unpack16x2(w[k], std::is_same<T, __half>::value, v[2 * k], v[2 * k + 1]);
-  }
-}
-
-// One group of 8 elements from column c of a row (the row's first element at
-// x): vector loads where the group lies inside the row and vec holds.
-template <typename T>
-__device__ __forceinline__ Raw<T> load_group(const void* x, int64_t row0, int64_t c, int64_t K, bool vec) {
-  Raw<T> r;
-  if (vec && c + 8 <= K) {
-    const char* p = static_cast<const char*>(x) + (row0 + c) * (int64_t)sizeof(T);
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.v[i] = ldg_nc_v4(p + 16 * i);
-  } else {
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      w[k] = 0u;
-      if (c + k < K) {
-        if constexpr (sizeof(T) == 4) w[k] = static_cast<const uint32_t*>(x)[row0 + c + k];
-        else w[k] = static_cast<const uint16_t*>(x)[row0 + c + k];
-      }
-    }
-    if constexpr (sizeof(T) == 4) {
-      r.v[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      r.v[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-      r.v[0] = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
-    }
-  }
-  return r;
-}
 
 struct QuantArgs {
   const void* x;
   int64_t rows, K, ldx;
   uint8_t* codes;
   uint8_t* scales;
-  int64_t nb;        // blocks per row
-  int64_t groups;    // groups of 8 walked per row: 4 nb, or up to whole chunks
-  int sf_chunks;     // MMA order: 512-byte chunks per row block
-  bool vec;
+  int64_t nb;      // blocks per row
+  int64_t walked;  // blocks walked per row: nb, or up to whole chunks
+  int sf_chunks;   // MMA order: 512-byte chunks per row block
+  int align;       // bytes that divide every row's address: 32, 16, or less (0)
 };
 
-// Codes of one group and its block's scale byte (valid in every lane of the quad).
+// The bits of one block.
 template <typename T>
-__device__ __forceinline__ uint32_t encode_group(const Raw<T>& raw, uint32_t& byte) {
-  float v[8];
-  raw_to_f32<T>(raw, v);
-  uint32_t a = 0;
+struct Blk {
+  static constexpr int W = 32 * sizeof(T) / 4;
+  uint32_t w[W];
+};
+
+// Valid elements c..min(c + 32, K) of a row whose first element is row0
+// elements past x, zeros behind them.
+template <typename T>
+__device__ __forceinline__ Blk<T> load_block_any(const void* x, int64_t row0, int64_t c, int64_t K) {
+  constexpr int W = Blk<T>::W;
+  Blk<T> r;
+  const int valid = (int)(K - c < 32 ? (K - c > 0 ? K - c : 0) : 32);
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x) + (uintptr_t)(row0 + c) * sizeof(T);
+  const int o = (int)(a & 15);                           // bytes before the block in its first piece
+  const int bytes = valid * (int)sizeof(T);
+  const uint4* src = reinterpret_cast<const uint4*>(a - o);
+  uint32_t v[W + 4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) a = max(a, abs_bits(v[k]));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  byte = mx_scale_byte(a);
-  return mx_encode8(v, byte);
+  for (int i = 0; i < W / 4 + 1; ++i) {
+    const uint4 q = 16 * i < o + bytes && valid > 0 ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+    v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+  }
+  if (o & 8) {
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) v[i] = v[i + 2];
+  }
+  if (o & 4) {
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) v[i] = v[i + 1];
+  }
+  const bool odd = o & 2;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    uint32_t w = v[i];
+    if (sizeof(T) == 2 && odd) w = __byte_perm(v[i], v[i + 1], 0x5432);
+    const int left = bytes - 4 * i;                      // valid bytes of this word
+    r.w[i] = left >= 4 ? w : (left > 0 ? w & 0xFFFFu : 0u);
+  }
+  return r;
 }
 
-// Walks the groups [blk * kQGroups, + kQGroups) of the flattened (row, group)
-// order; all lanes of a quad are in the same block of the same row.
-template <typename T, bool MMA>
-__device__ __forceinline__ void quant_block(const QuantArgs& p, int64_t blk) {
-  const int64_t first = blk * kQGroups;
-  const int64_t r0 = first / p.groups;
-  const uint32_t g0 = (uint32_t)(first - r0 * p.groups), gpr = (uint32_t)p.groups;
-  Raw<T> raw[kQU];
-  int64_t row[kQU];
-  uint32_t grp[kQU];
+template <typename T, int ALIGN>
+__device__ __forceinline__ Blk<T> load_block(const void* x, int64_t row0, int64_t c, int64_t K) {
+  constexpr int W = Blk<T>::W;
+  if (ALIGN < 16 || c + 32 > K) return load_block_any<T>(x, row0, c, K);
+  Blk<T> r;
+  const char* p = static_cast<const char*>(x) + (row0 + c) * (int64_t)sizeof(T);
+  if (ALIGN == 32) {
 #pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint32_t g = g0 + u * kQT + threadIdx.x, dr = g / gpr;
+    for (int i = 0; i < W / 8; ++i) {
+      uint32_t q[8];
+      ld_nc_v8(p + 32 * i, q);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r.w[8 * i + k] = q[k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const uint4 q = ldg_nc_v4(p + 16 * i);
+      r.w[4 * i] = q.x; r.w[4 * i + 1] = q.y; r.w[4 * i + 2] = q.z; r.w[4 * i + 3] = q.w;
+    }
+  }
+  return r;
+}
+
+// The block's scale byte and its 32 codes.
+template <typename T>
+__device__ __forceinline__ uint4 encode_block(const Blk<T>& r, uint32_t& byte) {
+  constexpr bool F16 = std::is_same<T, __half>::value;
+  uint32_t a = 0;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a = max(a, r.w[i] & 0x7FFFFFFFu);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a = __vmaxu2(a, r.w[i] & 0x7FFF7FFFu);
+    float lo, hi;
+    unpack16x2(a, F16, lo, hi);
+    a = max(abs_bits(lo), abs_bits(hi));
+  }
+  byte = mx_scale_byte(a);
+  uint32_t c[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r.w[8 * q + k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) unpack16x2(r.w[4 * q + k], F16, v[2 * k], v[2 * k + 1]);
+    }
+    c[q] = mx_encode8(v, byte);
+  }
+  return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// One block of the flattened (row, block) order per thread and step, U steps
+// of kQT blocks per CTA with their loads issued together.
+template <typename T, int ALIGN, bool MMA>
+__device__ __forceinline__ void quant_cta(const QuantArgs& p, int64_t cta) {
+  constexpr int U = 2;
+  const int64_t first = cta * (kQT * U);
+  const int64_t r0 = first / p.walked;
+  const uint32_t b0 = (uint32_t)(first - r0 * p.walked), per = (uint32_t)p.walked;
+  Blk<T> blk[U];
+  int64_t row[U];
+  uint32_t b[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = b0 + u * kQT + threadIdx.x, dr = i / per;
     row[u] = r0 + dr;
-    grp[u] = g - dr * gpr;
-    if (row[u] < p.rows) raw[u] = load_group<T>(p.x, row[u] * p.ldx, (int64_t)grp[u] * 8, p.K, p.vec);
-    else raw[u] = Raw<T>{};
+    b[u] = i - dr * per;
+    // past the last row: nothing is read
+    blk[u] = load_block<T, ALIGN>(p.x, row[u] * p.ldx, (int64_t)b[u] * 32, row[u] < p.rows ? p.K : 0);
   }
 #pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    uint32_t byte;
-    const uint32_t c = encode_group<T>(raw[u], byte);
+  for (int u = 0; u < U; ++u) {
     if (row[u] >= p.rows) continue;
-    const int64_t b = grp[u] >> 2;
-    if (!MMA || b < p.nb) reinterpret_cast<uint32_t*>(p.codes)[row[u] * (4 * p.nb) + grp[u]] = c;
-    if ((threadIdx.x & 3) == 0) {
-      if (MMA) {
-        // blocks past K: scale 2^-127 on zero codes
-        const int64_t chunk = (row[u] >> 7) * p.sf_chunks + (b >> 2);
-        const int r = (int)(row[u] & 127);
-        p.scales[chunk * kSfChunkB + 16 * (r & 31) + 4 * (r >> 5) + (b & 3)] = (uint8_t)byte;
-      } else {
-        p.scales[row[u] * p.nb + b] = (uint8_t)byte;
-      }
+    uint32_t byte;
+    const uint4 c = encode_block<T>(blk[u], byte);
+    if (!MMA || b[u] < p.nb) reinterpret_cast<uint4*>(p.codes)[row[u] * p.nb + b[u]] = c;
+    if (MMA) {
+      // blocks past K: scale 2^-127 on zero codes
+      const int64_t chunk = (row[u] >> 7) * p.sf_chunks + (b[u] >> 2);
+      const int r = (int)(row[u] & 127);
+      p.scales[chunk * kSfChunkB + 16 * (r & 31) + 4 * (r >> 5) + (b[u] & 3)] = (uint8_t)byte;
+    } else {
+      p.scales[row[u] * p.nb + b[u]] = (uint8_t)byte;
     }
   }
 }
+constexpr int kQBlocks = 2 * kQT;  // blocks per CTA
 
-template <typename T>
+template <typename T, int ALIGN>
 __global__ void __launch_bounds__(kQT) mxfp4_quantize_kernel(QuantArgs p) {
-  quant_block<T, false>(p, blockIdx.x);
+  quant_cta<T, ALIGN, false>(p, blockIdx.x);
 }
 
 struct TileScales {
@@ -150,10 +186,10 @@ struct TileScales {
 // Blocks below qblocks quantise activations into the tensor core's operand
 // form; the others lay the weight's scales out (one 4-byte word a thread: the
 // scales of 4 blocks of one row).
-template <typename T>
+template <typename T, int ALIGN>
 __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qblocks, TileScales t) {
   if ((int64_t)blockIdx.x < qblocks) {
-    quant_block<T, true>(p, blockIdx.x);
+    quant_cta<T, ALIGN, true>(p, blockIdx.x);
     return;
   }
   const int64_t w = ((int64_t)blockIdx.x - qblocks) * kQT + threadIdx.x;
@@ -176,33 +212,35 @@ __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qb
   reinterpret_cast<uint32_t*>(t.wsf)[w] = v;
 }
 
-// 8 codes per thread; a row's values are K apart in `out`.
+// Values of 8 codes per thread, four such groups with their loads issued
+// together: one 32-byte (f32) or 16-byte (bf16) store a group, contiguous over
+// a warp.  Rows of whole groups only (K % 8 == 0).
+constexpr int kDU = 4, kDGroups = kQT * kDU;
+
 template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t rows,
-                                                               int64_t K, T* __restrict__ out, bool vec) {
-  const int64_t nb = (K + 31) / 32;
-  const int64_t first = (int64_t)blockIdx.x * kQGroups;
-  const uint32_t gpr = (uint32_t)(4 * nb);
+                                                               int64_t K, T* __restrict__ out) {
+  const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * kDGroups;
+  const uint32_t gpr = (uint32_t)(K / 8);
   const int64_t r0 = first / gpr;
   const uint32_t g0 = (uint32_t)(first - r0 * gpr);
-  uint32_t w[kQU], sc[kQU];
+  uint32_t w[kDU], sc[kDU];
 #pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint32_t g = g0 + u * kQT + threadIdx.x, dr = g / gpr;
+  for (int u = 0; u < kDU; ++u) {
+    const uint32_t i = g0 + u * kQT + threadIdx.x, dr = i / gpr, g = i - dr * gpr;
     const int64_t row = r0 + dr;
     w[u] = sc[u] = 0;
     if (row < rows) {
-      w[u] = __ldcs(reinterpret_cast<const uint32_t*>(codes) + row * gpr + (g - dr * gpr));
-      sc[u] = __ldg(scales + row * nb + ((g - dr * gpr) >> 2));
+      w[u] = __ldg(reinterpret_cast<const uint32_t*>(codes) + row * (4 * nb) + g);
+      sc[u] = __ldg(scales + row * nb + (g >> 2));
     }
   }
 #pragma unroll
-  for (int u = 0; u < kQU; ++u) {
-    const uint32_t g = g0 + u * kQT + threadIdx.x, dr = g / gpr;
-    const int64_t row = r0 + dr, c = (int64_t)(g - dr * gpr) * 8;
-    if (row >= rows || c >= K) continue;
-    uint32_t h[4];
+  for (int u = 0; u < kDU; ++u) {
+    const int64_t at = (first + u * kQT + threadIdx.x) * 8;  // rows are whole groups: out is flat
+    if (at >= rows * K) continue;
+    uint32_t h[4], o[8];
     e2m1x8_to_f16x2(w[u], h);
     const float s = mx_scale(sc[u]);
     float v[8];
@@ -212,30 +250,56 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __
       v[2 * k] *= s;
       v[2 * k + 1] *= s;
     }
-    T* dst = out + row * K + c;
-    if (vec && c + 8 <= K) {
-      if constexpr (sizeof(T) == 4) {
-        __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0], v[1], v[2], v[3]));
-        __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
-      } else {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(pack16x2(v[0], v[1], false), pack16x2(v[2], v[3], false),
-                                                    pack16x2(v[4], v[5], false), pack16x2(v[6], v[7], false));
-      }
-    } else {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < K) {
-          if constexpr (sizeof(T) == 4) dst[k] = v[k];
-          else dst[k] = __float2bfloat16_rn(v[k]);
-        }
+      for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(v[k]);
+      st_v8(out + at, o);
+    } else {
+      *reinterpret_cast<uint4*>(out + at) = make_uint4(pack16x2(v[0], v[1], false), pack16x2(v[2], v[3], false),
+                                                       pack16x2(v[4], v[5], false), pack16x2(v[6], v[7], false));
     }
   }
 }
 
-int64_t blocks_for(int64_t groups) { return (groups + kQGroups - 1) / kQGroups; }
+// Any K: one value per thread and step, consecutive over a warp.
+template <typename T>
+__global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t* __restrict__ codes,
+                                                                   const uint8_t* __restrict__ scales, int64_t rows,
+                                                                   int64_t K, T* __restrict__ out) {
+  constexpr int U = 8;
+  const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * (kQT * U);
+  const int64_t r0 = first / K;
+  const uint32_t c0 = (uint32_t)(first - r0 * K), k = (uint32_t)K;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = c0 + u * kQT + threadIdx.x, dr = i / k, c = i - dr * k;
+    const int64_t row = r0 + dr;
+    if (row >= rows) continue;
+    const uint32_t code = ((uint32_t)__ldg(codes + row * (16 * nb) + (c >> 1)) >> (4 * (c & 1))) & 15u;
+    uint32_t h[4];
+    e2m1x8_to_f16x2(code, h);
+    float lo, hi;
+    unpack16x2(h[0], true, lo, hi);
+    const float v = lo * mx_scale(__ldg(scales + row * nb + (c >> 5)));
+    if constexpr (sizeof(T) == 4) out[row * K + c] = v;
+    else out[row * K + c] = __float2bfloat16_rn(v);
+  }
+}
 
-bool vector_rows(const void* p, int64_t ld, int elsize) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * elsize) % 16 == 0;
+unsigned blocks_for(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+
+int row_align(const void* p, int64_t ld, int elsize) {
+  for (int a = 32; a >= 16; a /= 2)
+    if (reinterpret_cast<uintptr_t>(p) % a == 0 && (ld * elsize) % a == 0) return a;
+  return 0;
+}
+
+template <typename T>
+void quantize_t(const QuantArgs& p, cudaStream_t st) {
+  const unsigned grid = blocks_for(p.rows * p.walked, kQBlocks);
+  if (p.align == 32) mxfp4_quantize_kernel<T, 32><<<grid, kQT, 0, st>>>(p);
+  else if (p.align == 16) mxfp4_quantize_kernel<T, 16><<<grid, kQT, 0, st>>>(p);
+  else mxfp4_quantize_kernel<T, 0><<<grid, kQT, 0, st>>>(p);
 }
 
 }  // namespace
@@ -249,25 +313,27 @@ cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_
   p.ldx = ldx;
   p.codes = codes;
   p.scales = scales;
-  p.nb = mx_blocks(K);
-  p.groups = 4 * p.nb;
-  p.vec = vector_rows(x, ldx, dtype == kF32 ? 4 : 2);
-  const unsigned grid = (unsigned)blocks_for(rows * p.groups);
-  if (dtype == kF32) mxfp4_quantize_kernel<float><<<grid, kQT, 0, st>>>(p);
-  else if (dtype == kF16) mxfp4_quantize_kernel<__half><<<grid, kQT, 0, st>>>(p);
-  else mxfp4_quantize_kernel<__nv_bfloat16><<<grid, kQT, 0, st>>>(p);
+  p.nb = p.walked = mx_blocks(K);
+  p.align = row_align(x, ldx, dtype == kF32 ? 4 : 2);
+  if (dtype == kF32) quantize_t<float>(p, st);
+  else if (dtype == kF16) quantize_t<__half>(p, st);
+  else quantize_t<__nv_bfloat16>(p, st);
   return cudaGetLastError();
 }
 
 cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out,
                                     int dtype, cudaStream_t st) {
-  const unsigned grid = (unsigned)blocks_for(rows * 4 * mx_blocks(K));
-  const bool vec = vector_rows(out, K, dtype == kF32 ? 4 : 2);
-  if (dtype == kF32)
-    mxfp4_dequantize_kernel<float><<<grid, kQT, 0, st>>>(codes, scales, rows, K, static_cast<float*>(out), vec);
-  else
-    mxfp4_dequantize_kernel<__nv_bfloat16>
-        <<<grid, kQT, 0, st>>>(codes, scales, rows, K, static_cast<__nv_bfloat16*>(out), vec);
+  const bool groups = K % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0;
+  const unsigned grid = groups ? blocks_for(rows * (K / 8), kDGroups) : blocks_for(rows * K, 8 * kQT);
+  if (dtype == kF32) {
+    float* o = static_cast<float*>(out);
+    if (groups) mxfp4_dequantize_kernel<float><<<grid, kQT, 0, st>>>(codes, scales, rows, K, o);
+    else mxfp4_dequantize_any_kernel<float><<<grid, kQT, 0, st>>>(codes, scales, rows, K, o);
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
+    if (groups) mxfp4_dequantize_kernel<__nv_bfloat16><<<grid, kQT, 0, st>>>(codes, scales, rows, K, o);
+    else mxfp4_dequantize_any_kernel<__nv_bfloat16><<<grid, kQT, 0, st>>>(codes, scales, rows, K, o);
+  }
   return cudaGetLastError();
 }
 
@@ -281,13 +347,18 @@ cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st) {
   p.scales = a.xsf;
   p.nb = mx_blocks(a.K);
   p.sf_chunks = mx_sf_chunks(a.K);
-  p.groups = (int64_t)p.sf_chunks * 16;
-  p.vec = vector_rows(a.x, a.ldx, 2);
-  const int64_t qb = blocks_for(p.rows * p.groups);
+  p.walked = (int64_t)p.sf_chunks * 4;
+  const int64_t qb = blocks_for(p.rows * p.walked, kQBlocks);
   const TileScales t{a.wscales, a.wsf, mx_wsf_blocks(a.N, a.gated, a.bn) * p.sf_chunks * 128, a.N, a.bn, a.gated};
-  const unsigned grid = (unsigned)(qb + (t.words + kQT - 1) / kQT);
-  if (a.dtype == kF16) mxfp4_prep_kernel<__half><<<grid, kQT, 0, st>>>(p, qb, t);
-  else mxfp4_prep_kernel<__nv_bfloat16><<<grid, kQT, 0, st>>>(p, qb, t);
+  const unsigned grid = (unsigned)qb + blocks_for(t.words, kQT);
+  // x's rows are 16-byte aligned (checked by the entry point)
+  if (row_align(a.x, a.ldx, 2) == 32) {
+    if (a.dtype == kF16) mxfp4_prep_kernel<__half, 32><<<grid, kQT, 0, st>>>(p, qb, t);
+    else mxfp4_prep_kernel<__nv_bfloat16, 32><<<grid, kQT, 0, st>>>(p, qb, t);
+  } else {
+    if (a.dtype == kF16) mxfp4_prep_kernel<__half, 16><<<grid, kQT, 0, st>>>(p, qb, t);
+    else mxfp4_prep_kernel<__nv_bfloat16, 16><<<grid, kQT, 0, st>>>(p, qb, t);
+  }
   return cudaGetLastError();
 }
 

@@ -17,10 +17,10 @@
 //           boxes and the descriptors say M- or N-major.
 //   gated   B's halves are gate rows and up rows of the same hidden units (SM 0
 //           loads the gate half, SM 1 the up half); each accumulator row then
-//           holds both, and the epilogue writes act(g) u, and g and u if kept.
-//   gated backward   the accumulators are dh; the epilogue reads g and u and
-//           writes dg = dh u act'(g) and du = dh act(g), so dh never leaves
-//           the chip.
+//           holds both, and the epilogue writes h = act(g) u and, if kept for
+//           the backward pass, p = u act'(g) and a = act(g).
+//   gated backward   the accumulators are dh; the epilogue reads p and a and
+//           writes dg = dh p and du = dh a, so dh never leaves the chip.
 //
 // Warps: 0 TMA producer (in both SMs), 1 MMA issuer (in SM 0 of the pair; the
 // whole warp runs the loop and one elected lane issues), 4-11 epilogue: a warp
@@ -82,11 +82,12 @@ struct alignas(64) PProb {
   int kc0, kc;             // K stages of segment 0 and in all
   int tm, t0;              // tiles along M; first tile in the list
   int a_mn, b_mn;
+  int wide;                // rows of the outputs are 32-byte aligned
 };
 
 struct PEpi {
-  void *g, *u;             // gated: kept g and u (or null); backward: dg and du
-  const void *gi, *ui;     // backward: g and u
+  uint8_t *p_hi, *a_hi, *p_lo, *a_lo;  // kept (null: not kept)
+  uint8_t *dg, *du;                    // backward
   int act, f16;
   int ksteps;              // MXFP4: MMA steps of 64 along K
 };
@@ -235,10 +236,98 @@ __device__ __forceinline__ PTile ptile(const PParams<NP>& p, int t) {
   return r;
 }
 
-// 8 consecutive 16-bit values
-__device__ __forceinline__ uint4 pack8(const float* v, bool f16) {
-  return make_uint4(pack16x2(v[0], v[1], f16), pack16x2(v[2], v[3], f16), pack16x2(v[4], v[5], f16),
-                    pack16x2(v[6], v[7], f16));
+// 16 consecutive columns n.. of a row of N (N a multiple of 8): 32 or 16 bytes
+// at element offset `at`, the part past N left alone.
+__device__ __forceinline__ void store16(void* base, size_t at, int n, int N, const uint32_t (&w)[8], bool wide) {
+  uint16_t* p = static_cast<uint16_t*>(base) + at;
+  if (wide) {
+    if (n < N) st_v8(p, w);  // N is a multiple of 16
+    return;
+  }
+  if (n < N) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (n + 8 < N) *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void store8(uint8_t* base, size_t at, int n, int N, const uint32_t (&w)[4], bool wide) {
+  uint8_t* p = base + at;
+  if (wide) {
+    if (n < N) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+  if (n < N) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  if (n + 8 < N) *reinterpret_cast<uint2*>(p + 8) = make_uint2(w[2], w[3]);
+}
+__device__ __forceinline__ void load16(const uint8_t* base, size_t at, int n, int N, uint32_t (&w)[8], bool wide) {
+  const uint8_t* p = base + 2 * at;
+  if (wide) {
+    if (n < N) ld_nc_v8(p, w);
+    return;
+  }
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  const uint4 a = n < N ? ldg_nc_v4(p) : z, b = n + 8 < N ? ldg_nc_v4(p + 16) : z;
+  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+}
+__device__ __forceinline__ void load8(const uint8_t* base, size_t at, int n, int N, uint32_t (&w)[4], bool wide) {
+  const uint8_t* p = base + at;
+  if (wide) {
+    if (n < N) {
+      const uint4 a = ldg_nc_v4(p);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    }
+    return;
+  }
+  const uint2 z = make_uint2(0u, 0u);
+  const uint2 a = n < N ? __ldg(reinterpret_cast<const uint2*>(p)) : z;
+  const uint2 b = n + 8 < N ? __ldg(reinterpret_cast<const uint2*>(p + 8)) : z;
+  w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
+}
+
+// p and a of 16 columns
+struct Kept16 {
+  uint32_t ph[8], ah[8], pl[4], al[4];
+};
+
+__device__ __forceinline__ void pack16(const float* v, bool f16, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack16x2(v[2 * i], v[2 * i + 1], f16);
+}
+
+// Epilogue of 16 hidden units: h, and p and a where kept.
+__device__ __forceinline__ void gate16(const PEpi& e, void* out, size_t at, int n, int N, const float* g,
+                                       const float* u, bool f16, bool wide) {
+  float v[16];
+  uint32_t w[8];
+  if (!e.p_hi) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = act_fwd(g[i], e.act) * u[i];
+    pack16(v, f16, w);
+    store16(out, at, n, N, w, wide);
+    return;
+  }
+  float p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float da;
+    act_fwd_grad(g[i], e.act, v[i], da);
+    p[i] = u[i] * da;
+  }
+  uint32_t l[4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = keep_hi2(p[2 * i], p[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) l[i] = keep_lo4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+  store16(e.p_hi, at, n, N, w, wide);
+  store8(e.p_lo, at, n, N, l, wide);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = keep_hi2(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) l[i] = keep_lo4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  store16(e.a_hi, at, n, N, w, wide);
+  store8(e.a_lo, at, n, N, l, wide);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] *= u[i];
+  pack16(v, f16, w);
+  store16(out, at, n, N, w, wide);
 }
 
 template <int KIND, int BN, int EPI, int NP>
@@ -393,89 +482,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     for (int t = cluster; t < p.n_tiles; t += clusters, ++titer) {
       const PTile d = ptile<NP>(p, t);
       const PProb& q = p.p[d.prob];
+      const bool wide = q.wide;
       const int db = titer % C::NACC, duse = titer / C::NACC;
-      if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
-      tc_fence_after();
       const int row = d.m * 256 + (int)rank * 128 + quarter * 32 + lane;
       const bool rok = row < q.M;
+      const size_t base = (size_t)row * q.N;
       const uint32_t trow = taddr + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(db * BN);
+      const int N = rok ? q.N : 0;  // a row past M has no columns
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(leader_addr(&sm.d_empty[db]));
+      };
       if constexpr (EPI == kEpiGated) {
         constexpr int HU = BN / 4;  // hidden units of this warp
-        constexpr int CW = 16;
-        const size_t base = (size_t)row * q.N;
+        const int col0 = half * HU, n0 = d.n * (BN / 2) + col0;
+        if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
+        tc_fence_after();
+        if constexpr (C::NACC == 1) {
+          // the only accumulator: into registers at once, so that the next
+          // tile's products start before this one's gate is computed
+          float g[HU], u[HU];
 #pragma unroll
-        for (int cc = 0; cc < HU / CW; ++cc) {
-          const int col = half * HU + cc * CW;
-          float g[CW], u[CW];
-          tmem_ld16(trow + col, g);
-          tmem_ld16(trow + BN / 2 + col, u);
-          const int n = d.n * (BN / 2) + col;
+          for (int c = 0; c < HU; c += 32) {
+            tmem_ld32(trow + col0 + c, *reinterpret_cast<float(*)[32]>(g + c));
+            tmem_ld32(trow + BN / 2 + col0 + c, *reinterpret_cast<float(*)[32]>(u + c));
+          }
+          release();
 #pragma unroll
-          for (int k = 0; k < CW; k += 8) {
-            if (rok && n + k < q.N) {
-              if (p.e.g) {
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.g) + base + n + k) = pack8(g + k, f16);
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.u) + base + n + k) = pack8(u + k, f16);
-              }
-              float h[8];
+          for (int c = 0; c < HU; c += 16) gate16(p.e, q.out, base + n0 + c, n0 + c, N, g + c, u + c, f16, wide);
+        } else {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) h[i] = act_fwd(g[k + i], p.e.act) * u[k + i];
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(q.out) + base + n + k) = pack8(h, f16);
+          for (int c = 0; c < HU; c += 16) {
+            float g[16], u[16];
+            tmem_ld16(trow + col0 + c, g);
+            tmem_ld16(trow + BN / 2 + col0 + c, u);
+            gate16(p.e, q.out, base + n0 + c, n0 + c, N, g, u, f16, wide);
+          }
+          release();
+        }
+      } else if constexpr (EPI == kEpiPlain) {
+        constexpr int HC = BN / 2;
+        const int col0 = half * HC, n0 = d.n * BN + col0;
+        if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
+        tc_fence_after();
+        if constexpr (C::NACC == 1) {
+          float v[HC];
+#pragma unroll
+          for (int c = 0; c < HC; c += 32) tmem_ld32(trow + col0 + c, *reinterpret_cast<float(*)[32]>(v + c));
+          release();
+#pragma unroll
+          for (int c = 0; c < HC; c += 16) {
+            uint32_t w[8];
+            pack16(v + c, f16, w);
+            store16(q.out, base + n0 + c, n0 + c, N, w, wide);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC; c += 32) {
+            float v[32];
+            tmem_ld32(trow + col0 + c, v);
+#pragma unroll
+            for (int k = 0; k < 32; k += 16) {
+              uint32_t w[8];
+              pack16(v + k, f16, w);
+              store16(q.out, base + n0 + c + k, n0 + c + k, N, w, wide);
             }
           }
+          release();
         }
       } else {
-        constexpr int HC = BN / 2, CW = 32;
-        const size_t base = (size_t)row * q.N;
+        // p and a of the first columns are on their way while the products run,
+        // and those of the next 16 while 16 are computed
+        constexpr int HC = BN / 2;
+        const int col0 = half * HC, n0 = d.n * BN + col0;
+        Kept16 k[2];
+        auto fetch = [&](int c, Kept16& r) {
+          load16(p.e.p_hi, base + n0 + c, n0 + c, N, r.ph, wide);
+          load16(p.e.a_hi, base + n0 + c, n0 + c, N, r.ah, wide);
+          load8(p.e.p_lo, base + n0 + c, n0 + c, N, r.pl, wide);
+          load8(p.e.a_lo, base + n0 + c, n0 + c, N, r.al, wide);
+        };
+        fetch(0, k[0]);
+        if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
+        tc_fence_after();
 #pragma unroll
-        for (int cc = 0; cc < HC / CW; ++cc) {
-          const int col = half * HC + cc * CW;
-          const int n = d.n * BN + col;
-          uint4 gi[EPI == kEpiGatedBwd ? 4 : 1], ui[EPI == kEpiGatedBwd ? 4 : 1];
-          if constexpr (EPI == kEpiGatedBwd) {
+        for (int c = 0; c < HC; c += 16) {
+          if (c + 16 < HC) fetch(c + 16, k[(c / 16 + 1) & 1]);
+          const Kept16& r = k[(c / 16) & 1];
+          float v[16], o[16];
+          tmem_ld16(trow + col0 + c, v);
+          uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              gi[k] = ui[k] = make_uint4(0u, 0u, 0u, 0u);
-              if (rok && n + 8 * k < q.N) {
-                gi[k] = ldg_nc_v4(static_cast<const uint16_t*>(p.e.gi) + base + n + 8 * k);
-                ui[k] = ldg_nc_v4(static_cast<const uint16_t*>(p.e.ui) + base + n + 8 * k);
-              }
-            }
-          }
-          float v[CW];
-          tmem_ld32(trow + col, v);
+          for (int i = 0; i < 16; ++i) o[i] = v[i] * kept(r.ph[(i / 4) * 2], r.ph[(i / 4) * 2 + 1], r.pl[i / 4], i & 3);
+          pack16(o, f16, w);
+          store16(p.e.dg, base + n0 + c, n0 + c, N, w, wide);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (!rok || n + 8 * k >= q.N) continue;
-            if constexpr (EPI == kEpiPlain) {
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(q.out) + base + n + 8 * k) = pack8(v + 8 * k, f16);
-            } else {
-              const uint32_t gw[4] = {gi[k].x, gi[k].y, gi[k].z, gi[k].w};
-              const uint32_t uw[4] = {ui[k].x, ui[k].y, ui[k].z, ui[k].w};
-              float dg[8], du[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float g2[2], u2[2];
-                unpack16x2(gw[i], f16, g2[0], g2[1]);
-                unpack16x2(uw[i], f16, u2[0], u2[1]);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  float a, da;
-                  act_fwd_grad(g2[j], p.e.act, a, da);
-                  const float dh = v[8 * k + 2 * i + j];
-                  dg[2 * i + j] = dh * u2[j] * da;
-                  du[2 * i + j] = dh * a;
-                }
-              }
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.g) + base + n + 8 * k) = pack8(dg, f16);
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.u) + base + n + 8 * k) = pack8(du, f16);
-            }
-          }
+          for (int i = 0; i < 16; ++i) o[i] = v[i] * kept(r.ah[(i / 4) * 2], r.ah[(i / 4) * 2 + 1], r.al[i / 4], i & 3);
+          pack16(o, f16, w);
+          store16(p.e.du, base + n0 + c, n0 + c, N, w, wide);
         }
+        release();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(leader_addr(&sm.d_empty[db]));
     }
   }
 
@@ -529,6 +637,10 @@ int pick_bn(int64_t tiles256, int64_t tiles128, int64_t tiles64, int clusters) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// 32-byte accesses of 16-bit rows of N (the kept planes and the workspace's
+// tensors are 256-byte aligned, so their rows follow N alone)
+bool wide_rows(const void* p, int N) { return N % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+
 }  // namespace
 
 cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st) {
@@ -556,6 +668,7 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
     q.out = g[i].out;
     q.M = g[i].M;
     q.N = g[i].N;
+    q.wide = wide_rows(q.out, q.N);
     q.kc0 = (int)cdiv(g[i].seg[0].K, 64);
     q.kc = q.kc0 + (g[i].nseg > 1 ? (int)cdiv(g[i].seg[1].K, 64) : 0);
     q.tm = (int)cdiv(q.M, 256);
@@ -589,10 +702,15 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   q.out = a.h;
   q.M = a.T;
   q.N = a.I;
+  q.wide = wide_rows(a.h, a.I);
   q.kc0 = q.kc = (int)cdiv(a.K, 64);
   q.tm = (int)tm;
-  p.e.g = a.g;
-  p.e.u = a.u;
+  if (a.keep) {
+    p.e.p_hi = a.kept.p_hi;
+    p.e.a_hi = a.kept.a_hi;
+    p.e.p_lo = a.kept.p_lo;
+    p.e.a_lo = a.kept.a_lo;
+  }
   p.e.act = a.act;
   p.e.f16 = a.dtype == kF16;
   p.np = 1;
@@ -620,11 +738,13 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   q.kc0 = q.kc = (int)cdiv(a.H, 64);
   q.tm = (int)tm;
   q.b_mn = 1;
-  p.e.g = a.dg;
-  p.e.u = a.du;
-  p.e.gi = a.g;
-  p.e.ui = a.u;
-  p.e.act = a.act;
+  q.wide = wide_rows(a.dg, a.I);
+  p.e.p_hi = a.kept.p_hi;
+  p.e.a_hi = a.kept.a_hi;
+  p.e.p_lo = a.kept.p_lo;
+  p.e.a_lo = a.kept.a_lo;
+  p.e.dg = static_cast<uint8_t*>(a.dg);
+  p.e.du = static_cast<uint8_t*>(a.du);
   p.e.f16 = a.dtype == kF16;
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn));
@@ -661,6 +781,7 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   q.out = a.y;
   q.M = a.T;
   q.N = a.N;
+  q.wide = wide_rows(a.y, a.N);
   q.kc0 = q.kc = (int)cdiv(a.K, 256);
   q.tm = (int)tm;
   p.e.act = a.act;

@@ -53,7 +53,9 @@ struct SkinnyParams {
 template <int CODEC, int NT8, bool GATED, bool OPT>
 __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
   constexpr bool F16 = CODEC == 0 && OPT, QX = CODEC == 1 && OPT;
-  constexpr int U = CODEC == 1 ? 3 : 6;   // steps of K in flight per warp
+  // steps of K in flight per warp: for one group of tokens the whole K of the
+  // layer's sizes, for more what the registers allow
+  constexpr int U = CODEC == 1 ? 3 : (NT8 == 1 ? 11 : 6);
   constexpr int XW = CODEC == 1 ? 4 : 1;  // 16-byte pieces of x per step and token
   __shared__ float4 red[kSkWarps][NT8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

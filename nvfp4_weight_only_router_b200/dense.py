@@ -42,9 +42,10 @@ def _rows(t: torch.Tensor, what: str, features: int | None = None) -> int:
         raise ValueError(f"{what} must have contiguous features")
     if n <= 1:
         return f
-    if t.stride(0) < f:
+    ld = t.stride(0)
+    if ld < f:
         raise ValueError(f"{what} has overlapping rows")
-    return t.stride(0)
+    return ld
 
 
 def _same(what: str, *tensors: torch.Tensor) -> None:
@@ -63,18 +64,23 @@ def _contiguous(what: str, *tensors: torch.Tensor) -> None:
 def _on(stream, *tensors: torch.Tensor):
     """Context in which the call allocates and launches: the tensors' device,
     and `stream` if given (the tensors are then also held for it)."""
-    dev = tensors[0].device
     if stream is not None:
-        if stream.device != dev:
+        if stream.device != tensors[0].device:
             raise ValueError("stream and tensors are on different devices")
         for t in tensors:
             t.record_stream(stream)
         return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    dev = tensors[0].get_device()
+    return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _stream_ptr(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+# the stream's handle, without a Stream object around it (1 us of a call's 10)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _bytes(n: int, t: torch.Tensor) -> torch.Tensor:
+    """n (at least 256) bytes of workspace on t's device; 0 means arguments that the call refuses."""
+    return t.new_empty(max(n, 256), dtype=torch.uint8)
 
 
 # ------------------------------------------------------------------- MXFP4
@@ -87,10 +93,9 @@ def mxfp4_quantize(x: torch.Tensor, stream=None):
     R, K = x.shape
     nb = (K + 31) // 32
     with _on(stream, x):
-        codes = torch.empty((R, 16 * nb), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((R, nb), dtype=torch.uint8, device=x.device)
+        codes, scales = x.new_empty((R, 16 * nb), dtype=torch.uint8), x.new_empty((R, nb), dtype=torch.uint8)
         check(dc.mxfp4_quantize(x.data_ptr(), _DTYPE[x.dtype], R, K, ld, codes.data_ptr(), scales.data_ptr(),
-                                _stream_ptr(x)), "mxfp4_quantize")
+                                _raw_stream(x.get_device())), "mxfp4_quantize")
     return codes, scales
 
 
@@ -108,7 +113,7 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor, K: int | None = 
     with _on(stream, codes, scales):
         out = torch.empty((R, K), dtype=dtype, device=codes.device)
         check(dc.mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), R, K, out.data_ptr(), _DTYPE[dtype],
-                                  _stream_ptr(codes)), "mxfp4_dequantize")
+                                  _raw_stream(codes.get_device())), "mxfp4_dequantize")
     return out
 
 
@@ -151,7 +156,7 @@ class Mxfp4Weight:
         return mxfp4_dequantize(self.codes, self.scales, self.K, dtype, stream)
 
 
-def _linear(name, x, weight, activation, stream):
+def _linear(name, call, size, x, weight, activation, stream):
     act = _act(activation)
     ld = _rows(x, "x", weight.K)
     if x.dtype not in _DTYPE:
@@ -161,24 +166,24 @@ def _linear(name, x, weight, activation, stream):
     T = x.shape[0]
     c = _byref(weight._c)
     with _on(stream, x, weight.codes, weight.scales):
-        y = torch.empty((T, weight.N // 2 if act else weight.N), dtype=x.dtype, device=x.device)
-        # 0 bytes: arguments that the call below refuses
-        ws = torch.empty(max(getattr(dc, name + "_workspace_bytes")(T, c, act), 256), dtype=torch.uint8,
-                         device=x.device)
-        check(getattr(dc, name)(x.data_ptr(), _DTYPE[x.dtype], ld, T, c, act, y.data_ptr(), ws.data_ptr(), ws.numel(),
-                                _stream_ptr(x)), name)
+        y = x.new_empty((T, weight.N // 2 if act else weight.N))
+        need = size(T, c, act)
+        ws = _bytes(need, x) if need > 256 else None   # few tokens take none
+        check(call(x.data_ptr(), _DTYPE[x.dtype], ld, T, c, act, y.data_ptr(), None if ws is None else ws.data_ptr(),
+                   need, _raw_stream(x.get_device())), name)
     return y
 
 
 def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A16: y [T, N] = x weight^T for bf16 x [T, K]; with an activation the
     gated form y [T, N/2] = act(x Wg^T) * (x Wu^T)."""
-    return _linear("mxfp4_linear", x, weight, activation, stream)
+    return _linear("mxfp4_linear", dc.mxfp4_linear, dc.mxfp4_linear_workspace_bytes, x, weight, activation, stream)
 
 
 def mxfp4_linear_a4(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A4: mxfp4_linear with x (bf16 or f16) quantised to MXFP4 on the way in."""
-    return _linear("mxfp4_linear_a4", x, weight, activation, stream)
+    return _linear("mxfp4_linear_a4", dc.mxfp4_linear_a4, dc.mxfp4_linear_a4_workspace_bytes, x, weight, activation,
+                   stream)
 
 
 # ------------------------------------------------------------- feed-forward
@@ -199,23 +204,22 @@ def _ffn_weights(gate, up, down, activation) -> dc.gated_ffn_weights:
 def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                       activation: str = "gelu_tanh", save: bool = False, stream=None):
     """y [T, H] = (act(x gate^T) * (x up^T)) down^T, for bf16 or f16 x [T, H],
-    gate, up [I, H], down [H, I]; with save, (y, saved) where saved [3, T, I]
-    is what gated_ffn_backward takes."""
+    gate, up [I, H], down [H, I]; with save, (y, saved) where saved (bytes, 8 T I
+    of them and padding) is what gated_ffn_backward takes."""
     f = _ffn_weights(gate, up, down, activation)
     ld = _rows(x, "x", f.H)
     _same("x and the weights", x, gate)
     T = x.shape[0]
     with _on(stream, x, gate, up, down):
-        y = torch.empty((T, f.H), dtype=x.dtype, device=x.device)
+        y = x.new_empty((T, f.H))
         if save:
-            saved = torch.empty((3, T, f.I), dtype=x.dtype, device=x.device)
-            check(dc.gated_ffn_forward(x.data_ptr(), ld, T, _byref(f), y.data_ptr(), saved.data_ptr() or None, None, 0,
-                                       _stream_ptr(x)) if T else 0, "gated_ffn_forward")
+            saved = _bytes(dc.gated_ffn_saved_bytes(T, _byref(f)), x)
+            check(dc.gated_ffn_forward(x.data_ptr(), ld, T, _byref(f), y.data_ptr(), saved.data_ptr(), None, 0,
+                                       _raw_stream(x.get_device())), "gated_ffn_forward")
             return y, saved
-        ws = torch.empty(max(dc.gated_ffn_forward_workspace_bytes(T, _byref(f)), 256), dtype=torch.uint8,
-                         device=x.device)
+        ws = _bytes(dc.gated_ffn_forward_workspace_bytes(T, _byref(f)), x)
         check(dc.gated_ffn_forward(x.data_ptr(), ld, T, _byref(f), y.data_ptr(), None, ws.data_ptr(), ws.numel(),
-                                   _stream_ptr(x)), "gated_ffn_forward")
+                                   _raw_stream(x.get_device())), "gated_ffn_forward")
     return y
 
 
@@ -227,18 +231,17 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up
     f = _ffn_weights(gate, up, down, activation)
     ld, lddy = _rows(x, "x", f.H), _rows(dy, "dy", f.H)
     T = x.shape[0]
-    _same("dy, x, saved and the weights", dy, x, saved, gate)
-    if dy.shape[0] != T or saved.shape != (3, T, f.I):
+    _same("dy, x and the weights", dy, x, gate)
+    if (dy.shape[0] != T or saved.dtype != torch.uint8 or saved.device != x.device
+            or saved.shape != (max(dc.gated_ffn_saved_bytes(T, _byref(f)), 256),)):
         raise ValueError("dy and saved must be those of x's forward pass")
     _contiguous("saved", saved)
     with _on(stream, dy, x, gate, up, down, saved):
-        outs = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need else None
-                for w, need in zip((x, gate, up, down), needs)]
-        ws = torch.empty(max(dc.gated_ffn_backward_workspace_bytes(T, _byref(f)), 256), dtype=torch.uint8,
-                         device=x.device)
+        outs = [w.new_empty(w.shape) if need else None for w, need in zip((x, gate, up, down), needs)]
+        ws = _bytes(dc.gated_ffn_backward_workspace_bytes(T, _byref(f)), x)
         check(dc.gated_ffn_backward(dy.data_ptr(), lddy, x.data_ptr(), ld, saved.data_ptr(), T, _byref(f),
                                     *(None if o is None else o.data_ptr() for o in outs), ws.data_ptr(), ws.numel(),
-                                    _stream_ptr(x)), "gated_ffn_backward")
+                                    _raw_stream(x.get_device())), "gated_ffn_backward")
     return tuple(outs)
 
 

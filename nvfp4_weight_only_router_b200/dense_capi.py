@@ -42,6 +42,7 @@ SIGNATURES = {
     "mxfp4_linear": (c_int32, _LINEAR),
     "mxfp4_linear_a4_workspace_bytes": (c_size_t, [c_int32, _W, c_int32]),
     "mxfp4_linear_a4": (c_int32, _LINEAR),
+    "gated_ffn_saved_bytes": (c_size_t, [c_int32, _F]),
     "gated_ffn_forward_workspace_bytes": (c_size_t, [c_int32, _F]),
     "gated_ffn_forward": (c_int32, [c_void_p, c_int64, c_int32, _F, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "gated_ffn_backward_workspace_bytes": (c_size_t, [c_int32, _F]),

@@ -87,10 +87,10 @@ def test_linear_refusals(dc, codes, a4):
     assert run(T=(1 << 20) + 1) == c.NVFP4_ERR_UNSUPPORTED
     assert run(x=P + 2) == run(y=P + 8) == run(ldx=68) == run(w=_w(dc, s=P + 4)) == c.NVFP4_ERR_ALIGNMENT
     assert run(ws=P + 16) == c.NVFP4_ERR_ALIGNMENT
-    for T in (4, 500):
-        n = size(T, ctypes.byref(w), 0)
-        assert n >= 256
-        assert run(T=T, n=n - 1) == run(T=T, ws=None) == c.NVFP4_ERR_WORKSPACE
+    assert size(4, ctypes.byref(w), 0) == 256                           # few tokens: none is used
+    n = size(500, ctypes.byref(w), 0)
+    assert n > 256
+    assert run(T=500, n=n - 1) == run(T=500, ws=None) == c.NVFP4_ERR_WORKSPACE
     assert run(T=0, x=None, y=None) == c.NVFP4_OK
 
 
@@ -122,6 +122,12 @@ def test_ffn_refusals(dc, codes):
     assert bwd(outs=(None,) * 4, T=0) == c.NVFP4_OK
     n = dc.gated_ffn_backward_workspace_bytes(100, ctypes.byref(_f(dc)))
     assert bwd(T=100, n=n - 1) == c.NVFP4_ERR_WORKSPACE
+    assert bwd(saved=P + 16) == c.NVFP4_ERR_ALIGNMENT
+    # h in 16 bits, two tensors in 24, each plane on a 256-byte boundary
+    assert dc.gated_ffn_saved_bytes(100, ctypes.byref(_f(dc))) == 3 * 12800 + 2 * 6400
+    assert dc.gated_ffn_saved_bytes(3, ctypes.byref(_f(dc, I=8))) == 5 * 256
+    assert dc.gated_ffn_saved_bytes(0, ctypes.byref(_f(dc))) == 256
+    assert dc.gated_ffn_saved_bytes(100, ctypes.byref(_f(dc, I=4))) == 0
     assert dc.gated_ffn_backward_workspace_bytes(100, ctypes.byref(_f(dc, I=4))) == 0
 
 
