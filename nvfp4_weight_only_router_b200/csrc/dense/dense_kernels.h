@@ -49,7 +49,10 @@ inline int64_t mx_wsf_blocks(int N, bool gated, int bn) {
 cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- skinny.cu
-constexpr int kSkinnyMaxTokens = 32;
+#ifndef SK_MAX
+#define SK_MAX 32
+#endif
+constexpr int kSkinnyMaxTokens = SK_MAX;
 struct SkinnyArgs {
   const void* x;      // [T, K]
   int64_t ldx;        // elements
@@ -87,16 +90,20 @@ struct PairGemm {
 constexpr int kPairMaxProblems = 4;
 // plain products, one launch for all (at most kPairMaxProblems); out = sum over segments A B^T
 cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st);
-// What the forward pass keeps for the backward one: h, and p = u act'(g) and
-// a = act(g) in 24 bits (a 16-bit and an 8-bit plane each), [T, I] all
+// What the forward pass keeps for the backward one: h [T, I], and p = u act'(g)
+// and a = act(g) in 24 bits, in blocks of 32 rows x 16 hidden units (row blocks
+// outermost, edges padded) as an epilogue warp holds them, a row per lane:
+// 32 x 32 bytes of p's upper 16 bits, as many of a's, 32 x 16 bytes of p's
+// lower 8 bits and of a's.
+constexpr int kKeptBlockB = 3072;
 struct PairKept {
-  uint8_t *h, *p_hi, *a_hi, *p_lo, *a_lo;
+  uint8_t *h, *blocks;
   size_t bytes;
 };
 inline PairKept pair_kept(void* base, int64_t T, int64_t I) {
-  const size_t p2 = ((size_t)(T * I) * 2 + 255) / 256 * 256, p1 = ((size_t)(T * I) + 255) / 256 * 256;
+  const size_t hb = ((size_t)(T * I) * 2 + 255) / 256 * 256;
   uint8_t* b = static_cast<uint8_t*>(base);
-  return PairKept{b, b + p2, b + 2 * p2, b + 3 * p2, b + 3 * p2 + p1, 3 * p2 + 2 * p1};
+  return PairKept{b, b + hb, hb + (size_t)((T + 31) / 32 * ((I + 15) / 16)) * kKeptBlockB};
 }
 // h = act(x gate^T) * (x up^T)
 struct PairGated {

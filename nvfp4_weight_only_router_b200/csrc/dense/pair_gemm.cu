@@ -86,8 +86,8 @@ struct alignas(64) PProb {
 };
 
 struct PEpi {
-  uint8_t *p_hi, *a_hi, *p_lo, *a_lo;  // kept (null: not kept)
-  uint8_t *dg, *du;                    // backward
+  uint8_t* kept;           // PairKept's blocks (null: not kept)
+  uint8_t *dg, *du;        // backward
   int act, f16;
   int ksteps;              // MXFP4: MMA steps of 64 along K
 };
@@ -247,85 +247,62 @@ __device__ __forceinline__ void store16(void* base, size_t at, int n, int N, con
   if (n < N) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   if (n + 8 < N) *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
-__device__ __forceinline__ void store8(uint8_t* base, size_t at, int n, int N, const uint32_t (&w)[4], bool wide) {
-  uint8_t* p = base + at;
-  if (wide) {
-    if (n < N) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    return;
-  }
-  if (n < N) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  if (n + 8 < N) *reinterpret_cast<uint2*>(p + 8) = make_uint2(w[2], w[3]);
-}
-__device__ __forceinline__ void load16(const uint8_t* base, size_t at, int n, int N, uint32_t (&w)[8], bool wide) {
-  const uint8_t* p = base + 2 * at;
-  if (wide) {
-    if (n < N) ld_nc_v8(p, w);
-    return;
-  }
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  const uint4 a = n < N ? ldg_nc_v4(p) : z, b = n + 8 < N ? ldg_nc_v4(p + 16) : z;
-  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-  w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-}
-__device__ __forceinline__ void load8(const uint8_t* base, size_t at, int n, int N, uint32_t (&w)[4], bool wide) {
-  const uint8_t* p = base + at;
-  if (wide) {
-    if (n < N) {
-      const uint4 a = ldg_nc_v4(p);
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    }
-    return;
-  }
-  const uint2 z = make_uint2(0u, 0u);
-  const uint2 a = n < N ? __ldg(reinterpret_cast<const uint2*>(p)) : z;
-  const uint2 b = n + 8 < N ? __ldg(reinterpret_cast<const uint2*>(p + 8)) : z;
-  w[0] = a.x; w[1] = a.y; w[2] = b.x; w[3] = b.y;
-}
-
-// p and a of 16 columns
+// p and a of 16 hidden units of one row
 struct Kept16 {
   uint32_t ph[8], ah[8], pl[4], al[4];
 };
+// the lane's part of a kept block
+__device__ __forceinline__ void kept_load(const uint8_t* blk, int lane, Kept16& k) {
+  ld_nc_v8(blk + lane * 32, k.ph);
+  ld_nc_v8(blk + 1024 + lane * 32, k.ah);
+  const uint4 a = ldg_nc_v4(blk + 2048 + lane * 16), b = ldg_nc_v4(blk + 2560 + lane * 16);
+  k.pl[0] = a.x; k.pl[1] = a.y; k.pl[2] = a.z; k.pl[3] = a.w;
+  k.al[0] = b.x; k.al[1] = b.y; k.al[2] = b.z; k.al[3] = b.w;
+}
+__device__ __forceinline__ void kept_store(uint8_t* blk, int lane, const Kept16& k) {
+  st_v8(blk + lane * 32, k.ph);
+  st_v8(blk + 1024 + lane * 32, k.ah);
+  *reinterpret_cast<uint4*>(blk + 2048 + lane * 16) = make_uint4(k.pl[0], k.pl[1], k.pl[2], k.pl[3]);
+  *reinterpret_cast<uint4*>(blk + 2560 + lane * 16) = make_uint4(k.al[0], k.al[1], k.al[2], k.al[3]);
+}
 
 __device__ __forceinline__ void pack16(const float* v, bool f16, uint32_t (&w)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack16x2(v[2 * i], v[2 * i + 1], f16);
 }
 
-// Epilogue of 16 hidden units: h, and p and a where kept.
-__device__ __forceinline__ void gate16(const PEpi& e, void* out, size_t at, int n, int N, const float* g,
-                                       const float* u, bool f16, bool wide) {
+// Epilogue of 16 hidden units of a row: h, and p and a where kept (blk, null
+// where the warp's rows or the units lie outside).
+__device__ __forceinline__ void gate16(const PEpi& e, void* out, size_t at, int n, int N, uint8_t* blk, int lane,
+                                       const float* g, const float* u, bool f16, bool wide) {
   float v[16];
   uint32_t w[8];
-  if (!e.p_hi) {
+  if (!e.kept) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = act_fwd(g[i], e.act) * u[i];
-    pack16(v, f16, w);
-    store16(out, at, n, N, w, wide);
-    return;
+  } else {
+    float p[16];
+    Kept16 k;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float da;
+      act_fwd_grad(g[i], e.act, v[i], da);
+      p[i] = u[i] * da;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      k.ph[i] = keep_hi2(p[2 * i], p[2 * i + 1]);
+      k.ah[i] = keep_hi2(v[2 * i], v[2 * i + 1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      k.pl[i] = keep_lo4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+      k.al[i] = keep_lo4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    if (blk) kept_store(blk, lane, k);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= u[i];
   }
-  float p[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float da;
-    act_fwd_grad(g[i], e.act, v[i], da);
-    p[i] = u[i] * da;
-  }
-  uint32_t l[4];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = keep_hi2(p[2 * i], p[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) l[i] = keep_lo4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-  store16(e.p_hi, at, n, N, w, wide);
-  store8(e.p_lo, at, n, N, l, wide);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = keep_hi2(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) l[i] = keep_lo4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-  store16(e.a_hi, at, n, N, w, wide);
-  store8(e.a_lo, at, n, N, l, wide);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] *= u[i];
   pack16(v, f16, w);
   store16(out, at, n, N, w, wide);
 }
@@ -489,6 +466,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       const size_t base = (size_t)row * q.N;
       const uint32_t trow = taddr + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(db * BN);
       const int N = rok ? q.N : 0;  // a row past M has no columns
+      // the kept block of this warp's rows and hidden units n..n + 15, null outside
+      const int row_blk = (row - lane) >> 5, blks = (q.N + 15) >> 4;
+      auto kept_blk = [&](int n) {
+        return EPI != kEpiPlain && row - lane < q.M && n < q.N
+                   ? p.e.kept + ((size_t)row_blk * blks + (n >> 4)) * kKeptBlockB : nullptr;
+      };
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -510,14 +493,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           }
           release();
 #pragma unroll
-          for (int c = 0; c < HU; c += 16) gate16(p.e, q.out, base + n0 + c, n0 + c, N, g + c, u + c, f16, wide);
+          for (int c = 0; c < HU; c += 16) 
+            gate16(p.e, q.out, base + n0 + c, n0 + c, N, kept_blk(n0 + c), lane, g + c, u + c, f16, wide);
         } else {
 #pragma unroll
           for (int c = 0; c < HU; c += 16) {
             float g[16], u[16];
             tmem_ld16(trow + col0 + c, g);
             tmem_ld16(trow + BN / 2 + col0 + c, u);
-            gate16(p.e, q.out, base + n0 + c, n0 + c, N, g, u, f16, wide);
+            gate16(p.e, q.out, base + n0 + c, n0 + c, N, kept_blk(n0 + c), lane, g, u, f16, wide);
           }
           release();
         }
@@ -553,23 +537,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         }
       } else {
         // p and a of the first columns are on their way while the products run,
-        // and those of the next 16 while 16 are computed
+        // and those of the next 32 while 16 are computed
         constexpr int HC = BN / 2;
         const int col0 = half * HC, n0 = d.n * BN + col0;
-        Kept16 k[2];
-        auto fetch = [&](int c, Kept16& r) {
-          load16(p.e.p_hi, base + n0 + c, n0 + c, N, r.ph, wide);
-          load16(p.e.a_hi, base + n0 + c, n0 + c, N, r.ah, wide);
-          load8(p.e.p_lo, base + n0 + c, n0 + c, N, r.pl, wide);
-          load8(p.e.a_lo, base + n0 + c, n0 + c, N, r.al, wide);
+        constexpr int AHEAD = 2;
+        Kept16 k[AHEAD + 1];
+        auto fetch = [&](int c) {
+          const uint8_t* blk = kept_blk(n0 + c);
+          if (blk) kept_load(blk, lane, k[(c / 16) % (AHEAD + 1)]);  // else: unused
         };
-        fetch(0, k[0]);
+#pragma unroll
+        for (int c = 0; c < 16 * AHEAD; c += 16) fetch(c);
         if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < HC; c += 16) {
-          if (c + 16 < HC) fetch(c + 16, k[(c / 16 + 1) & 1]);
-          const Kept16& r = k[(c / 16) & 1];
+          if (c + 16 * AHEAD < HC) fetch(c + 16 * AHEAD);
+          const Kept16& r = k[(c / 16) % (AHEAD + 1)];
           float v[16], o[16];
           tmem_ld16(trow + col0 + c, v);
           uint32_t w[8];
@@ -637,8 +621,7 @@ int pick_bn(int64_t tiles256, int64_t tiles128, int64_t tiles64, int clusters) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// 32-byte accesses of 16-bit rows of N (the kept planes and the workspace's
-// tensors are 256-byte aligned, so their rows follow N alone)
+// 32-byte stores of 16-bit rows of N
 bool wide_rows(const void* p, int N) { return N % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0; }
 
 }  // namespace
@@ -705,12 +688,7 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   q.wide = wide_rows(a.h, a.I);
   q.kc0 = q.kc = (int)cdiv(a.K, 64);
   q.tm = (int)tm;
-  if (a.keep) {
-    p.e.p_hi = a.kept.p_hi;
-    p.e.a_hi = a.kept.a_hi;
-    p.e.p_lo = a.kept.p_lo;
-    p.e.a_lo = a.kept.a_lo;
-  }
+  if (a.keep) p.e.kept = a.kept.blocks;
   p.e.act = a.act;
   p.e.f16 = a.dtype == kF16;
   p.np = 1;
@@ -739,10 +717,7 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   q.tm = (int)tm;
   q.b_mn = 1;
   q.wide = wide_rows(a.dg, a.I);
-  p.e.p_hi = a.kept.p_hi;
-  p.e.a_hi = a.kept.a_hi;
-  p.e.p_lo = a.kept.p_lo;
-  p.e.a_lo = a.kept.a_lo;
+  p.e.kept = a.kept.blocks;
   p.e.dg = static_cast<uint8_t*>(a.dg);
   p.e.du = static_cast<uint8_t*>(a.du);
   p.e.f16 = a.dtype == kF16;

@@ -62,6 +62,11 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
   const int r = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  // this CTA's tokens
+  const uint8_t* px = p.x + (size_t)blockIdx.y * (NT8 * 8) * p.ldx_bytes;
+  uint16_t* py = p.y + (size_t)blockIdx.y * (NT8 * 8) * p.N;
+  const int T = p.T - (int)blockIdx.y * (NT8 * 8);
+
   const int row_a = GATED ? blockIdx.x * 8 + r : blockIdx.x * 16 + r;
   const int row_b = GATED ? row_a : row_a + 8;
   const bool ok_a = row_a < p.N, ok_b = row_b < p.N;
@@ -112,8 +117,8 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
         for (int i = 0; i < XW; ++i) {
           xv[j][i] = make_uint4(0u, 0u, 0u, 0u);
           // plain loads: x may have been written by the kernel before
-          if (t < p.T && unit < p.units)
-            xv[j][i] = *reinterpret_cast<const uint4*>(p.x + (size_t)t * p.ldx_bytes + ((size_t)unit * XW + i) * 16);
+          if (t < T && unit < p.units)
+            xv[j][i] = *reinterpret_cast<const uint4*>(px + (size_t)t * p.ldx_bytes + ((size_t)unit * XW + i) * 16);
         }
       }
       if constexpr (CODEC == 0) {
@@ -189,9 +194,9 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t0 + i;
-      if (t >= p.T) break;
+      if (t >= T) break;
       const float v0 = i ? d.y : d.x, v1 = i ? d.w : d.z;
-      uint16_t* y = p.y + (size_t)t * p.N;
+      uint16_t* y = py + (size_t)t * p.N;
       if (GATED) {
         if (ok_a) y[row_a] = (uint16_t)pack16x2(act_fwd(v0, p.act) * v1, 0.f, p.f16);
       } else {
@@ -207,7 +212,7 @@ template <int CODEC, bool GATED, bool OPT>
 cudaError_t launch_nt(const SkinnyParams& p, int T, bool after, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   const int rows = GATED ? 8 : 16;
-  cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows));
+  cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows), (unsigned)((T + 31) / 32));
   cfg.blockDim = dim3(kSkThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];

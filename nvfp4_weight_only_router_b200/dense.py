@@ -204,8 +204,8 @@ def _ffn_weights(gate, up, down, activation) -> dc.gated_ffn_weights:
 def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
                       activation: str = "gelu_tanh", save: bool = False, stream=None):
     """y [T, H] = (act(x gate^T) * (x up^T)) down^T, for bf16 or f16 x [T, H],
-    gate, up [I, H], down [H, I]; with save, (y, saved) where saved (bytes, 8 T I
-    of them and padding) is what gated_ffn_backward takes."""
+    gate, up [I, H], down [H, I]; with save, (y, saved) where saved (8 T I bytes and
+    padding) is what gated_ffn_backward takes."""
     f = _ffn_weights(gate, up, down, activation)
     ld = _rows(x, "x", f.H)
     _same("x and the weights", x, gate)
