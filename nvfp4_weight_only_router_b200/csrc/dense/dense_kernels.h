@@ -41,10 +41,10 @@ struct MxPrepArgs {
   int bn;
   uint8_t* wsf;          // [mx_wsf_blocks][chunks][512]
 };
-// 128-row scale blocks of the weight: max(1, bn/128) for each tile
+// 128-row scale blocks of the weight: ceil(bn/128) for each tile
 inline int64_t mx_wsf_blocks(int N, bool gated, int bn) {
   const int tn = gated ? bn / 2 : bn;
-  return (int64_t)((N + tn - 1) / tn) * (bn >= 256 ? 2 : 1);
+  return (int64_t)((N + tn - 1) / tn) * ((bn + 127) / 128);
 }
 cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
 

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qb
   const int64_t ch = w >> 7;
   const int c = (int)(ch % p.sf_chunks);
   const int64_t rb = ch / p.sf_chunks;
-  const int bpt = t.bn >= 256 ? 2 : 1;  // scale blocks per tile
+  const int bpt = (t.bn + 127) / 128;  // scale blocks per tile
   const int tile = (int)(rb / bpt), l = (int)(rb % bpt) * 128 + (wi >> 2) + 32 * (wi & 3);  // row of the tile
   const int half = t.bn / 2;
   const int r = t.gated ? tile * half + l % half : tile * t.bn + l;

@@ -48,16 +48,17 @@ template <int KIND, int BN>
 struct PCfg {
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = BN / 2 * 128;
-  static constexpr int SFB_BLK = BN >= 256 ? 2 : 1;                 // 128-row scale blocks of B
+  static constexpr int SFB_BLK = (BN + 127) / 128;                  // 128-row scale blocks of B
   static constexpr int SFA_BYTES = KIND == kKindMx ? 2 * kSfChunkB : 0;
   static constexpr int SFB_BYTES = KIND == kKindMx ? SFB_BLK * 2 * kSfChunkB : 0;
   static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int NS_RAW = (225 * 1024) / STAGE;
+  static constexpr int SF_COL0 = 2 * BN;                            // behind the two accumulators
+  static constexpr int SF_COLS = KIND == kKindMx ? 8 + 8 * SFB_BLK : 0;  // per stage
+  static constexpr int NS_SMEM = (225 * 1024) / STAGE;
+  static constexpr int NS_TMEM = KIND == kKindMx ? (kPTmem - SF_COL0) / SF_COLS : 8;
+  static constexpr int NS_RAW = NS_SMEM < NS_TMEM ? NS_SMEM : NS_TMEM;
   static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
-  static constexpr int NACC = (KIND == kKindMx && BN == 256) ? 1 : 2;
-  static constexpr int SF_COL0 = NACC * BN;
-  static constexpr int SF_COLS = 8 + 8 * SFB_BLK;                   // per stage
-  static_assert(KIND == kKind16 ? NACC * BN <= kPTmem : SF_COL0 + NS * SF_COLS <= kPTmem, "tensor memory");
+  static_assert(NS >= 3 && SF_COL0 + NS * SF_COLS <= kPTmem, "tensor memory");
 };
 
 template <int KIND, int BN>
@@ -126,12 +127,24 @@ __device__ __forceinline__ void tmem_relinquish2() {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t n) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(n) : "memory");
 }
+// The elect.sync forms are executed by a whole converged warp with uniform
+// operands; one lane issues.
 // into this SM's shared memory, completing on SM 0's barrier
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void expect_tx_elect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes)
       : "memory");
 }
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {  // arrives in both SMs
@@ -165,13 +178,27 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
     if (globaltimer_ns() - t0 > timeout_ns) return false;
   }
 }
-__device__ __forceinline__ void mma16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// The four products of a stage and the commit that frees it, under one
+// election: an election and the moves to uniform registers before each took
+// longer than the products of up to 128 columns.  Descriptors of product k:
+// low words a + k da, b + k db.
+__device__ __forceinline__ void mma16_stage(uint32_t d, uint64_t a, uint32_t da, uint64_t b, uint32_t db,
+                                            uint32_t idesc, bool acc, uint64_t* bar) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b32 al, ah, bl, bh;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %3;\n\t"
+      "add.u32 al, al, %2;\n\tmov.b64 a1, {al, ah};\n\tadd.u32 bl, bl, %4;\n\tmov.b64 b1, {bl, bh};\n\t"
+      "add.u32 al, al, %2;\n\tmov.b64 a2, {al, ah};\n\tadd.u32 bl, bl, %4;\n\tmov.b64 b2, {bl, bh};\n\t"
+      "add.u32 al, al, %2;\n\tmov.b64 a3, {al, ah};\n\tadd.u32 bl, bl, %4;\n\tmov.b64 b3, {bl, bh};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %3, %5, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %5, t;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], %8;\n\t}" ::"r"(
+          d),
+      "l"(a), "r"(da), "l"(b), "r"(db), "r"(idesc), "r"((uint32_t)acc), "r"(smem_u32(bar)), "h"((uint16_t)3)
       : "memory");
 }
 __device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
@@ -183,6 +210,29 @@ __device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, 
       "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
           d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// The four products of a whole MXFP4 stage (32 bytes of K each) and the commit
+// that frees it.  Products 0 and 1 use the first 128 elements' scale columns
+// (bytes 0-1 and 2-3: id0, id1), products 2 and 3 those at sfa + 4, sfb + dsfb.
+__device__ __forceinline__ void mma_mx_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t id0, uint32_t id1,
+                                             uint32_t sfa, uint32_t sfb, uint32_t dsfb, bool acc, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b32 al, ah, bl, bh;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %2;\n\t"
+      "add.u32 al, al, 2;\n\tmov.b64 a1, {al, ah};\n\tadd.u32 bl, bl, 2;\n\tmov.b64 b1, {bl, bh};\n\t"
+      "add.u32 al, al, 2;\n\tmov.b64 a2, {al, ah};\n\tadd.u32 bl, bl, 2;\n\tmov.b64 b2, {bl, bh};\n\t"
+      "add.u32 al, al, 2;\n\tmov.b64 a3, {al, ah};\n\tadd.u32 bl, bl, 2;\n\tmov.b64 b3, {bl, bh};\n\t"
+      "setp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%7], p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, %4, [%5], [%7], t;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, %3, [%6], [%8], t;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, %4, [%6], [%8], t;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%10], %11;\n\t}" ::"r"(
+          d),
+      "l"(a), "l"(b), "r"(id0), "r"(id1), "r"(sfa), "r"(sfa + 4), "r"(sfb), "r"(sfb + dsfb), "r"((uint32_t)acc),
+      "r"(smem_u32(bar)), "h"((uint16_t)3)
       : "memory");
 }
 // a 512-byte scale chunk of each SM's shared memory into its tensor memory
@@ -223,6 +273,14 @@ __device__ __forceinline__ bool pwait(PSmem<KIND, BN>& sm, uint64_t* bar, uint32
 struct PTile {
   int prob, m, n;
 };
+// A stage's barrier (completed by copies and tcgen05.commit, whose data only
+// the asynchronous engines touch), waited for by a whole warp.
+template <int KIND, int BN>
+__device__ __forceinline__ bool swait(PSmem<KIND, BN>& sm, uint64_t* bar, uint32_t parity, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, pwait(sm, bar, parity, status));
+}
+
 template <int NP>
 __device__ __forceinline__ PTile ptile(const PParams<NP>& p, int t) {
   PTile r;
@@ -344,104 +402,141 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 
   if (warp == kPProd) {
     // -------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      uint32_t kiter = 0;
-      bool ok = true;
-      for (int t = cluster; t < p.n_tiles && ok; t += clusters) {
-        const PTile d = ptile<NP>(p, t);
-        const PProb& q = p.p[d.prob];
-        const int arow = d.m * 256 + (int)rank * 128;
-        const int brow = EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
-        for (int kc = 0; kc < q.kc; ++kc, ++kiter) {
-          const int s = kiter % C::NS, use = kiter / C::NS;
-          if (use > 0 && !pwait(sm, &sm.empty[s], (use - 1) & 1, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t bar = leader_addr(&sm.full[s]);
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
-          const int seg = kc >= q.kc0, kk = seg ? kc - q.kc0 : kc;
-          const uint32_t da = smem_u32(sm.a[s]), db = smem_u32(sm.b[s]);
-          if constexpr (KIND == kKind16) {
-            const CUtensorMap* ma = &q.a[seg];
-            const CUtensorMap* mb = &q.b[EPI == kEpiGated ? rank : seg];
-            if (q.a_mn) {
-              tma_load_pair(da, ma, arow, kk * 64, bar);
-              tma_load_pair(da + 8192, ma, arow + 64, kk * 64, bar);
-            } else {
-              tma_load_pair(da, ma, kk * 64, arow, bar);
-            }
-            if (BN >= 128 && q.b_mn) {
-#pragma unroll
-              for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + 8192 * j, mb, brow + 64 * j, kk * 64, bar);
-            } else {
-              tma_load_pair(db, mb, kk * 64, brow, bar);
-            }
+    // The whole warp runs the loop: a loop in one lane cannot keep its
+    // operands in uniform registers, and took 470 to 680 cycles a stage where
+    // the products take 512 (256 columns) or less.
+    const uint32_t full0 = leader_addr(&sm.full[0]), a0 = smem_u32(sm.a[0]), b0 = smem_u32(sm.b[0]);
+    const uint32_t sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
+    uint32_t s = 0, parity = 1;  // the first pass finds every stage free
+    int issued = 0;
+    bool ok = true;
+    for (int t = cluster; t < p.n_tiles && ok; t += clusters) {
+      const PTile d = ptile<NP>(p, t);
+      const PProb& q = p.p[d.prob];
+      const int arow = d.m * 256 + (int)rank * 128;
+      const int brow = EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
+      const int kc_all = q.kc, kc0 = q.kc0;
+      const bool a_mn = KIND == kKind16 && q.a_mn, b_mn = KIND == kKind16 && BN >= 128 && q.b_mn;
+      const CUtensorMap *ma = &q.a[0], *mb = &q.b[EPI == kEpiGated ? rank : 0];
+      for (int kc = 0, kk = 0; kc < kc_all; ++kc, ++kk) {
+        if (kc == kc0) {  // the second segment
+          ma = &q.a[1];
+          mb = &q.b[1];
+          kk = 0;
+        }
+        ok = swait(sm, &sm.empty[s], parity, p.status);
+        if (!ok) break;
+        const uint32_t bar = full0 + 8 * s, da = a0 + s * C::A_BYTES, db = b0 + s * C::B_BYTES;
+        if (rank == 0) expect_tx_elect(bar, 2 * C::STAGE);
+        if constexpr (KIND == kKind16) {
+          if (a_mn) {
+            tma_load_pair(da, ma, arow, kk * 64, bar);
+            tma_load_pair(da + 8192, ma, arow + 64, kk * 64, bar);
           } else {
-            tma_load_pair(da, &q.a[0], kk * 128, arow, bar);
-            tma_load_pair(db, &q.b[EPI == kEpiGated ? rank : 0], kk * 128, brow, bar);
-            tma_load_pair(smem_u32(sm.sfa[s]), &p.sfa, kk * 256, arow >> 7, bar);
-            tma_load_pair(smem_u32(sm.sfb[s]), &p.sfb, kk * 256, d.n * C::SFB_BLK, bar);
+            tma_load_pair(da, ma, kk * 64, arow, bar);
           }
-          sm.issued = (int)kiter + 1;
+          if (b_mn) {
+#pragma unroll
+            for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + 8192 * j, mb, brow + 64 * j, kk * 64, bar);
+          } else {
+            tma_load_pair(db, mb, kk * 64, brow, bar);
+          }
+        } else {
+          tma_load_pair(da, ma, kk * 128, arow, bar);
+          tma_load_pair(db, mb, kk * 128, brow, bar);
+          tma_load_pair(sfa0 + s * C::SFA_BYTES, &p.sfa, kk * 256, arow >> 7, bar);
+          tma_load_pair(sfb0 + s * C::SFB_BYTES, &p.sfb, kk * 256, d.n * C::SFB_BLK, bar);
+        }
+        ++issued;
+        if (++s == C::NS) {
+          s = 0;
+          parity ^= 1;
         }
       }
     }
+    if (lane == 0) sm.issued = issued;
   } else if (warp == kPMma) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
-      uint32_t kiter = 0, titer = 0;
+      const uint32_t a0 = smem_u32(sm.a[0]), b0 = smem_u32(sm.b[0]);
+      uint32_t s = 0, parity = 0, titer = 0;
       bool ok = true;
+      // MXFP4: a stage's scales enter tensor memory one stage ahead of its
+      // products, behind which they would otherwise queue
+      uint32_t cs = 0, cparity = 0;
+      int cleft = 0;
+      auto next_scales = [&]() {
+        if (cleft == 0) return true;
+        if (!swait(sm, &sm.full[cs], cparity, p.status)) return false;
+        tc_fence_after();
+        const uint32_t ta = taddr + (uint32_t)C::SF_COL0 + cs * C::SF_COLS, tb = ta + 8;
+        const uint32_t fa = smem_u32(sm.sfa[0]) + cs * C::SFA_BYTES, fb = smem_u32(sm.sfb[0]) + cs * C::SFB_BYTES;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          cp_sf_pair(ta + 4 * ch, fa + ch * kSfChunkB);
+#pragma unroll
+          for (int bb = 0; bb < C::SFB_BLK; ++bb)
+            cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), fb + (bb * 2 + ch) * kSfChunkB);
+        }
+        --cleft;
+        if (++cs == C::NS) {
+          cs = 0;
+          cparity ^= 1;
+        }
+        return true;
+      };
+      if constexpr (KIND == kKindMx) {
+        if (cluster < p.n_tiles) cleft = ((p.n_tiles - cluster - 1) / clusters + 1) * p.p[0].kc;
+        ok = next_scales();
+      }
       for (int t = cluster; t < p.n_tiles && ok; t += clusters, ++titer) {
         const PTile d = ptile<NP>(p, t);
         const PProb& q = p.p[d.prob];
-        const int db = titer % C::NACC, duse = titer / C::NACC;
-        if (duse > 0) ok = pwait(sm, &sm.d_empty[db], (duse - 1) & 1, p.status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        const int db = titer & 1, duse = titer >> 1;
+        if (duse > 0) ok = __all_sync(0xffffffffu, pwait(sm, &sm.d_empty[db], (duse - 1) & 1, p.status));
         if (!ok) break;
         tc_fence_after();
         const uint32_t dcol = taddr + (uint32_t)(db * BN);
+        const bool a_mn = KIND == kKind16 && q.a_mn, b_mn = KIND == kKind16 && q.b_mn;
+        const int kc_all = q.kc;
         // D fp32 (kind::f16), M = 256, N = BN
         uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
         if (KIND == kKind16) {
           idesc |= 1u << 4;
           if (!p.e.f16) idesc |= (1u << 7) | (1u << 10);
-          idesc |= (uint32_t)q.a_mn << 15 | (uint32_t)q.b_mn << 16;
+          idesc |= (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
         } else {
           idesc |= (1u << 7) | (1u << 10) | (1u << 23);  // E2M1 x E2M1, E8M0 scales
         }
-        const uint32_t astep = KIND == kKind16 && q.a_mn ? 2048u >> 4 : 2u;
-        const uint32_t bstep = KIND == kKind16 && q.b_mn ? 2048u >> 4 : 2u;
-        for (int kc = 0; kc < q.kc; ++kc, ++kiter) {
-          const int s = kiter % C::NS, use = kiter / C::NS;
-          ok = __shfl_sync(0xffffffffu, pwait(sm, &sm.full[s], use & 1, p.status), 0);
+        const uint32_t astep = a_mn ? 2048u >> 4 : 2u, bstep = b_mn ? 2048u >> 4 : 2u;
+        // a stage's descriptor is its first stage's with the address advanced
+        const uint64_t ad0 = a_mn ? make_mn_desc(a0) : make_sw128_desc(a0);
+        const uint64_t bd0 = b_mn ? make_mn_desc(b0) : make_sw128_desc(b0);
+        for (int kc = 0; kc < kc_all; ++kc) {
+          if constexpr (KIND == kKindMx) ok = next_scales();
+          else ok = swait(sm, &sm.full[s], parity, p.status);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = smem_u32(sm.a[s]), sb = smem_u32(sm.b[s]);
-          const uint64_t ad = KIND == kKind16 && q.a_mn ? make_mn_desc(sa) : make_sw128_desc(sa);
-          const uint64_t bd = KIND == kKind16 && q.b_mn ? make_mn_desc(sb) : make_sw128_desc(sb);
+          const uint64_t ad = ad0 + (uint64_t)(s * (C::A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (C::B_BYTES >> 4));
           if constexpr (KIND == kKind16) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma16_pair(dcol, ad + (uint64_t)(kk * astep), bd + (uint64_t)(kk * bstep), idesc, kc > 0 || kk > 0);
+            mma16_stage(dcol, ad, astep, bd, bstep, idesc, kc > 0, &sm.empty[s]);
           } else {
-            const uint32_t ta = taddr + (uint32_t)(C::SF_COL0 + s * C::SF_COLS), tb = ta + 8;
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              cp_sf_pair(ta + 4 * ch, smem_u32(sm.sfa[s]) + ch * kSfChunkB);
-#pragma unroll
-              for (int bb = 0; bb < C::SFB_BLK; ++bb)
-                cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), smem_u32(sm.sfb[s]) + (bb * 2 + ch) * kSfChunkB);
-            }
-            const int nks = min(4, p.e.ksteps - 4 * kc);
-            for (int k = 0; k < nks; ++k) {
-              // steps 2 ch and 2 ch + 1 use scale bytes 0-1 and 2-3 of chunk ch
-              const uint32_t id = idesc | ((uint32_t)(k & 1) * 2u) << 4 | ((uint32_t)(k & 1) * 2u) << 29;
-              mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), id, ta + 4 * (k >> 1),
-                          tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+            const uint32_t ta = taddr + (uint32_t)C::SF_COL0 + s * C::SF_COLS, tb = ta + 8;
+            const uint32_t id1 = idesc | 2u << 4 | 2u << 29;  // scale bytes 2-3
+            const int nks = p.e.ksteps - 4 * kc;
+            if (nks >= 4) {
+              mma_mx_stage(dcol, ad, bd, idesc, id1, ta, tb, 4 * C::SFB_BLK, kc > 0, &sm.empty[s]);
+            } else {  // the last stage of a K that ends inside it
+              for (int k = 0; k < nks; ++k)
+                mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
+                            ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+              commit_pair(&sm.empty[s]);
             }
           }
-          commit_pair(&sm.empty[s]);
+          if (++s == C::NS) {
+            s = 0;
+            parity ^= 1;
+          }
         }
         if (!ok) break;
         commit_pair(&sm.d_full[db]);
@@ -460,7 +555,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       const PTile d = ptile<NP>(p, t);
       const PProb& q = p.p[d.prob];
       const bool wide = q.wide;
-      const int db = titer % C::NACC, duse = titer / C::NACC;
+      const int db = titer & 1, duse = titer >> 1;
       const int row = d.m * 256 + (int)rank * 128 + quarter * 32 + lane;
       const bool rok = row < q.M;
       const size_t base = (size_t)row * q.N;
@@ -482,59 +577,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         const int col0 = half * HU, n0 = d.n * (BN / 2) + col0;
         if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
         tc_fence_after();
-        if constexpr (C::NACC == 1) {
-          // the only accumulator: into registers at once, so that the next
-          // tile's products start before this one's gate is computed
-          float g[HU], u[HU];
 #pragma unroll
-          for (int c = 0; c < HU; c += 32) {
-            tmem_ld32(trow + col0 + c, *reinterpret_cast<float(*)[32]>(g + c));
-            tmem_ld32(trow + BN / 2 + col0 + c, *reinterpret_cast<float(*)[32]>(u + c));
-          }
-          release();
-#pragma unroll
-          for (int c = 0; c < HU; c += 16) 
-            gate16(p.e, q.out, base + n0 + c, n0 + c, N, kept_blk(n0 + c), lane, g + c, u + c, f16, wide);
-        } else {
-#pragma unroll
-          for (int c = 0; c < HU; c += 16) {
-            float g[16], u[16];
-            tmem_ld16(trow + col0 + c, g);
-            tmem_ld16(trow + BN / 2 + col0 + c, u);
-            gate16(p.e, q.out, base + n0 + c, n0 + c, N, kept_blk(n0 + c), lane, g, u, f16, wide);
-          }
-          release();
+        for (int c = 0; c < HU; c += 16) {
+          float g[16], u[16];
+          tmem_ld16(trow + col0 + c, g);
+          tmem_ld16(trow + BN / 2 + col0 + c, u);
+          gate16(p.e, q.out, base + n0 + c, n0 + c, N, kept_blk(n0 + c), lane, g, u, f16, wide);
         }
+        release();
       } else if constexpr (EPI == kEpiPlain) {
         constexpr int HC = BN / 2;
         const int col0 = half * HC, n0 = d.n * BN + col0;
         if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
         tc_fence_after();
-        if constexpr (C::NACC == 1) {
-          float v[HC];
 #pragma unroll
-          for (int c = 0; c < HC; c += 32) tmem_ld32(trow + col0 + c, *reinterpret_cast<float(*)[32]>(v + c));
-          release();
+        for (int c = 0; c < HC; c += 32) {
+          float v[32];
+          tmem_ld32(trow + col0 + c, v);
 #pragma unroll
-          for (int c = 0; c < HC; c += 16) {
+          for (int k = 0; k < 32; k += 16) {
             uint32_t w[8];
-            pack16(v + c, f16, w);
-            store16(q.out, base + n0 + c, n0 + c, N, w, wide);
+            pack16(v + k, f16, w);
+            store16(q.out, base + n0 + c + k, n0 + c + k, N, w, wide);
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < HC; c += 32) {
-            float v[32];
-            tmem_ld32(trow + col0 + c, v);
-#pragma unroll
-            for (int k = 0; k < 32; k += 16) {
-              uint32_t w[8];
-              pack16(v + k, f16, w);
-              store16(q.out, base + n0 + c + k, n0 + c + k, N, w, wide);
-            }
-          }
-          release();
         }
+        release();
       } else {
         // p and a of the first columns are on their way while the products run,
         // and those of the next 32 while 16 are computed
@@ -610,16 +677,31 @@ bool map16(CUtensorMap* m, const PairOperand& o, int rows, int K, int dtype, int
   return encode_tma_2d(m, dt, o.p, K, rows, o.ld * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Relative time of one tile by its column count, from the tensor pipe's share
-// at each width; the width whose whole list takes the fewest tile times wins.
-int pick_bn(int64_t tiles256, int64_t tiles128, int64_t tiles64, int clusters) {
-  auto waves = [&](int64_t t) { return (double)((t + clusters - 1) / clusters); };
-  const double c256 = waves(tiles256) * 1.0, c128 = waves(tiles128) * 0.6, c64 = tiles64 ? waves(tiles64) * 0.4 : 1e30;
-  if (c64 < c128 && c64 < c256) return 64;
-  return c128 < c256 ? 128 : 256;
-}
-
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile widths and the cycles that a stage of each takes.
+struct Widths {
+  int n;
+  int bn[3], cycles[3];
+};
+constexpr Widths kWidths16{3, {256, 128, 64}, {512, 300, 260}};
+constexpr Widths kWidths16Mn{2, {256, 128, 0}, {512, 300, 0}};  // an MN-major box is 64 columns of each SM's half
+constexpr Widths kWidthsMx{3, {192, 128, 64}, {400, 300, 260}};
+
+// The width whose whole list of tiles takes the fewest cycles; tiles(bn) counts them.
+template <typename F>
+int pick_bn(const Widths& w, int clusters, F tiles) {
+  int best = 0;
+  int64_t t = INT64_MAX;
+  for (int i = 0; i < w.n; ++i) {
+    const int64_t c = cdiv(tiles(w.bn[i]), clusters) * w.cycles[i];
+    if (c < t) {
+      t = c;
+      best = w.bn[i];
+    }
+  }
+  return best;
+}
 
 // 32-byte stores of 16-bit rows of N
 bool wide_rows(const void* p, int N) { return N % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0; }
@@ -631,13 +713,14 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
   int sms = 0;
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
-  int64_t tiles[3] = {0, 0, 0};
   bool mn = false;
-  for (int i = 0; i < n; ++i) {
-    for (int b = 0; b < 3; ++b) tiles[b] += cdiv(g[i].M, 256) * cdiv(g[i].N, 256 >> b);
+  for (int i = 0; i < n; ++i)
     for (int s = 0; s < g[i].nseg; ++s) mn |= g[i].seg[s].b.mn;
-  }
-  const int bn = pick_bn(tiles[0], tiles[1], mn ? 0 : tiles[2], sms / 2);
+  const int bn = pick_bn(mn ? kWidths16Mn : kWidths16, sms / 2, [&](int w) {
+    int64_t t = 0;
+    for (int i = 0; i < n; ++i) t += cdiv(g[i].M, 256) * cdiv(g[i].N, w);
+    return t;
+  });
   PParams<kPairMaxProblems> p;
   std::memset(&p, 0, sizeof(p));
   int t0 = 0;
@@ -674,7 +757,7 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   const int64_t tm = cdiv(a.T, 256);
-  const int bn = pick_bn(tm * cdiv(a.I, 128), tm * cdiv(a.I, 64), tm * cdiv(a.I, 32), sms / 2);
+  const int bn = pick_bn(kWidths16, sms / 2, [&](int w) { return tm * cdiv(a.I, w / 2); });
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
@@ -704,7 +787,7 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   const int64_t tm = cdiv(a.T, 256);
-  const int bn = pick_bn(tm * cdiv(a.I, 256), tm * cdiv(a.I, 128), 0, sms / 2);
+  const int bn = pick_bn(kWidths16Mn, sms / 2, [&](int w) { return tm * cdiv(a.I, w); });
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
@@ -732,14 +815,14 @@ int pair_mx_tile(int T, int N, int act) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 148;
   const int64_t tm = cdiv(T, 256), cols = act != kActNone ? 2 * (int64_t)N : N;
-  return pick_bn(tm * cdiv(cols, 256), tm * cdiv(cols, 128), tm * cdiv(cols, 64), sms / 2);
+  return pick_bn(kWidthsMx, sms / 2, [&](int w) { return tm * cdiv(cols, w); });
 }
 
 cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   const bool gated = a.act != kActNone;
   const int bn = a.bn, tn = gated ? bn / 2 : bn;  // output columns per tile
   const int64_t pitch = mx_pitch(a.K), tm = cdiv(a.T, 256), tiles_n = cdiv(a.N, tn);
-  const int chunks = mx_sf_chunks(a.K), blks = bn >= 256 ? 2 : 1;
+  const int chunks = mx_sf_chunks(a.K), blks = (bn + 127) / 128;
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
@@ -768,11 +851,11 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   if (gated) {
     if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, st);
     if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, st);
-    return launch_pair<kKindMx, 256, kEpiGated, 1>(p, st);
+    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, st);
   }
   if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, st);
   if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, st);
-  return launch_pair<kKindMx, 256, kEpiPlain, 1>(p, st);
+  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, st);
 }
 
 }  // namespace nvfp4moe
