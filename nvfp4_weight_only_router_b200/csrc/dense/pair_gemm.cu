@@ -127,31 +127,26 @@ __device__ __forceinline__ void tmem_relinquish2() {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t n) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(n) : "memory");
 }
-// The elect.sync forms are executed by a whole converged warp with uniform
-// operands; one lane issues.
+// One lane of a converged warp.  Copies, products and commits are issued by
+// the branch that it selects, from a loop that the whole warp runs: a loop in
+// one lane (or an election for each instruction) took 470 to 680 cycles a
+// stage where the products take 512 (256 columns) or less.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // into this SM's shared memory, completing on SM 0's barrier
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void expect_tx_elect(uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
-      "r"(bytes)
       : "memory");
 }
 __device__ __forceinline__ void commit_pair(uint64_t* bar) {  // arrives in both SMs
   asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
@@ -178,61 +173,22 @@ __device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uin
     if (globaltimer_ns() - t0 > timeout_ns) return false;
   }
 }
-// The four products of a stage and the commit that frees it, under one
-// election: an election and the moves to uniform registers before each took
-// longer than the products of up to 128 columns.  Descriptors of product k:
-// low words a + k da, b + k db.
-__device__ __forceinline__ void mma16_stage(uint32_t d, uint64_t a, uint32_t da, uint64_t b, uint32_t db,
-                                            uint32_t idesc, bool acc, uint64_t* bar) {
+__device__ __forceinline__ void mma16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e, t;\n\t.reg .b32 al, ah, bl, bh;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %3;\n\t"
-      "add.u32 al, al, %2;\n\tmov.b64 a1, {al, ah};\n\tadd.u32 bl, bl, %4;\n\tmov.b64 b1, {bl, bh};\n\t"
-      "add.u32 al, al, %2;\n\tmov.b64 a2, {al, ah};\n\tadd.u32 bl, bl, %4;\n\tmov.b64 b2, {bl, bh};\n\t"
-      "add.u32 al, al, %2;\n\tmov.b64 a3, {al, ah};\n\tadd.u32 bl, bl, %4;\n\tmov.b64 b3, {bl, bh};\n\t"
-      "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %3, %5, p;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a1, b1, %5, t;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a2, b2, %5, t;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], a3, b3, %5, t;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], %8;\n\t}" ::"r"(
-          d),
-      "l"(a), "r"(da), "l"(b), "r"(db), "r"(idesc), "r"((uint32_t)acc), "r"(smem_u32(bar)), "h"((uint16_t)3)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                             uint32_t sfb, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
+      "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
           d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc), "r"(sfa), "r"(sfb)
-      : "memory");
-}
-// The four products of a whole MXFP4 stage (32 bytes of K each) and the commit
-// that frees it.  Products 0 and 1 use the first 128 elements' scale columns
-// (bytes 0-1 and 2-3: id0, id1), products 2 and 3 those at sfa + 4, sfb + dsfb.
-__device__ __forceinline__ void mma_mx_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t id0, uint32_t id1,
-                                             uint32_t sfa, uint32_t sfb, uint32_t dsfb, bool acc, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred p, e, t;\n\t.reg .b32 al, ah, bl, bh;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-      "mov.b64 {al, ah}, %1;\n\tmov.b64 {bl, bh}, %2;\n\t"
-      "add.u32 al, al, 2;\n\tmov.b64 a1, {al, ah};\n\tadd.u32 bl, bl, 2;\n\tmov.b64 b1, {bl, bh};\n\t"
-      "add.u32 al, al, 2;\n\tmov.b64 a2, {al, ah};\n\tadd.u32 bl, bl, 2;\n\tmov.b64 b2, {bl, bh};\n\t"
-      "add.u32 al, al, 2;\n\tmov.b64 a3, {al, ah};\n\tadd.u32 bl, bl, 2;\n\tmov.b64 b3, {bl, bh};\n\t"
-      "setp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%7], p;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, %4, [%5], [%7], t;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, %3, [%6], [%8], t;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, %4, [%6], [%8], t;\n\t"
-      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%10], %11;\n\t}" ::"r"(
-          d),
-      "l"(a), "l"(b), "r"(id0), "r"(id1), "r"(sfa), "r"(sfa + 4), "r"(sfb), "r"(sfb + dsfb), "r"((uint32_t)acc),
-      "r"(smem_u32(bar)), "h"((uint16_t)3)
       : "memory");
 }
 // a 512-byte scale chunk of each SM's shared memory into its tensor memory
@@ -241,12 +197,7 @@ __device__ __forceinline__ void cp_sf_pair(uint32_t taddr, uint32_t smem_addr) {
   d |= (uint64_t)1u << 16;
   d |= (uint64_t)(128u >> 4) << 32;
   d |= (uint64_t)1u << 46;
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-      "l"(d)
-      : "memory");
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
 // Descriptor of an operand stored with K outermost: boxes of 64 (M or N) x 64
@@ -402,9 +353,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 
   if (warp == kPProd) {
     // -------------------------------------------------------- TMA producer
-    // The whole warp runs the loop: a loop in one lane cannot keep its
-    // operands in uniform registers, and took 470 to 680 cycles a stage where
-    // the products take 512 (256 columns) or less.
     const uint32_t full0 = leader_addr(&sm.full[0]), a0 = smem_u32(sm.a[0]), b0 = smem_u32(sm.b[0]);
     const uint32_t sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
     uint32_t s = 0, parity = 1;  // the first pass finds every stage free
@@ -427,26 +375,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         ok = swait(sm, &sm.empty[s], parity, p.status);
         if (!ok) break;
         const uint32_t bar = full0 + 8 * s, da = a0 + s * C::A_BYTES, db = b0 + s * C::B_BYTES;
-        if (rank == 0) expect_tx_elect(bar, 2 * C::STAGE);
-        if constexpr (KIND == kKind16) {
-          if (a_mn) {
-            tma_load_pair(da, ma, arow, kk * 64, bar);
-            tma_load_pair(da + 8192, ma, arow + 64, kk * 64, bar);
-          } else {
-            tma_load_pair(da, ma, kk * 64, arow, bar);
-          }
-          if (b_mn) {
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
+          if constexpr (KIND == kKind16) {
+            if (a_mn) {
+              tma_load_pair(da, ma, arow, kk * 64, bar);
+              tma_load_pair(da + 8192, ma, arow + 64, kk * 64, bar);
+            } else {
+              tma_load_pair(da, ma, kk * 64, arow, bar);
+            }
+            if (b_mn) {
 #pragma unroll
-            for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + 8192 * j, mb, brow + 64 * j, kk * 64, bar);
+              for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + 8192 * j, mb, brow + 64 * j, kk * 64, bar);
+            } else {
+              tma_load_pair(db, mb, kk * 64, brow, bar);
+            }
           } else {
-            tma_load_pair(db, mb, kk * 64, brow, bar);
+            tma_load_pair(da, ma, kk * 128, arow, bar);
+            tma_load_pair(db, mb, kk * 128, brow, bar);
+            tma_load_pair(sfa0 + s * C::SFA_BYTES, &p.sfa, kk * 256, arow >> 7, bar);
+            tma_load_pair(sfb0 + s * C::SFB_BYTES, &p.sfb, kk * 256, d.n * C::SFB_BLK, bar);
           }
-        } else {
-          tma_load_pair(da, ma, kk * 128, arow, bar);
-          tma_load_pair(db, mb, kk * 128, brow, bar);
-          tma_load_pair(sfa0 + s * C::SFA_BYTES, &p.sfa, kk * 256, arow >> 7, bar);
-          tma_load_pair(sfb0 + s * C::SFB_BYTES, &p.sfb, kk * 256, d.n * C::SFB_BLK, bar);
         }
+        __syncwarp();
         ++issued;
         if (++s == C::NS) {
           s = 0;
@@ -464,13 +415,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       // MXFP4: a stage's scales enter tensor memory one stage ahead of its
       // products, behind which they would otherwise queue
       uint32_t cs = 0, cparity = 0;
-      int cleft = 0;
-      auto next_scales = [&]() {
-        if (cleft == 0) return true;
-        if (!swait(sm, &sm.full[cs], cparity, p.status)) return false;
-        tc_fence_after();
-        const uint32_t ta = taddr + (uint32_t)C::SF_COL0 + cs * C::SF_COLS, tb = ta + 8;
-        const uint32_t fa = smem_u32(sm.sfa[0]) + cs * C::SFA_BYTES, fb = smem_u32(sm.sfb[0]) + cs * C::SFB_BYTES;
+      int cleft = 0;  // stages whose scales are still to come
+      const uint32_t sf0 = taddr + (uint32_t)C::SF_COL0, sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
+      auto copy_scales = [&]() {  // stage cs, one lane
+        const uint32_t ta = sf0 + cs * C::SF_COLS, tb = ta + 8;
+        const uint32_t fa = sfa0 + cs * C::SFA_BYTES, fb = sfb0 + cs * C::SFB_BYTES;
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           cp_sf_pair(ta + 4 * ch, fa + ch * kSfChunkB);
@@ -478,16 +427,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           for (int bb = 0; bb < C::SFB_BLK; ++bb)
             cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), fb + (bb * 2 + ch) * kSfChunkB);
         }
+      };
+      auto next_scales = [&]() {
         --cleft;
         if (++cs == C::NS) {
           cs = 0;
           cparity ^= 1;
         }
-        return true;
       };
       if constexpr (KIND == kKindMx) {
-        if (cluster < p.n_tiles) cleft = ((p.n_tiles - cluster - 1) / clusters + 1) * p.p[0].kc;
-        ok = next_scales();
+        if (cluster < p.n_tiles) {
+          cleft = ((p.n_tiles - cluster - 1) / clusters + 1) * p.p[0].kc;
+          ok = swait(sm, &sm.full[0], 0, p.status);
+          if (ok) {
+            tc_fence_after();
+            if (elect_one()) copy_scales();
+            __syncwarp();
+            next_scales();
+          }
+        }
       }
       for (int t = cluster; t < p.n_tiles && ok; t += clusters, ++titer) {
         const PTile d = ptile<NP>(p, t);
@@ -513,36 +471,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         const uint64_t ad0 = a_mn ? make_mn_desc(a0) : make_sw128_desc(a0);
         const uint64_t bd0 = b_mn ? make_mn_desc(b0) : make_sw128_desc(b0);
         for (int kc = 0; kc < kc_all; ++kc) {
-          if constexpr (KIND == kKindMx) ok = next_scales();
-          else ok = swait(sm, &sm.full[s], parity, p.status);
+          if (KIND == kKind16) ok = swait(sm, &sm.full[s], parity, p.status);
+          else if (cleft > 0) ok = swait(sm, &sm.full[cs], cparity, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t ad = ad0 + (uint64_t)(s * (C::A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (C::B_BYTES >> 4));
-          if constexpr (KIND == kKind16) {
-            mma16_stage(dcol, ad, astep, bd, bstep, idesc, kc > 0, &sm.empty[s]);
-          } else {
-            const uint32_t ta = taddr + (uint32_t)C::SF_COL0 + s * C::SF_COLS, tb = ta + 8;
-            const uint32_t id1 = idesc | 2u << 4 | 2u << 29;  // scale bytes 2-3
-            const int nks = p.e.ksteps - 4 * kc;
-            if (nks >= 4) {
-              mma_mx_stage(dcol, ad, bd, idesc, id1, ta, tb, 4 * C::SFB_BLK, kc > 0, &sm.empty[s]);
-            } else {  // the last stage of a K that ends inside it
-              for (int k = 0; k < nks; ++k)
-                mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
-                            ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
-              commit_pair(&sm.empty[s]);
+          if (elect_one()) {
+            if constexpr (KIND == kKind16) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma16_pair(dcol, ad + (uint64_t)(k * astep), bd + (uint64_t)(k * bstep), idesc, kc > 0 || k > 0);
+            } else {
+              if (cleft > 0) copy_scales();
+              const uint32_t ta = sf0 + s * C::SF_COLS, tb = ta + 8;
+              const int nks = p.e.ksteps - 4 * kc;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                // steps 2 ch and 2 ch + 1 use scale bytes 0-1 and 2-3 of chunk ch
+                if (k < nks)
+                  mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k),
+                              k & 1 ? idesc | 2u << 4 | 2u << 29 : idesc, ta + 4 * (k >> 1),
+                              tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+              }
             }
+            commit_pair(&sm.empty[s]);
+            if (kc == kc_all - 1) commit_pair(&sm.d_full[db]);
           }
+          __syncwarp();
+          if (KIND == kKindMx && cleft > 0) next_scales();
           if (++s == C::NS) {
             s = 0;
             parity ^= 1;
           }
         }
         if (!ok) break;
-        commit_pair(&sm.d_full[db]);
       }
       // every MMA issued has completed before the tear-down
-      commit_pair(&sm.fin);
+      if (elect_one()) commit_pair(&sm.fin);
+      __syncwarp();
       wait_cluster(&sm.fin, 0);
       __syncwarp();
     }
