@@ -22,12 +22,12 @@
 //   gated backward   the accumulators are dh; the epilogue reads p and a and
 //           writes dg = dh p and du = dh a, so dh never leaves the chip.
 //
-// Warps: 0 TMA producer (in both SMs), 1 MMA issuer (in SM 0 of the pair; the
-// whole warp runs the loop and one elected lane issues), 4-11 epilogue: a warp
-// per tensor-memory lane quarter and column half.  With two accumulators a
-// tile's epilogue overlaps the next tile's products; the 256-column MXFP4 tile
-// has one (scales need the other columns).  Every wait is bounded in wall
-// time; one that gives up records a timeout and the pair tears down.
+// Warps: 0 and 2 TMA producers of A and B (in both SMs), 1 MMA issuer (in SM 0
+// of the pair), 4-11 epilogue: a warp per tensor-memory lane quarter and column
+// half.  Two accumulators, so that a tile's epilogue overlaps the next tile's
+// products (MXFP4 tiles have at most 192 columns: scales need tensor memory
+// too).  Every wait is bounded in wall time; one that gives up records a timeout
+// and the pair tears down.
 #include <algorithm>
 #include <cstring>
 
@@ -39,7 +39,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kPThreads = 384;
-constexpr int kPProd = 0, kPMma = 1, kPEpi0 = 4, kPEpiWarps = 8;
+constexpr int kPProdA = 0, kPMma = 1, kPProdB = 2, kPEpi0 = 4, kPEpiWarps = 8;
 constexpr int kPTmem = 512;
 constexpr int kKind16 = 0, kKindMx = 1;
 constexpr int kEpiPlain = 0, kEpiGated = 1, kEpiGatedBwd = 2;
@@ -73,7 +73,7 @@ struct alignas(1024) PSmem {
   uint64_t fin;
   uint32_t taddr;
   int abort_flag;
-  int issued;
+  int issued[2];           // stages of A and of B copied
 };
 
 struct alignas(64) PProb {
@@ -338,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
     mbar_init(&sm.fin, 1);
     sm.abort_flag = 0;
-    sm.issued = 0;
+    sm.issued[0] = sm.issued[1] = 0;
     fence_mbar_init();
   }
   if (warp == kPMma) {
@@ -351,50 +351,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   tc_fence_after();
   const uint32_t taddr = sm.taddr;
 
-  if (warp == kPProd) {
-    // -------------------------------------------------------- TMA producer
-    const uint32_t full0 = leader_addr(&sm.full[0]), a0 = smem_u32(sm.a[0]), b0 = smem_u32(sm.b[0]);
-    const uint32_t sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
+  if (warp == kPProdA || warp == kPProdB) {
+    // ------------------------------------------- TMA producers of A and of B
+    const bool is_a = warp == kPProdA;
+    const uint32_t full0 = leader_addr(&sm.full[0]), op0 = smem_u32(is_a ? sm.a[0] : sm.b[0]);
+    const uint32_t sf0 = smem_u32(is_a ? sm.sfa[0] : sm.sfb[0]);
     uint32_t s = 0, parity = 1;  // the first pass finds every stage free
     int issued = 0;
     bool ok = true;
     for (int t = cluster; t < p.n_tiles && ok; t += clusters) {
       const PTile d = ptile<NP>(p, t);
       const PProb& q = p.p[d.prob];
-      const int arow = d.m * 256 + (int)rank * 128;
-      const int brow = EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
       const int kc_all = q.kc, kc0 = q.kc0;
-      const bool a_mn = KIND == kKind16 && q.a_mn, b_mn = KIND == kKind16 && BN >= 128 && q.b_mn;
-      const CUtensorMap *ma = &q.a[0], *mb = &q.b[EPI == kEpiGated ? rank : 0];
+      // first row (M or N) of this SM's part, and of its scales
+      const int row = is_a ? d.m * 256 + (int)rank * 128
+                           : EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
+      const int sf_row = is_a ? row >> 7 : d.n * C::SFB_BLK;
+      const bool mn = KIND == kKind16 && (is_a ? q.a_mn : BN >= 128 && q.b_mn);
+      const int boxes = is_a ? 2 : BN / 128;  // 64-row boxes of an operand with K outermost
+      const CUtensorMap* map = is_a ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0];
       for (int kc = 0, kk = 0; kc < kc_all; ++kc, ++kk) {
         if (kc == kc0) {  // the second segment
-          ma = &q.a[1];
-          mb = &q.b[1];
+          map = is_a ? &q.a[1] : &q.b[1];
           kk = 0;
         }
         ok = swait(sm, &sm.empty[s], parity, p.status);
         if (!ok) break;
-        const uint32_t bar = full0 + 8 * s, da = a0 + s * C::A_BYTES, db = b0 + s * C::B_BYTES;
+        const uint32_t bar = full0 + 8 * s, dst = op0 + s * (is_a ? C::A_BYTES : C::B_BYTES);
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
+          if (is_a && rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
           if constexpr (KIND == kKind16) {
-            if (a_mn) {
-              tma_load_pair(da, ma, arow, kk * 64, bar);
-              tma_load_pair(da + 8192, ma, arow + 64, kk * 64, bar);
+            if (mn) {
+              tma_load_pair(dst, map, row, kk * 64, bar);
+              if (boxes > 1) tma_load_pair(dst + 8192, map, row + 64, kk * 64, bar);
             } else {
-              tma_load_pair(da, ma, kk * 64, arow, bar);
-            }
-            if (b_mn) {
-#pragma unroll
-              for (int j = 0; j < BN / 128; ++j) tma_load_pair(db + 8192 * j, mb, brow + 64 * j, kk * 64, bar);
-            } else {
-              tma_load_pair(db, mb, kk * 64, brow, bar);
+              tma_load_pair(dst, map, kk * 64, row, bar);
             }
           } else {
-            tma_load_pair(da, ma, kk * 128, arow, bar);
-            tma_load_pair(db, mb, kk * 128, brow, bar);
-            tma_load_pair(sfa0 + s * C::SFA_BYTES, &p.sfa, kk * 256, arow >> 7, bar);
-            tma_load_pair(sfb0 + s * C::SFB_BYTES, &p.sfb, kk * 256, d.n * C::SFB_BLK, bar);
+            tma_load_pair(dst, map, kk * 128, row, bar);
+            tma_load_pair(sf0 + s * (is_a ? C::SFA_BYTES : C::SFB_BYTES), is_a ? &p.sfa : &p.sfb, kk * 256, sf_row, bar);
           }
         }
         __syncwarp();
@@ -405,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         }
       }
     }
-    if (lane == 0) sm.issued = issued;
+    if (lane == 0) sm.issued[is_a ? 0 : 1] = issued;
   } else if (warp == kPMma) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
@@ -484,14 +479,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             } else {
               if (cleft > 0) copy_scales();
               const uint32_t ta = sf0 + s * C::SF_COLS, tb = ta + 8;
+              const uint32_t id1 = idesc | 2u << 4 | 2u << 29;  // scale bytes 2-3 of a chunk
               const int nks = p.e.ksteps - 4 * kc;
+              if (nks >= 4) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                // steps 2 ch and 2 ch + 1 use scale bytes 0-1 and 2-3 of chunk ch
-                if (k < nks)
-                  mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k),
-                              k & 1 ? idesc | 2u << 4 | 2u << 29 : idesc, ta + 4 * (k >> 1),
-                              tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+                for (int k = 0; k < 4; ++k)
+                  mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
+                              ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+              } else {  // K ends inside the stage
+                for (int k = 0; k < nks; ++k)
+                  mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
+                              ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
               }
             }
             commit_pair(&sm.empty[s]);
@@ -609,7 +607,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   __syncthreads();
   if (threadIdx.x == 0 && sm.abort_flag) {
     // copies in flight land before the pair leaves (SM 1's complete on SM 0's barriers)
-    for (int it = max(0, sm.issued - C::NS); it < sm.issued; ++it)
+    const int issued = max(sm.issued[0], sm.issued[1]);
+    for (int it = max(0, issued - C::NS); it < issued; ++it)
       wait_cluster(&sm.full[it % C::NS], (it / C::NS) & 1, kAbortDrainNs);
   }
   __syncthreads();
