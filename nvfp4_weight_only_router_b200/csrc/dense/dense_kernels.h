@@ -49,10 +49,7 @@ inline int64_t mx_wsf_blocks(int N, bool gated, int bn) {
 cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- skinny.cu
-#ifndef SK_MAX
-#define SK_MAX 32
-#endif
-constexpr int kSkinnyMaxTokens = SK_MAX;
+constexpr int kSkinnyMaxTokens = 32;
 struct SkinnyArgs {
   const void* x;      // [T, K]
   int64_t ldx;        // elements
@@ -89,7 +86,8 @@ struct PairGemm {
 };
 constexpr int kPairMaxProblems = 4;
 // plain products, one launch for all (at most kPairMaxProblems); out = sum over segments A B^T
-cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st);
+// `after`: an operand is written by the kernel launched just before on the stream
+cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, int* status, cudaStream_t st);
 // What the forward pass keeps for the backward one: h [T, I], and p = u act'(g)
 // and a = act(g) in 24 bits, in blocks of 32 rows x 16 hidden units (row blocks
 // outermost, edges padded) as an epilogue warp holds them, a row per lane:
@@ -115,6 +113,7 @@ struct PairGated {
   void* h;
   bool keep;       // kept.h == h
   PairKept kept;
+  bool after_producer;  // as SkinnyArgs
 };
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st);
 // dh = dy down with dg = dh p, du = dh a written in its place
@@ -128,7 +127,8 @@ struct PairGatedBwd {
   void *dg, *du;
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
-// MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns)
+// MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns);
+// launched just behind launch_mxfp4_prep_a4
 struct PairMx {
   const uint8_t *xq, *xsf, *wq, *wsf;
   int T, N, K;

@@ -188,6 +188,7 @@ struct TileScales {
 // scales of 4 blocks of one row).
 template <typename T, int ALIGN>
 __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qblocks, TileScales t) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product sets up meanwhile
   if ((int64_t)blockIdx.x < qblocks) {
     quant_cta<T, ALIGN, true>(p, blockIdx.x);
     return;
@@ -221,6 +222,7 @@ template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t rows,
                                                                int64_t K, T* __restrict__ out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a product may set up meanwhile
   const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * kDGroups;
   const uint32_t gpr = (uint32_t)(K / 8);
   const int64_t r0 = first / gpr;

@@ -41,54 +41,55 @@ namespace {
 constexpr int kPThreads = 384;
 constexpr int kPProdA = 0, kPMma = 1, kPProdB = 2, kPEpi0 = 4, kPEpiWarps = 8;
 constexpr int kPTmem = 512;
+constexpr int kPOutB = 4096;  // output buffer of an epilogue warp: 32 rows x 64 columns
 constexpr int kKind16 = 0, kKindMx = 1;
 constexpr int kEpiPlain = 0, kEpiGated = 1, kEpiGatedBwd = 2;
 
 template <int KIND, int BN>
 struct PCfg {
-  static constexpr int A_BYTES = 128 * 128;
-  static constexpr int B_BYTES = BN / 2 * 128;
+  // sub-stages of 128 bytes of K per stage: a stage's waits and commits take
+  // about 320 cycles, more than the products of 64 x up to 128 columns
+  static constexpr int KS = BN <= 128 ? 2 : 1;
+  static constexpr int A_SUB = 128 * 128, B_SUB = BN / 2 * 128;
   static constexpr int SFB_BLK = (BN + 127) / 128;                  // 128-row scale blocks of B
-  static constexpr int SFA_BYTES = KIND == kKindMx ? 2 * kSfChunkB : 0;
-  static constexpr int SFB_BYTES = KIND == kKindMx ? SFB_BLK * 2 * kSfChunkB : 0;
-  static constexpr int STAGE = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int SFA_SUB = KIND == kKindMx ? 2 * kSfChunkB : 0;
+  static constexpr int SFB_SUB = KIND == kKindMx ? SFB_BLK * 2 * kSfChunkB : 0;
+  static constexpr int STAGE = KS * (A_SUB + B_SUB + SFA_SUB + SFB_SUB);
   static constexpr int SF_COL0 = 2 * BN;                            // behind the two accumulators
-  static constexpr int SF_COLS = KIND == kKindMx ? 8 + 8 * SFB_BLK : 0;  // per stage
-  static constexpr int NS_SMEM = (225 * 1024) / STAGE;
-  static constexpr int NS_TMEM = KIND == kKindMx ? (kPTmem - SF_COL0) / SF_COLS : 8;
-  static constexpr int NS_RAW = NS_SMEM < NS_TMEM ? NS_SMEM : NS_TMEM;
-  static constexpr int NS = NS_RAW > 8 ? 8 : NS_RAW;
-  static_assert(NS >= 3 && SF_COL0 + NS * SF_COLS <= kPTmem, "tensor memory");
+  static constexpr int SF_COLS = KIND == kKindMx ? 8 + 8 * SFB_BLK : 0;  // per sub-stage
+  static constexpr int NS_SMEM = (225 * 1024 - kPEpiWarps * kPOutB) / STAGE;
+  static constexpr int NS_TMEM = KIND == kKindMx ? (kPTmem - SF_COL0) / (KS * SF_COLS) : 8;
+  static constexpr int NS = NS_SMEM < NS_TMEM ? NS_SMEM : NS_TMEM;
+  static_assert(NS >= 3 && SF_COL0 + NS * KS * SF_COLS <= kPTmem, "tensor memory");
 };
 
 template <int KIND, int BN>
 struct alignas(1024) PSmem {
   using C = PCfg<KIND, BN>;
-  uint8_t a[C::NS][C::A_BYTES];
-  uint8_t b[C::NS][C::B_BYTES];
-  uint8_t sfa[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::SFA_BYTES : 16];
-  uint8_t sfb[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::SFB_BYTES : 16];
+  uint8_t a[C::NS][C::KS][C::A_SUB];
+  uint8_t b[C::NS][C::KS][C::B_SUB];
+  uint8_t out[kPEpiWarps][kPOutB];     // output on its way to global memory
+  uint8_t sfa[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::KS * C::SFA_SUB : 16];
+  uint8_t sfb[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::KS * C::SFB_SUB : 16];
   uint64_t full[C::NS], empty[C::NS];  // full: SM 0's barrier counts both SMs' bytes
   uint64_t d_full[2], d_empty[2];      // d_empty: SM 0's, arrivals of both SMs' epilogues
   uint64_t fin;
   uint32_t taddr;
   int abort_flag;
-  int issued[2];           // stages of A and of B copied
+  int issued[2];                       // stages of A and of B copied
 };
 
 struct alignas(64) PProb {
   CUtensorMap a[2], b[2];  // by K segment; gated: b[0] gate rows, b[1] up rows
-  void* out;
+  CUtensorMap o[2];        // output; gated backward: dg, du
   int M, N;                // output rows and columns
   int kc0, kc;             // K stages of segment 0 and in all
   int tm, t0;              // tiles along M; first tile in the list
   int a_mn, b_mn;
-  int wide;                // rows of the outputs are 32-byte aligned
 };
 
 struct PEpi {
   uint8_t* kept;           // PairKept's blocks (null: not kept)
-  uint8_t *dg, *du;        // backward
   int act, f16;
   int ksteps;              // MXFP4: MMA steps of 64 along K
 };
@@ -245,17 +246,47 @@ __device__ __forceinline__ PTile ptile(const PParams<NP>& p, int t) {
   return r;
 }
 
-// 16 consecutive columns n.. of a row of N (N a multiple of 8): 32 or 16 bytes
-// at element offset `at`, the part past N left alone.
-__device__ __forceinline__ void store16(void* base, size_t at, int n, int N, const uint32_t (&w)[8], bool wide) {
-  uint16_t* p = static_cast<uint16_t*>(base) + at;
-  if (wide) {
-    if (n < N) st_v8(p, w);  // N is a multiple of 16
-    return;
+// ---- output.  A lane holds columns of one row; 32-byte stores of 32 rows are
+// 32 lines an instruction (6500 cycles for a 256 x 256 tile, exposed behind the
+// last one), so a warp lays CW columns of its rows out in shared memory, in the
+// swizzle that keeps both sides free of conflicts, and a TMA store writes them
+// as whole lines and leaves what lies past the edges alone.
+template <int CW>
+struct POut {
+  static constexpr int BYTES = 32 * CW * 2, BUFS = kPOutB / BYTES;
+  static constexpr CUtensorMapSwizzle SW = CW == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                           : CW == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
+  // 16 columns (group g of CW / 16) of row `lane`
+  static __device__ __forceinline__ void put(uint8_t* buf, int lane, int g, const uint32_t (&w)[8]) {
+    const int x = CW == 64 ? lane & 7 : CW == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
+    uint8_t* r = buf + lane * (CW * 2);
+    *reinterpret_cast<uint4*>(r + ((2 * g) ^ x) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(r + ((2 * g + 1) ^ x) * 16) = make_uint4(w[4], w[5], w[6], w[7]);
   }
-  if (n < N) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (n + 8 < N) *reinterpret_cast<uint4*>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+};
+// at most `left` of the warp's earlier stores still read their buffers
+template <int LEFT>
+__device__ __forceinline__ void out_reuse(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+  __syncwarp();
 }
+__device__ __forceinline__ void out_ready() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const uint8_t* buf, int n, int row) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(n), "r"(row), "r"(smem_u32(buf))
+               : "memory");
+}
+__device__ __forceinline__ void out_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // p and a of 16 hidden units of one row
 struct Kept16 {
   uint32_t ph[8], ah[8], pl[4], al[4];
@@ -280,12 +311,11 @@ __device__ __forceinline__ void pack16(const float* v, bool f16, uint32_t (&w)[8
   for (int i = 0; i < 8; ++i) w[i] = pack16x2(v[2 * i], v[2 * i + 1], f16);
 }
 
-// Epilogue of 16 hidden units of a row: h, and p and a where kept (blk, null
-// where the warp's rows or the units lie outside).
-__device__ __forceinline__ void gate16(const PEpi& e, void* out, size_t at, int n, int N, uint8_t* blk, int lane,
-                                       const float* g, const float* u, bool f16, bool wide) {
+// Epilogue of 16 hidden units of a row: h packed into w, and p and a written
+// where kept (blk, null where the warp's rows or the units lie outside).
+__device__ __forceinline__ void gate16(const PEpi& e, uint8_t* blk, int lane, const float* g, const float* u, bool f16,
+                                       uint32_t (&w)[8]) {
   float v[16];
-  uint32_t w[8];
   if (!e.kept) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = act_fwd(g[i], e.act) * u[i];
@@ -313,7 +343,6 @@ __device__ __forceinline__ void gate16(const PEpi& e, void* out, size_t at, int 
     for (int i = 0; i < 16; ++i) v[i] *= u[i];
   }
   pack16(v, f16, w);
-  store16(out, at, n, N, w, wide);
 }
 
 template <int KIND, int BN, int EPI, int NP>
@@ -326,6 +355,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // The first tile's description and descriptors are fetched while the pair
+  // sets up: cold, they took 3300 cycles behind it.
+  PTile tile = ptile<NP>(p, cluster);
+  if (warp == kPProdA || warp == kPProdB) {
+    const PProb& q = p.p[tile.prob];
+    if (elect_one()) {
+      prefetch_map(warp == kPProdA ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0]);
+      if (KIND == kKindMx) prefetch_map(warp == kPProdA ? &p.sfa : &p.sfb);
+    }
+    __syncwarp();
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
@@ -350,17 +392,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t taddr = sm.taddr;
+  // behind the kernel before, whose results are the operands
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == kPProdA || warp == kPProdB) {
     // ------------------------------------------- TMA producers of A and of B
     const bool is_a = warp == kPProdA;
-    const uint32_t full0 = leader_addr(&sm.full[0]), op0 = smem_u32(is_a ? sm.a[0] : sm.b[0]);
+    const uint32_t full0 = leader_addr(&sm.full[0]), op0 = smem_u32(is_a ? sm.a[0][0] : sm.b[0][0]);
     const uint32_t sf0 = smem_u32(is_a ? sm.sfa[0] : sm.sfb[0]);
     uint32_t s = 0, parity = 1;  // the first pass finds every stage free
     int issued = 0;
     bool ok = true;
     for (int t = cluster; t < p.n_tiles && ok; t += clusters) {
-      const PTile d = ptile<NP>(p, t);
+      if (t != cluster) tile = ptile<NP>(p, t);
+      const PTile d = tile;
       const PProb& q = p.p[d.prob];
       const int kc_all = q.kc, kc0 = q.kc0;
       // first row (M or N) of this SM's part, and of its scales
@@ -370,26 +415,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       const bool mn = KIND == kKind16 && (is_a ? q.a_mn : BN >= 128 && q.b_mn);
       const int boxes = is_a ? 2 : BN / 128;  // 64-row boxes of an operand with K outermost
       const CUtensorMap* map = is_a ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0];
-      for (int kc = 0, kk = 0; kc < kc_all; ++kc, ++kk) {
+      for (int kc = 0, kk = 0; kc < kc_all; ++kc, kk += C::KS) {
         if (kc == kc0) {  // the second segment
           map = is_a ? &q.a[1] : &q.b[1];
           kk = 0;
         }
         ok = swait(sm, &sm.empty[s], parity, p.status);
         if (!ok) break;
-        const uint32_t bar = full0 + 8 * s, dst = op0 + s * (is_a ? C::A_BYTES : C::B_BYTES);
+        const uint32_t bar = full0 + 8 * s;
         if (elect_one()) {
           if (is_a && rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
-          if constexpr (KIND == kKind16) {
-            if (mn) {
-              tma_load_pair(dst, map, row, kk * 64, bar);
-              if (boxes > 1) tma_load_pair(dst + 8192, map, row + 64, kk * 64, bar);
+#pragma unroll
+          for (int u = 0; u < C::KS; ++u) {
+            const uint32_t dst = op0 + (s * C::KS + u) * (is_a ? C::A_SUB : C::B_SUB);
+            if constexpr (KIND == kKind16) {
+              if (mn) {
+                tma_load_pair(dst, map, row, (kk + u) * 64, bar);
+                if (boxes > 1) tma_load_pair(dst + 8192, map, row + 64, (kk + u) * 64, bar);
+              } else {
+                tma_load_pair(dst, map, (kk + u) * 64, row, bar);
+              }
             } else {
-              tma_load_pair(dst, map, kk * 64, row, bar);
+              tma_load_pair(dst, map, (kk + u) * 128, row, bar);
+              tma_load_pair(sf0 + (s * C::KS + u) * (is_a ? C::SFA_SUB : C::SFB_SUB), is_a ? &p.sfa : &p.sfb,
+                            (kk + u) * 256, sf_row, bar);
             }
-          } else {
-            tma_load_pair(dst, map, kk * 128, row, bar);
-            tma_load_pair(sf0 + s * (is_a ? C::SFA_BYTES : C::SFB_BYTES), is_a ? &p.sfa : &p.sfb, kk * 256, sf_row, bar);
           }
         }
         __syncwarp();
@@ -404,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   } else if (warp == kPMma) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
-      const uint32_t a0 = smem_u32(sm.a[0]), b0 = smem_u32(sm.b[0]);
+      const uint32_t a0 = smem_u32(sm.a[0][0]), b0 = smem_u32(sm.b[0][0]);
       uint32_t s = 0, parity = 0, titer = 0;
       bool ok = true;
       // MXFP4: a stage's scales enter tensor memory one stage ahead of its
@@ -413,14 +463,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       int cleft = 0;  // stages whose scales are still to come
       const uint32_t sf0 = taddr + (uint32_t)C::SF_COL0, sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
       auto copy_scales = [&]() {  // stage cs, one lane
-        const uint32_t ta = sf0 + cs * C::SF_COLS, tb = ta + 8;
-        const uint32_t fa = sfa0 + cs * C::SFA_BYTES, fb = sfb0 + cs * C::SFB_BYTES;
 #pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
-          cp_sf_pair(ta + 4 * ch, fa + ch * kSfChunkB);
+        for (int u = 0; u < C::KS; ++u) {
+          const uint32_t ta = sf0 + (cs * C::KS + u) * C::SF_COLS, tb = ta + 8;
+          const uint32_t fa = sfa0 + (cs * C::KS + u) * C::SFA_SUB, fb = sfb0 + (cs * C::KS + u) * C::SFB_SUB;
 #pragma unroll
-          for (int bb = 0; bb < C::SFB_BLK; ++bb)
-            cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), fb + (bb * 2 + ch) * kSfChunkB);
+          for (int ch = 0; ch < 2; ++ch) {
+            cp_sf_pair(ta + 4 * ch, fa + ch * kSfChunkB);
+#pragma unroll
+            for (int bb = 0; bb < C::SFB_BLK; ++bb)
+              cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), fb + (bb * 2 + ch) * kSfChunkB);
+          }
         }
       };
       auto next_scales = [&]() {
@@ -443,8 +496,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         }
       }
       for (int t = cluster; t < p.n_tiles && ok; t += clusters, ++titer) {
-        const PTile d = ptile<NP>(p, t);
-        const PProb& q = p.p[d.prob];
+        if (t != cluster) tile = ptile<NP>(p, t);
+        const PProb& q = p.p[tile.prob];
         const int db = titer & 1, duse = titer >> 1;
         if (duse > 0) ok = __all_sync(0xffffffffu, pwait(sm, &sm.d_empty[db], (duse - 1) & 1, p.status));
         if (!ok) break;
@@ -470,26 +523,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           else if (cleft > 0) ok = swait(sm, &sm.full[cs], cparity, p.status);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t ad = ad0 + (uint64_t)(s * (C::A_BYTES >> 4)), bd = bd0 + (uint64_t)(s * (C::B_BYTES >> 4));
           if (elect_one()) {
-            if constexpr (KIND == kKind16) {
+            if (KIND == kKindMx && cleft > 0) copy_scales();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma16_pair(dcol, ad + (uint64_t)(k * astep), bd + (uint64_t)(k * bstep), idesc, kc > 0 || k > 0);
-            } else {
-              if (cleft > 0) copy_scales();
-              const uint32_t ta = sf0 + s * C::SF_COLS, tb = ta + 8;
-              const uint32_t id1 = idesc | 2u << 4 | 2u << 29;  // scale bytes 2-3 of a chunk
-              const int nks = p.e.ksteps - 4 * kc;
-              if (nks >= 4) {
+            for (int u = 0; u < C::KS; ++u) {
+              const uint64_t ad = ad0 + (uint64_t)((s * C::KS + u) * (C::A_SUB >> 4));
+              const uint64_t bd = bd0 + (uint64_t)((s * C::KS + u) * (C::B_SUB >> 4));
+              if constexpr (KIND == kKind16) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
-                              ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
-              } else {  // K ends inside the stage
-                for (int k = 0; k < nks; ++k)
-                  mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
-                              ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || k > 0);
+                  mma16_pair(dcol, ad + (uint64_t)(k * astep), bd + (uint64_t)(k * bstep), idesc,
+                             kc > 0 || u > 0 || k > 0);
+              } else {
+                const uint32_t ta = sf0 + (s * C::KS + u) * C::SF_COLS, tb = ta + 8;
+                const uint32_t id1 = idesc | 2u << 4 | 2u << 29;  // scale bytes 2-3 of a chunk
+                const int nks = p.e.ksteps - 4 * (kc * C::KS + u);
+                if (nks >= 4) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
+                                ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || u > 0 || k > 0);
+                } else {  // K ends inside the sub-stage
+                  for (int k = 0; k < nks; ++k)
+                    mma_mx_pair(dcol, ad + (uint64_t)(2 * k), bd + (uint64_t)(2 * k), k & 1 ? id1 : idesc,
+                                ta + 4 * (k >> 1), tb + 4 * C::SFB_BLK * (k >> 1), kc > 0 || u > 0 || k > 0);
+                }
               }
             }
             commit_pair(&sm.empty[s]);
@@ -512,94 +570,91 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     }
   } else if (warp >= kPEpi0) {
     // ------------------------------------------------------------ epilogue
+    constexpr int HC = EPI == kEpiGated ? BN / 4 : BN / 2;  // output columns of this warp
+    constexpr int CW = EPI == kEpiGatedBwd ? 32 : HC % 64 == 0 ? 64 : HC % 32 == 0 ? 32 : 16;
+    using Out = POut<CW>;
+    // backward: dg and du side by side
+    constexpr int BUFS = EPI == kEpiGatedBwd ? Out::BUFS / 2 : Out::BUFS;
     const int ew = warp - kPEpi0, quarter = warp & 3, half = ew >> 2;
     const bool f16 = p.e.f16;
-    uint32_t titer = 0;
+    uint32_t titer = 0, chunk = 0;
     for (int t = cluster; t < p.n_tiles; t += clusters, ++titer) {
-      const PTile d = ptile<NP>(p, t);
+      if (t != cluster) tile = ptile<NP>(p, t);
+      const PTile d = tile;
       const PProb& q = p.p[d.prob];
-      const bool wide = q.wide;
+      const int M = q.M, N = q.N;
       const int db = titer & 1, duse = titer >> 1;
-      const int row = d.m * 256 + (int)rank * 128 + quarter * 32 + lane;
-      const bool rok = row < q.M;
-      const size_t base = (size_t)row * q.N;
-      const uint32_t trow = taddr + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(db * BN);
-      const int N = rok ? q.N : 0;  // a row past M has no columns
+      const int row0 = d.m * 256 + (int)rank * 128 + quarter * 32;
+      const int col0 = half * HC, n0 = d.n * (EPI == kEpiGated ? BN / 2 : BN) + col0;
+      const uint32_t tcol = taddr + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(db * BN + col0);
       // the kept block of this warp's rows and hidden units n..n + 15, null outside
-      const int row_blk = (row - lane) >> 5, blks = (q.N + 15) >> 4;
+      const int blks = (N + 15) >> 4;
       auto kept_blk = [&](int n) {
-        return EPI != kEpiPlain && row - lane < q.M && n < q.N
-                   ? p.e.kept + ((size_t)row_blk * blks + (n >> 4)) * kKeptBlockB : nullptr;
+        return row0 < M && n < N ? p.e.kept + ((size_t)(row0 >> 5) * blks + (n >> 4)) * kKeptBlockB : nullptr;
       };
-      auto release = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(leader_addr(&sm.d_empty[db]));
+      constexpr int AHEAD = 2;
+      Kept16 kept16[EPI == kEpiGatedBwd ? AHEAD + 1 : 1];
+      auto fetch = [&](int c) {
+        const uint8_t* blk = kept_blk(n0 + c);
+        if (blk) kept_load(blk, lane, kept16[(c / 16) % (AHEAD + 1)]);  // else: unused
       };
-      if constexpr (EPI == kEpiGated) {
-        constexpr int HU = BN / 4;  // hidden units of this warp
-        const int col0 = half * HU, n0 = d.n * (BN / 2) + col0;
-        if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < HU; c += 16) {
-          float g[16], u[16];
-          tmem_ld16(trow + col0 + c, g);
-          tmem_ld16(trow + BN / 2 + col0 + c, u);
-          gate16(p.e, q.out, base + n0 + c, n0 + c, N, kept_blk(n0 + c), lane, g, u, f16, wide);
-        }
-        release();
-      } else if constexpr (EPI == kEpiPlain) {
-        constexpr int HC = BN / 2;
-        const int col0 = half * HC, n0 = d.n * BN + col0;
-        if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < HC; c += 32) {
-          float v[32];
-          tmem_ld32(trow + col0 + c, v);
-#pragma unroll
-          for (int k = 0; k < 32; k += 16) {
-            uint32_t w[8];
-            pack16(v + k, f16, w);
-            store16(q.out, base + n0 + c + k, n0 + c + k, N, w, wide);
-          }
-        }
-        release();
-      } else {
-        // p and a of the first columns are on their way while the products run,
-        // and those of the next 32 while 16 are computed
-        constexpr int HC = BN / 2;
-        const int col0 = half * HC, n0 = d.n * BN + col0;
-        constexpr int AHEAD = 2;
-        Kept16 k[AHEAD + 1];
-        auto fetch = [&](int c) {
-          const uint8_t* blk = kept_blk(n0 + c);
-          if (blk) kept_load(blk, lane, k[(c / 16) % (AHEAD + 1)]);  // else: unused
-        };
+      // backward: p and a of the first columns are on their way while the
+      // products run, and those of the next 32 while 16 are computed
+      if constexpr (EPI == kEpiGatedBwd) {
 #pragma unroll
         for (int c = 0; c < 16 * AHEAD; c += 16) fetch(c);
-        if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
-        tc_fence_after();
+      }
+      if (!pwait(sm, &sm.d_full[db], duse & 1, p.status)) break;
+      tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < HC; c += 16) {
-          if (c + 16 * AHEAD < HC) fetch(c + 16 * AHEAD);
-          const Kept16& r = k[(c / 16) % (AHEAD + 1)];
-          float v[16], o[16];
-          tmem_ld16(trow + col0 + c, v);
+      for (int c = 0; c < HC; c += CW) {
+        uint8_t* buf = sm.out[ew] + (chunk++ % BUFS) * (kPOutB / BUFS);
+        out_reuse<BUFS - 1>(lane);
+#pragma unroll
+        for (int k = 0; k < CW; k += 16) {
           uint32_t w[8];
+          if constexpr (EPI == kEpiGated) {
+            float g[16], u[16];
+            tmem_ld16(tcol + c + k, g);
+            tmem_ld16(tcol + BN / 2 + c + k, u);
+            gate16(p.e, p.e.kept ? kept_blk(n0 + c + k) : nullptr, lane, g, u, f16, w);
+          } else if constexpr (EPI == kEpiPlain) {
+            float v[16];
+            tmem_ld16(tcol + c + k, v);
+            pack16(v, f16, w);
+          } else {
+            if (c + k + 16 * AHEAD < HC) fetch(c + k + 16 * AHEAD);
+            const Kept16& r = kept16[((c + k) / 16) % (AHEAD + 1)];
+            float v[16], o[16];
+            tmem_ld16(tcol + c + k, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = v[i] * kept(r.ph[(i / 4) * 2], r.ph[(i / 4) * 2 + 1], r.pl[i / 4], i & 3);
-          pack16(o, f16, w);
-          store16(p.e.dg, base + n0 + c, n0 + c, N, w, wide);
+            for (int i = 0; i < 16; ++i)
+              o[i] = v[i] * kept(r.ah[(i / 4) * 2], r.ah[(i / 4) * 2 + 1], r.al[i / 4], i & 3);
+            pack16(o, f16, w);
+            Out::put(buf + Out::BYTES, lane, k / 16, w);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = v[i] * kept(r.ah[(i / 4) * 2], r.ah[(i / 4) * 2 + 1], r.al[i / 4], i & 3);
-          pack16(o, f16, w);
-          store16(p.e.du, base + n0 + c, n0 + c, N, w, wide);
+            for (int i = 0; i < 16; ++i)
+              o[i] = v[i] * kept(r.ph[(i / 4) * 2], r.ph[(i / 4) * 2 + 1], r.pl[i / 4], i & 3);
+            pack16(o, f16, w);
+          }
+          Out::put(buf, lane, k / 16, w);
         }
-        release();
+        if (c + CW == HC) {  // all read: the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(leader_addr(&sm.d_empty[db]));
+        }
+        out_ready();
+        if (lane == 0) {
+          if (row0 < M && n0 + c < N) {
+            tma_store(&q.o[0], buf, n0 + c, row0);
+            if (EPI == kEpiGatedBwd) tma_store(&q.o[1], buf + Out::BYTES, n0 + c, row0);
+          }
+          out_commit();
+        }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   // ------------------------------------------------------------- tear-down
@@ -621,8 +676,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 }
 
 // ---------------------------------------------------------------------- host
+template <int EPI, int BN>
+constexpr int out_cols() {  // columns of an output box, as in the kernel
+  return EPI == kEpiGatedBwd ? 32 : (EPI == kEpiGated ? BN / 4 : BN / 2) % 64 == 0 ? 64
+                                : (EPI == kEpiGated ? BN / 4 : BN / 2) % 32 == 0   ? 32 : 16;
+}
+// [M, N] 16-bit output, boxes of 32 rows
+template <int EPI, int BN>
+bool map_out(CUtensorMap* m, void* out, int M, int N) {
+  constexpr int CW = out_cols<EPI, BN>();
+  return encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, out, N, M, (uint64_t)N * 2, CW, 32, POut<CW>::SW);
+}
+
+// `after`: behind the kernel launched just before on the stream, whose tail this
+// one's set-up may overlap
 template <int KIND, int BN, int EPI, int NP>
-cudaError_t launch_pair(const PParams<NP>& p, cudaStream_t st) {
+cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, bool after, cudaStream_t st) {
+  for (int i = 0; i < p.np; ++i)
+    if (!map_out<EPI, BN>(&p.p[i].o[0], out[i], p.p[i].M, p.p[i].N)) return cudaErrorInvalidValue;
+  if (EPI == kEpiGatedBwd && !map_out<EPI, BN>(&p.p[0].o[1], out1, p.p[0].M, p.p[0].N)) return cudaErrorInvalidValue;
   constexpr int smem = (int)sizeof(PSmem<KIND, BN>) + 1024;
   static_assert(smem <= 232448, "shared memory budget");
   auto fn = pair_gemm_kernel<KIND, BN, EPI, NP>;
@@ -632,8 +704,17 @@ cudaError_t launch_pair(const PParams<NP>& p, cudaStream_t st) {
   err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   const int clusters = std::max(1, std::min(p.n_tiles, sms / 2));
-  fn<<<2 * clusters, kPThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, p);
 }
 
 bool map16(CUtensorMap* m, const PairOperand& o, int rows, int K, int dtype, int box_rows) {
@@ -668,12 +749,12 @@ int pick_bn(const Widths& w, int clusters, F tiles) {
   return best;
 }
 
-// 32-byte stores of 16-bit rows of N
-bool wide_rows(const void* p, int N) { return N % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 32 == 0; }
+// stages of a K of `subs` sub-stages
+int stages(int64_t subs, int bn) { return (int)(bn <= 128 ? cdiv(subs, 2) : subs); }
 
 }  // namespace
 
-cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st) {
+cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, int* status, cudaStream_t st) {
   if (n < 1 || n > kPairMaxProblems) return cudaErrorInvalidValue;
   int sms = 0;
   cudaError_t err = sm_count(&sms);
@@ -688,6 +769,7 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
   });
   PParams<kPairMaxProblems> p;
   std::memset(&p, 0, sizeof(p));
+  void* out[kPairMaxProblems] = {};
   int t0 = 0;
   for (int i = 0; i < n; ++i) {
     PProb& q = p.p[i];
@@ -696,12 +778,11 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
       if (!map16(&q.a[s], sg.a, g[i].M, sg.K, dtype, 128) || !map16(&q.b[s], sg.b, g[i].N, sg.K, dtype, bn / 2))
         return cudaErrorInvalidValue;
     }
-    q.out = g[i].out;
+    out[i] = g[i].out;
     q.M = g[i].M;
     q.N = g[i].N;
-    q.wide = wide_rows(q.out, q.N);
-    q.kc0 = (int)cdiv(g[i].seg[0].K, 64);
-    q.kc = q.kc0 + (g[i].nseg > 1 ? (int)cdiv(g[i].seg[1].K, 64) : 0);
+    q.kc0 = stages(cdiv(g[i].seg[0].K, 64), bn);
+    q.kc = q.kc0 + (g[i].nseg > 1 ? stages(cdiv(g[i].seg[1].K, 64), bn) : 0);
     q.tm = (int)cdiv(q.M, 256);
     q.t0 = t0;
     q.a_mn = g[i].seg[0].a.mn;
@@ -712,9 +793,9 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
   p.np = n;
   p.n_tiles = t0;
   p.status = status;
-  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, st);
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, st);
-  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, st);
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, out, nullptr, after, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, out, nullptr, after, st);
+  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, out, nullptr, after, st);
 }
 
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) {
@@ -730,11 +811,9 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   if (!map16(&q.a[0], x, a.T, a.K, a.dtype, 128) || !map16(&q.b[0], wg, a.I, a.K, a.dtype, bn / 2) ||
       !map16(&q.b[1], wu, a.I, a.K, a.dtype, bn / 2))
     return cudaErrorInvalidValue;
-  q.out = a.h;
   q.M = a.T;
   q.N = a.I;
-  q.wide = wide_rows(a.h, a.I);
-  q.kc0 = q.kc = (int)cdiv(a.K, 64);
+  q.kc0 = q.kc = stages(cdiv(a.K, 64), bn);
   q.tm = (int)tm;
   if (a.keep) p.e.kept = a.kept.blocks;
   p.e.act = a.act;
@@ -742,9 +821,9 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn / 2));
   p.status = status;
-  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, st);
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, st);
-  return launch_pair<kKind16, 256, kEpiGated, 1>(p, st);
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, {a.h}, nullptr, a.after_producer, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, {a.h}, nullptr, a.after_producer, st);
+  return launch_pair<kKind16, 256, kEpiGated, 1>(p, {a.h}, nullptr, a.after_producer, st);
 }
 
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st) {
@@ -761,19 +840,16 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
     return cudaErrorInvalidValue;
   q.M = a.T;
   q.N = a.I;
-  q.kc0 = q.kc = (int)cdiv(a.H, 64);
+  q.kc0 = q.kc = stages(cdiv(a.H, 64), bn);
   q.tm = (int)tm;
   q.b_mn = 1;
-  q.wide = wide_rows(a.dg, a.I);
   p.e.kept = a.kept.blocks;
-  p.e.dg = static_cast<uint8_t*>(a.dg);
-  p.e.du = static_cast<uint8_t*>(a.du);
   p.e.f16 = a.dtype == kF16;
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn));
   p.status = status;
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, st);
-  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, {a.dg}, a.du, false, st);
+  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, false, st);
 }
 
 int pair_mx_tile(int T, int N, int act) {
@@ -801,11 +877,9 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
       !encode_tma_2d(&p.sfb, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.wsf, (uint64_t)chunks * 128, tiles_n * blks,
                      (uint64_t)chunks * kSfChunkB, 256, blks, ns))
     return cudaErrorInvalidValue;
-  q.out = a.y;
   q.M = a.T;
   q.N = a.N;
-  q.wide = wide_rows(a.y, a.N);
-  q.kc0 = q.kc = (int)cdiv(a.K, 256);
+  q.kc0 = q.kc = stages(cdiv(a.K, 256), bn);
   q.tm = (int)tm;
   p.e.act = a.act;
   p.e.f16 = a.dtype == kF16;
@@ -814,13 +888,13 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   p.n_tiles = (int)(tm * tiles_n);
   p.status = status;
   if (gated) {
-    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, st);
-    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, st);
-    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, st);
+    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, {a.y}, nullptr, true, st);
+    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, {a.y}, nullptr, true, st);
+    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, {a.y}, nullptr, true, st);
   }
-  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, st);
-  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, st);
-  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, st);
+  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, {a.y}, nullptr, true, st);
+  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, {a.y}, nullptr, true, st);
+  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, {a.y}, nullptr, true, st);
 }
 
 }  // namespace nvfp4moe
