@@ -1,6 +1,7 @@
 """Build the in-tree shared libraries libnvfp4moe.so (csrc/*.cu) and
 libnvfp4dense.so (csrc/dense/*.cu and the host helpers it shares) for sm_100a
-with nvcc.
+with nvcc, and _dense_calls.so (csrc/dense/torch_calls.cpp), torch's calls of
+the latter, with the host compiler.
 
     python -m nvfp4_weight_only_router_b200.build [--force] [--verbose]
 
@@ -23,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libnvfp4moe.so")
 DENSE_LIB = os.path.join(PKG, "libnvfp4dense.so")
+DENSE_CALLS = os.path.join(PKG, "_dense_calls.so")
 DENSE_SHARED = ("host_util", "tma_map")  # csrc/*.cu that the dense library links too
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -50,10 +52,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     dense = {src: _object(src, "dense_") for src in sorted(glob.glob(os.path.join(CSRC, "dense", "*.cu")))}
     stale = [(src, obj) for src, obj in {**main, **dense}.items()
              if force or not os.path.exists(obj) or os.path.getmtime(obj) < max(os.path.getmtime(src), hdr_mtime)]
+    calls = os.path.join(CSRC, "dense", "torch_calls.cpp")
+    calls_obj = os.path.join(BUILD, "dense_torch_calls.o")
+    abi = max(os.path.getmtime(f) for f in [calls] + glob.glob(os.path.join(ROOT, "include", "*.h")))
     with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+        host = None
+        if force or not os.path.exists(calls_obj) or os.path.getmtime(calls_obj) < abi:
+            host = pool.submit(_compile_calls, calls, calls_obj, verbose)
         list(pool.map(lambda so: _compile(*so, flags, verbose), stale))
+        if host is not None:
+            host.result()
     _link(LIB, list(main.values()), force, verbose)
     _link(DENSE_LIB, list(dense.values()) + [_object(os.path.join(CSRC, n + ".cu")) for n in DENSE_SHARED], force, verbose)
+    if force or not os.path.exists(DENSE_CALLS) or os.path.getmtime(calls_obj) > os.path.getmtime(DENSE_CALLS):
+        _link_calls(calls_obj, verbose)
     return LIB
 
 
@@ -76,6 +88,31 @@ def _link(lib: str, objs: list[str], force: bool, verbose: bool) -> None:
         tmp = lib + ".tmp"
         _run([nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs, verbose)
         os.replace(tmp, lib)
+
+
+def _compile_calls(src: str, obj: str, verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = cpp_extension.include_paths("cuda") + [sysconfig.get_paths()["include"], _cuda_include()]
+    _run(["g++", "-O2", "-std=c++20", "-fPIC", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_dense_calls",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] +
+         ["-isystem" + i for i in inc] + ["-c", src, "-o", obj], verbose)
+
+
+def _cuda_include() -> str:
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+
+
+def _link_calls(obj: str, verbose: bool) -> None:
+    from torch.utils import cpp_extension
+    tmp = DENSE_CALLS + ".tmp"
+    libs = cpp_extension.library_paths()
+    # libnvfp4dense.so is found next to the module
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(DENSE_LIB), "-Wl,-rpath,$ORIGIN"] +
+         ["-L" + p for p in libs] + ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"], verbose)
+    os.replace(tmp, DENSE_CALLS)
 
 
 if __name__ == "__main__":
