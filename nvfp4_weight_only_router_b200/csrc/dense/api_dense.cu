@@ -73,16 +73,20 @@ nvfp4_status check_linear(int32_t T, const mxfp4_weight* w, int32_t act) {
   return NVFP4_OK;
 }
 
+bool few_tokens(int32_t T, const mxfp4_weight* w, int32_t act, bool a4) {
+  return skinny_fits(T, act ? w->N / 2 : w->N, act != kActNone, true, a4);
+}
+
 // W4A16 above the few-token kernel: the weight as bf16
-size_t linear_bytes(int32_t T, const mxfp4_weight* w) {
-  return T <= kSkinnyMaxTokens ? 256 : round_up((size_t)w->N * w->K * 2, 256);
+size_t linear_bytes(int32_t T, const mxfp4_weight* w, int32_t act) {
+  return few_tokens(T, w, act, false) ? 256 : round_up((size_t)w->N * w->K * 2, 256);
 }
 
 LinearLayout a4_layout(int32_t T, const mxfp4_weight* w, int32_t act) {
   LinearLayout L;
-  if (T <= kSkinnyMaxTokens) return L;
+  if (few_tokens(T, w, act, true)) return L;
   const int n = act ? w->N / 2 : w->N;
-  L.bn = pair_mx_tile(T, n, act);
+  L.bn = pair_mx_tile(T, n, w->K, act);
   const size_t chunks = (size_t)mx_sf_chunks(w->K) * kSfChunkB;
   L.xsf = round_up((size_t)T * mx_pitch(w->K), 256);
   L.wsf = L.xsf + (size_t)((T + 127) / 128) * chunks;
@@ -190,7 +194,7 @@ nvfp4_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64
 
 // ---------------------------------------------------------------- products
 size_t mxfp4_linear_workspace_bytes(int32_t T, const mxfp4_weight* w, int32_t act) {
-  return check_linear(T, w, act) == NVFP4_OK ? linear_bytes(T, w) : 0;
+  return check_linear(T, w, act) == NVFP4_OK ? linear_bytes(T, w, act) : 0;
 }
 
 nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, const mxfp4_weight* w, int32_t act,
@@ -198,11 +202,11 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
   NvtxRange nv("mxfp4_linear");
   nvfp4_status st = check_linear(T, w, act);
   if (st != NVFP4_OK) return st;
-  st = linear_checks(x, dtype, ldx, T, w, y, ws, ws_bytes, linear_bytes(T, w), false);
+  st = linear_checks(x, dtype, ldx, T, w, y, ws, ws_bytes, linear_bytes(T, w, act), false);
   if (st != NVFP4_OK || T == 0) return st;
   if (T == 1) ldx = w->K;
   cudaStream_t s = as_stream(stream);
-  if (T <= kSkinnyMaxTokens) return cuda_status(launch_skinny(skinny_mx(x, ldx, T, w, act, dtype, y, false), s));
+  if (few_tokens(T, w, act, false)) return cuda_status(launch_skinny(skinny_mx(x, ldx, T, w, act, dtype, y, false), s));
   cudaError_t e = launch_mxfp4_dequantize(w->codes, w->scales, w->N, w->K, ws, kBf16, s);
   if (e != cudaSuccess) return cuda_fail(e);
   if (act) {
@@ -244,7 +248,7 @@ nvfp4_status mxfp4_linear_a4(const void* x, int32_t dtype, int64_t ldx, int32_t 
   if (st != NVFP4_OK || T == 0) return st;
   if (T == 1) ldx = w->K;
   cudaStream_t s = as_stream(stream);
-  if (T <= kSkinnyMaxTokens) return cuda_status(launch_skinny(skinny_mx(x, ldx, T, w, act, dtype, y, true), s));
+  if (few_tokens(T, w, act, true)) return cuda_status(launch_skinny(skinny_mx(x, ldx, T, w, act, dtype, y, true), s));
   uint8_t* base = static_cast<uint8_t*>(ws);
   MxPrepArgs pa{};
   pa.x = x;
@@ -300,50 +304,56 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   if (T == 0) return NVFP4_OK;
   if (T == 1) ldx = f->H;
   cudaStream_t s = as_stream(stream);
-  if (!saved && T <= kSkinnyMaxTokens) {
+  int* status = device_status_ptr();
+  void* const h = saved ? saved : ws;
+  cudaError_t e;
+  if (!saved && skinny_fits(T, f->I, true, false, false)) {
     SkinnyArgs a{};
     a.x = x;
     a.ldx = ldx;
     a.w0 = f->gate;
     a.w1 = f->up;
-    a.y = ws;
+    a.y = h;
     a.T = T;
     a.N = f->I;
     a.K = f->H;
     a.act = f->act;
     a.dtype = f->dtype;
-    cudaError_t e = launch_skinny(a, s);
-    if (e != cudaSuccess) return cuda_fail(e);
-    a.x = ws;
+    e = launch_skinny(a, s);
+  } else {
+    PairGated a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.gate = f->gate;
+    a.up = f->up;
+    a.ldw = f->H;
+    a.T = T;
+    a.I = f->I;
+    a.K = f->H;
+    a.act = f->act;
+    a.dtype = f->dtype;
+    a.h = h;
+    a.keep = saved != nullptr;
+    a.kept = pair_kept(saved, T, f->I);
+    e = launch_pair_gated(a, status, s);
+  }
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (skinny_fits(T, f->H, false, false, false)) {
+    SkinnyArgs a{};
+    a.x = h;
     a.ldx = f->I;
     a.w0 = f->down;
-    a.w1 = nullptr;
     a.y = y;
+    a.T = T;
     a.N = f->H;
     a.K = f->I;
     a.act = kActNone;
+    a.dtype = f->dtype;
     a.after_producer = true;
     return cuda_status(launch_skinny(a, s));
   }
-  PairGated a{};
-  a.x = x;
-  a.ldx = ldx;
-  a.gate = f->gate;
-  a.up = f->up;
-  a.ldw = f->H;
-  a.T = T;
-  a.I = f->I;
-  a.K = f->H;
-  a.act = f->act;
-  a.dtype = f->dtype;
-  a.keep = saved != nullptr;
-  a.kept = pair_kept(saved, T, f->I);
-  a.h = saved ? saved : ws;
-  int* status = device_status_ptr();
-  cudaError_t e = launch_pair_gated(a, status, s);
-  if (e != cudaSuccess) return cuda_fail(e);
   PairGemm g{};
-  g.seg[0] = PairSegment{rows_of(a.h, f->I), rows_of(f->down, f->I), f->I};
+  g.seg[0] = PairSegment{rows_of(h, f->I), rows_of(f->down, f->I), f->I};
   g.nseg = 1;
   g.M = T;
   g.N = f->H;

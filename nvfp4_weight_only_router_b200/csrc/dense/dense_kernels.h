@@ -49,7 +49,8 @@ inline int64_t mx_wsf_blocks(int N, bool gated, int bn) {
 cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- skinny.cu
-constexpr int kSkinnyMaxTokens = 32;
+// whether launch_skinny is the faster kernel for a product (N: output columns)
+bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x);
 struct SkinnyArgs {
   const void* x;      // [T, K]
   int64_t ldx;        // elements
@@ -135,7 +136,7 @@ struct PairMx {
   int act, dtype, bn;  // bn: pair_mx_tile of the same product
   void* y;
 };
-int pair_mx_tile(int T, int N, int act);
+int pair_mx_tile(int T, int N, int K, int act);
 cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st);
 
 }  // namespace nvfp4moe

@@ -86,6 +86,7 @@ struct alignas(64) PProb {
   int kc0, kc;             // K stages of segment 0 and in all
   int tm, t0;              // tiles along M; first tile in the list
   int a_mn, b_mn;
+  int tx;                  // bytes of a stage that complete on the barrier, of both SMs
 };
 
 struct PEpi {
@@ -407,7 +408,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       if (t != cluster) tile = ptile<NP>(p, t);
       const PTile d = tile;
       const PProb& q = p.p[d.prob];
-      const int kc_all = q.kc, kc0 = q.kc0;
+      const int kc_all = q.kc, kc0 = q.kc0, tx = q.tx;
+      // SM 1 has no rows of A where M ends in SM 0: what its shared memory holds
+      // in their place only reaches accumulator rows that are not stored
+      const bool has = !is_a || rank == 0 || q.M > 128;
       // first row (M or N) of this SM's part, and of its scales
       const int row = is_a ? d.m * 256 + (int)rank * 128
                            : EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
@@ -424,9 +428,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         if (!ok) break;
         const uint32_t bar = full0 + 8 * s;
         if (elect_one()) {
-          if (is_a && rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::STAGE);
+          if (is_a && rank == 0) mbar_arrive_expect_tx(&sm.full[s], tx);
 #pragma unroll
           for (int u = 0; u < C::KS; ++u) {
+            if (!has) break;
             const uint32_t dst = op0 + (s * C::KS + u) * (is_a ? C::A_SUB : C::B_SUB);
             if constexpr (KIND == kKind16) {
               if (mn) {
@@ -654,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         }
       }
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    out_reuse<0>(lane);  // the buffers outlive the stores' reads
   }
 
   // ------------------------------------------------------------- tear-down
@@ -672,10 +677,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     tc_fence_after();
     tmem_dealloc2(taddr, kPTmem);
   }
-  cluster_sync();
 }
 
 // ---------------------------------------------------------------------- host
+// rows of a box of A: a box's time goes by its rows, those past M included
+int a_box(int M) { return M >= 128 ? 128 : (M + 7) / 8 * 8; }
+
 template <int EPI, int BN>
 constexpr int out_cols() {  // columns of an output box, as in the kernel
   return EPI == kEpiGatedBwd ? 32 : (EPI == kEpiGated ? BN / 4 : BN / 2) % 64 == 0 ? 64
@@ -692,8 +699,13 @@ bool map_out(CUtensorMap* m, void* out, int M, int N) {
 // one's set-up may overlap
 template <int KIND, int BN, int EPI, int NP>
 cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, bool after, cudaStream_t st) {
-  for (int i = 0; i < p.np; ++i)
-    if (!map_out<EPI, BN>(&p.p[i].o[0], out[i], p.p[i].M, p.p[i].N)) return cudaErrorInvalidValue;
+  using C = PCfg<KIND, BN>;
+  for (int i = 0; i < p.np; ++i) {
+    PProb& q = p.p[i];
+    if (!map_out<EPI, BN>(&q.o[0], out[i], q.M, q.N)) return cudaErrorInvalidValue;
+    const int a = q.a_mn ? C::A_SUB : a_box(q.M) * 128;
+    q.tx = C::KS * ((q.M > 128 ? 2 : 1) * (a + C::SFA_SUB) + 2 * (C::B_SUB + C::SFB_SUB));
+  }
   if (EPI == kEpiGatedBwd && !map_out<EPI, BN>(&p.p[0].o[1], out1, p.p[0].M, p.p[0].N)) return cudaErrorInvalidValue;
   constexpr int smem = (int)sizeof(PSmem<KIND, BN>) + 1024;
   static_assert(smem <= 232448, "shared memory budget");
@@ -725,25 +737,39 @@ bool map16(CUtensorMap* m, const PairOperand& o, int rows, int K, int dtype, int
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile widths and the cycles that a stage of each takes.
-struct Widths {
-  int n;
-  int bn[3], cycles[3];
+// The tile width of a list of problems: the one whose busiest cluster is done
+// first.  Clusters take every `clusters`-th tile; a sub-stage (128 bytes of K)
+// takes `cycles`, and behind the last tile comes its epilogue.
+struct Width {
+  int bn, cycles, tail;
 };
-constexpr Widths kWidths16{3, {256, 128, 64}, {512, 300, 260}};
-constexpr Widths kWidths16Mn{2, {256, 128, 0}, {512, 300, 0}};  // an MN-major box is 64 columns of each SM's half
-constexpr Widths kWidthsMx{3, {192, 128, 64}, {400, 300, 260}};
-
-// The width whose whole list of tiles takes the fewest cycles; tiles(bn) counts them.
-template <typename F>
-int pick_bn(const Widths& w, int clusters, F tiles) {
+constexpr Width kWidths16[] = {{256, 512, 3000}, {128, 290, 2000}, {64, 200, 1500}};
+constexpr Width kWidths16Mn[] = {{256, 540, 3000}, {128, 430, 2000}};  // an MN-major box is 64 columns of each SM's half
+constexpr Width kWidthsMx[] = {{192, 560, 3000}, {128, 480, 2000}, {64, 400, 1500}};
+struct Tiles {
+  int64_t m, cols, subs;  // tiles along M, columns, sub-stages along K
+};
+template <int NW>
+int pick_bn(const Width (&widths)[NW], const Tiles* g, int n, int clusters) {
   int best = 0;
-  int64_t t = INT64_MAX;
-  for (int i = 0; i < w.n; ++i) {
-    const int64_t c = cdiv(tiles(w.bn[i]), clusters) * w.cycles[i];
-    if (c < t) {
-      t = c;
-      best = w.bn[i];
+  int64_t least = INT64_MAX;
+  for (const Width& w : widths) {
+    int64_t worst = 0;
+    for (int c = 0; c < clusters; ++c) {
+      int64_t t0 = 0, cycles = 0;
+      for (int i = 0; i < n; ++i) {
+        const int64_t t1 = t0 + g[i].m * cdiv(g[i].cols, w.bn);
+        // multiples of `clusters` plus c in [t0, t1)
+        const int64_t tiles = (t1 + clusters - 1 - c) / clusters - (t0 + clusters - 1 - c) / clusters;
+        const int64_t subs = w.bn <= 128 ? cdiv(g[i].subs, 2) * 2 : g[i].subs;
+        cycles += tiles * subs * w.cycles;
+        t0 = t1;
+      }
+      worst = std::max(worst, cycles);
+    }
+    if (worst + w.tail < least) {
+      least = worst + w.tail;
+      best = w.bn;
     }
   }
   return best;
@@ -762,11 +788,12 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, in
   bool mn = false;
   for (int i = 0; i < n; ++i)
     for (int s = 0; s < g[i].nseg; ++s) mn |= g[i].seg[s].b.mn;
-  const int bn = pick_bn(mn ? kWidths16Mn : kWidths16, sms / 2, [&](int w) {
-    int64_t t = 0;
-    for (int i = 0; i < n; ++i) t += cdiv(g[i].M, 256) * cdiv(g[i].N, w);
-    return t;
-  });
+  Tiles tiles[kPairMaxProblems];
+  for (int i = 0; i < n; ++i) {
+    tiles[i] = Tiles{cdiv(g[i].M, 256), g[i].N, 0};
+    for (int s = 0; s < g[i].nseg; ++s) tiles[i].subs += cdiv(g[i].seg[s].K, 64);
+  }
+  const int bn = mn ? pick_bn(kWidths16Mn, tiles, n, sms / 2) : pick_bn(kWidths16, tiles, n, sms / 2);
   PParams<kPairMaxProblems> p;
   std::memset(&p, 0, sizeof(p));
   void* out[kPairMaxProblems] = {};
@@ -775,7 +802,7 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, in
     PProb& q = p.p[i];
     for (int s = 0; s < 2; ++s) {
       const PairSegment& sg = g[i].seg[s < g[i].nseg ? s : 0];
-      if (!map16(&q.a[s], sg.a, g[i].M, sg.K, dtype, 128) || !map16(&q.b[s], sg.b, g[i].N, sg.K, dtype, bn / 2))
+      if (!map16(&q.a[s], sg.a, g[i].M, sg.K, dtype, a_box(g[i].M)) || !map16(&q.b[s], sg.b, g[i].N, sg.K, dtype, bn / 2))
         return cudaErrorInvalidValue;
     }
     out[i] = g[i].out;
@@ -803,12 +830,13 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   const int64_t tm = cdiv(a.T, 256);
-  const int bn = pick_bn(kWidths16, sms / 2, [&](int w) { return tm * cdiv(a.I, w / 2); });
+  const Tiles tiles{tm, 2 * (int64_t)a.I, cdiv(a.K, 64)};
+  const int bn = pick_bn(kWidths16, &tiles, 1, sms / 2);
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
   const PairOperand x{a.x, a.ldx, false}, wg{a.gate, a.ldw, false}, wu{a.up, a.ldw, false};
-  if (!map16(&q.a[0], x, a.T, a.K, a.dtype, 128) || !map16(&q.b[0], wg, a.I, a.K, a.dtype, bn / 2) ||
+  if (!map16(&q.a[0], x, a.T, a.K, a.dtype, a_box(a.T)) || !map16(&q.b[0], wg, a.I, a.K, a.dtype, bn / 2) ||
       !map16(&q.b[1], wu, a.I, a.K, a.dtype, bn / 2))
     return cudaErrorInvalidValue;
   q.M = a.T;
@@ -831,12 +859,13 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   cudaError_t err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   const int64_t tm = cdiv(a.T, 256);
-  const int bn = pick_bn(kWidths16Mn, sms / 2, [&](int w) { return tm * cdiv(a.I, w); });
+  const Tiles tiles{tm, a.I, cdiv(a.H, 64)};
+  const int bn = pick_bn(kWidths16Mn, &tiles, 1, sms / 2);
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
   const PairOperand dy{a.dy, a.lddy, false}, wd{a.down, a.I, true};
-  if (!map16(&q.a[0], dy, a.T, a.H, a.dtype, 128) || !map16(&q.b[0], wd, a.I, a.H, a.dtype, bn / 2))
+  if (!map16(&q.a[0], dy, a.T, a.H, a.dtype, a_box(a.T)) || !map16(&q.b[0], wd, a.I, a.H, a.dtype, bn / 2))
     return cudaErrorInvalidValue;
   q.M = a.T;
   q.N = a.I;
@@ -852,11 +881,11 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, false, st);
 }
 
-int pair_mx_tile(int T, int N, int act) {
+int pair_mx_tile(int T, int N, int K, int act) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 148;
-  const int64_t tm = cdiv(T, 256), cols = act != kActNone ? 2 * (int64_t)N : N;
-  return pick_bn(kWidthsMx, sms / 2, [&](int w) { return tm * cdiv(cols, w); });
+  const Tiles tiles{cdiv(T, 256), act != kActNone ? 2 * (int64_t)N : N, cdiv(K, 256)};
+  return pick_bn(kWidthsMx, &tiles, 1, sms / 2);
 }
 
 cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
@@ -869,7 +898,7 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   PProb& q = p.p[0];
   const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, ns = CU_TENSOR_MAP_SWIZZLE_NONE;
-  if (!encode_tma_2d(&q.a[0], u8, a.xq, a.K / 2, a.T, pitch, 128, 128, sw) ||
+  if (!encode_tma_2d(&q.a[0], u8, a.xq, a.K / 2, a.T, pitch, 128, a_box(a.T), sw) ||
       !encode_tma_2d(&q.b[0], u8, a.wq, a.K / 2, a.N, pitch, 128, bn / 2, sw) ||
       !encode_tma_2d(&q.b[1], u8, a.wq + (gated ? a.N * pitch : 0), a.K / 2, a.N, pitch, 128, bn / 2, sw) ||
       !encode_tma_2d(&p.sfa, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.xsf, (uint64_t)chunks * 128, cdiv(a.T, 128),

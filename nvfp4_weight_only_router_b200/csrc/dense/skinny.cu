@@ -1,4 +1,4 @@
-// Products of up to 32 tokens with a weight matrix: y[t, n] = sum_k x[t, k]
+// Products of few tokens (up to 32 a CTA) with a weight matrix: y[t, n] = sum_k x[t, k]
 // w[n, k], optionally gated (y[t, i] = act(gate_i) up_i), with 16-bit or MXFP4
 // weights.
 //
@@ -226,6 +226,26 @@ cudaError_t launch_nt(const SkinnyParams& p, int T, bool after, cudaStream_t st)
 }
 
 }  // namespace
+
+// Measured against the tensor-core kernels (whole calls, us, N x K, `silu`
+// gated): the crossing lies where a group's CTAs no longer fit the SMs at once
+// (2 on each), or, with x quantised in every CTA, where a second group comes.
+//   W4A16  T = 32:  8192 x 2816 17.6 / 21.3, 2816 x 2112  8.1 / 11.8
+//          T = 64:  2816 x 2112 13.6 / 11.8 (two waves), 1024 x 1024 3.5 / 7.7
+//          T = 128: 512 x 2816 silu 6.0 / 11.4 (one wave)
+//   W4A4   T = 8:   4224 x 2816 silu 7.1 / 9.9, 8192 x 2816 11.7 / 10.6 (two waves)
+//          T = 16:  1024 x 1024 3.7 / 6.7, 2816 x 2112 8.6 / 8.4; T = 32: 13.8 / 8.4
+//   16-bit gated block, H = 2816: T = 16, I = 2112 12.8 / 18.6; T = 64, I = 256
+//          11.8 / 14.1 (one wave); T = 32, I = 8192 / H = 2816 55.1 / 47.1 (two waves)
+bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x) {
+  if (T > 128) return false;
+  int sms = 0;
+  if (sm_count(&sms) != cudaSuccess) sms = 148;
+  const int rows = gated ? 8 : 16;
+  const bool one_wave = (int64_t)((N + rows - 1) / rows) * ((T + 31) / 32) <= 2 * sms;
+  if (quant_x) return T <= 16 && one_wave;
+  return T <= (mx ? 32 : 16) || (one_wave && T <= (mx ? 128 : 64));
+}
 
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   const bool gated = a.act != kActNone;
