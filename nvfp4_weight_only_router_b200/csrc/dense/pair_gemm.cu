@@ -110,8 +110,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+// Execution order only: barrier initialisation has its own fence, and at the
+// end nothing is handed over (the releasing form takes 1000 cycles).
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 // shared::cluster address of `p` in SM 0 of the pair
 __device__ __forceinline__ uint32_t leader_addr(const void* p) {
@@ -615,6 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       for (int c = 0; c < HC; c += CW) {
         uint8_t* buf = sm.out[ew] + (chunk++ % BUFS) * (kPOutB / BUFS);
         out_reuse<BUFS - 1>(lane);
+        float v32[32];  // plain: of two groups
 #pragma unroll
         for (int k = 0; k < CW; k += 16) {
           uint32_t w[8];
@@ -624,9 +627,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             tmem_ld16(tcol + BN / 2 + c + k, u);
             gate16(p.e, p.e.kept ? kept_blk(n0 + c + k) : nullptr, lane, g, u, f16, w);
           } else if constexpr (EPI == kEpiPlain) {
-            float v[16];
-            tmem_ld16(tcol + c + k, v);
-            pack16(v, f16, w);
+            if (k % 32 == 0) tmem_ld32(tcol + c + k, v32);
+            pack16(v32 + k % 32, f16, w);
           } else {
             if (c + k + 16 * AHEAD < HC) fetch(c + k + 16 * AHEAD);
             const Kept16& r = kept16[((c + k) / 16) % (AHEAD + 1)];
