@@ -110,8 +110,8 @@ typedef struct {
  *   x [T, H] (row stride ldx), y [T, H]
  *   saved gated_ffn_saved_bytes bytes, 256-byte aligned, for
  *         gated_ffn_backward (h in 16 bits, act(g) and u act'(g) in 24: 8 bytes
- *         per token and hidden unit, and padding to blocks of 32 tokens x 16
- *         hidden units), or NULL
+ *         per token and hidden unit, and padding: rows of 64, blocks of 32 x 16
+ *         tokens x hidden units), or NULL
  * fp32 accumulation; h is rounded to the 16-bit type.  T <= 2^20.  With `saved`
  * the workspace is not used.
  * ------------------------------------------------------------------------- */

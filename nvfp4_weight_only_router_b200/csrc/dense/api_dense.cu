@@ -222,6 +222,7 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
     a.act = act;
     a.dtype = kBf16;
     a.h = y;
+    a.ldh = a.I;
     a.after_producer = true;
     return cuda_status(launch_pair_gated(a, device_status_ptr(), s));
   }
@@ -287,7 +288,7 @@ size_t gated_ffn_saved_bytes(int32_t T, const gated_ffn_weights* f) {
 }
 
 size_t gated_ffn_forward_workspace_bytes(int32_t T, const gated_ffn_weights* f) {
-  return check_ffn(T, f) == NVFP4_OK ? round_up((size_t)T * f->I * 2 + 1, 256) : 0;
+  return check_ffn(T, f) == NVFP4_OK ? round_up((size_t)T * pair_pitch(f->I) * 2 + 1, 256) : 0;
 }
 
 nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gated_ffn_weights* f, void* y, void* saved,
@@ -306,8 +307,10 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   cudaStream_t s = as_stream(stream);
   int* status = device_status_ptr();
   void* const h = saved ? saved : ws;
+  const bool few = !saved && skinny_fits(T, f->I, true, false, false);
+  const int64_t ldh = few ? f->I : pair_pitch(f->I);
   cudaError_t e;
-  if (!saved && skinny_fits(T, f->I, true, false, false)) {
+  if (few) {
     SkinnyArgs a{};
     a.x = x;
     a.ldx = ldx;
@@ -333,6 +336,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
     a.act = f->act;
     a.dtype = f->dtype;
     a.h = h;
+    a.ldh = ldh;
     a.keep = saved != nullptr;
     a.kept = pair_kept(saved, T, f->I);
     e = launch_pair_gated(a, status, s);
@@ -341,7 +345,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   if (skinny_fits(T, f->H, false, false, false)) {
     SkinnyArgs a{};
     a.x = h;
-    a.ldx = f->I;
+    a.ldx = ldh;
     a.w0 = f->down;
     a.y = y;
     a.T = T;
@@ -353,7 +357,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
     return cuda_status(launch_skinny(a, s));
   }
   PairGemm g{};
-  g.seg[0] = PairSegment{rows_of(h, f->I), rows_of(f->down, f->I), f->I};
+  g.seg[0] = PairSegment{rows_of(h, ldh), rows_of(f->down, f->I), f->I};
   g.nseg = 1;
   g.M = T;
   g.N = f->H;
@@ -362,7 +366,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
 }
 
 size_t gated_ffn_backward_workspace_bytes(int32_t T, const gated_ffn_weights* f) {
-  return check_ffn(T, f) == NVFP4_OK ? round_up(2 * round_up((size_t)T * f->I * 2, 256) + 1, 256) : 0;
+  return check_ffn(T, f) == NVFP4_OK ? round_up(2 * round_up((size_t)T * pair_pitch(f->I) * 2, 256) + 1, 256) : 0;
 }
 
 nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* saved, int32_t T,
@@ -391,10 +395,10 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
     return NVFP4_OK;
   }
   if (T == 1) ldx = lddy = H;
-  const size_t plane = (size_t)T * I;
+  const int64_t ldi = pair_pitch(I);
   const PairKept kept = pair_kept(const_cast<void*>(saved), T, I);
   uint16_t* dg = static_cast<uint16_t*>(ws);
-  uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + round_up(plane * 2, 256));
+  uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + round_up((size_t)T * ldi * 2, 256));
   int* status = device_status_ptr();
   if (dx || dgate || dup) {
     PairGatedBwd a{};
@@ -415,8 +419,8 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
   int n = 0;
   if (dx) {
     PairGemm& p = q[n++];
-    p.seg[0] = PairSegment{rows_of(dg, I), cols_of(f->gate, H), I};
-    p.seg[1] = PairSegment{rows_of(du, I), cols_of(f->up, H), I};
+    p.seg[0] = PairSegment{rows_of(dg, ldi), cols_of(f->gate, H), I};
+    p.seg[1] = PairSegment{rows_of(du, ldi), cols_of(f->up, H), I};
     p.nseg = 2;
     p.M = T;
     p.N = H;
@@ -430,9 +434,9 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
     p.N = N;
     p.out = out;
   };
-  if (dgate) weight_grad(dg, I, x, ldx, I, H, dgate);
-  if (dup) weight_grad(du, I, x, ldx, I, H, dup);
-  if (ddown) weight_grad(dy, lddy, kept.h, I, H, I, ddown);
+  if (dgate) weight_grad(dg, ldi, x, ldx, I, H, dgate);
+  if (dup) weight_grad(du, ldi, x, ldx, I, H, dup);
+  if (ddown) weight_grad(dy, lddy, kept.h, ldi, H, I, ddown);
   if (n == 0) return NVFP4_OK;
   return cuda_status(launch_pair_gemm(q, n, f->dtype, dx || dgate || dup, status, s));
 }

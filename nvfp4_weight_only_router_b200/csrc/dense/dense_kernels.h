@@ -89,7 +89,11 @@ constexpr int kPairMaxProblems = 4;
 // plain products, one launch for all (at most kPairMaxProblems); out = sum over segments A B^T
 // `after`: an operand is written by the kernel launched just before on the stream
 cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, int* status, cudaStream_t st);
-// What the forward pass keeps for the backward one: h [T, I], and p = u act'(g)
+// Row pitch of the 16-bit tensors that one kernel hands to the next (h, dg, du):
+// whole 128-byte lines.  A TMA box row off them is two requests, and the copies
+// of a 1001 x 2008 x 1000 step, not the products, then set its time.
+inline int64_t pair_pitch(int64_t I) { return (I + 63) / 64 * 64; }
+// What the forward pass keeps for the backward one: h [T, pair_pitch(I)], and p = u act'(g)
 // and a = act(g) in 24 bits, in blocks of 32 rows x 16 hidden units (row blocks
 // outermost, edges padded) as an epilogue warp holds them, a row per lane:
 // 32 x 32 bytes of p's upper 16 bits, as many of a's, 32 x 16 bytes of p's
@@ -100,7 +104,7 @@ struct PairKept {
   size_t bytes;
 };
 inline PairKept pair_kept(void* base, int64_t T, int64_t I) {
-  const size_t hb = ((size_t)(T * I) * 2 + 255) / 256 * 256;
+  const size_t hb = ((size_t)(T * pair_pitch(I)) * 2 + 255) / 256 * 256;
   uint8_t* b = static_cast<uint8_t*>(base);
   return PairKept{b, b + hb, hb + (size_t)((T + 31) / 32 * ((I + 15) / 16)) * kKeptBlockB};
 }
@@ -111,7 +115,8 @@ struct PairGated {
   int64_t ldw;
   int T, I, K;
   int act, dtype;
-  void* h;
+  void* h;         // [T, I]
+  int64_t ldh;
   bool keep;       // kept.h == h
   PairKept kept;
   bool after_producer;  // as SkinnyArgs
@@ -125,7 +130,7 @@ struct PairGatedBwd {
   int T, H, I;
   int dtype;
   PairKept kept;
-  void *dg, *du;
+  void *dg, *du;          // [T, pair_pitch(I)]
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
 // MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns);

@@ -692,23 +692,26 @@ constexpr int out_cols() {  // columns of an output box, as in the kernel
 }
 // [M, N] 16-bit output, boxes of 32 rows
 template <int EPI, int BN>
-bool map_out(CUtensorMap* m, void* out, int M, int N) {
+bool map_out(CUtensorMap* m, void* out, int M, int N, int64_t ld) {
   constexpr int CW = out_cols<EPI, BN>();
-  return encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, out, N, M, (uint64_t)N * 2, CW, 32, POut<CW>::SW);
+  return encode_tma_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, out, N, M, (uint64_t)ld * 2, CW, 32, POut<CW>::SW);
 }
 
+// ldo: the outputs' row pitch in elements, 0 for N.
 // `after`: behind the kernel launched just before on the stream, whose tail this
 // one's set-up may overlap
 template <int KIND, int BN, int EPI, int NP>
-cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, bool after, cudaStream_t st) {
+cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int64_t ldo, bool after, cudaStream_t st) {
   using C = PCfg<KIND, BN>;
   for (int i = 0; i < p.np; ++i) {
     PProb& q = p.p[i];
-    if (!map_out<EPI, BN>(&q.o[0], out[i], q.M, q.N)) return cudaErrorInvalidValue;
+    const int64_t ld = ldo ? ldo : q.N;
+    if (!map_out<EPI, BN>(&q.o[0], out[i], q.M, q.N, ld) ||
+        (EPI == kEpiGatedBwd && !map_out<EPI, BN>(&q.o[1], out1, q.M, q.N, ld)))
+      return cudaErrorInvalidValue;
     const int a = q.a_mn ? C::A_SUB : a_box(q.M) * 128;
     q.tx = C::KS * ((q.M > 128 ? 2 : 1) * (a + C::SFA_SUB) + 2 * (C::B_SUB + C::SFB_SUB));
   }
-  if (EPI == kEpiGatedBwd && !map_out<EPI, BN>(&p.p[0].o[1], out1, p.p[0].M, p.p[0].N)) return cudaErrorInvalidValue;
   constexpr int smem = (int)sizeof(PSmem<KIND, BN>) + 1024;
   static_assert(smem <= 232448, "shared memory budget");
   auto fn = pair_gemm_kernel<KIND, BN, EPI, NP>;
@@ -822,9 +825,9 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, in
   p.np = n;
   p.n_tiles = t0;
   p.status = status;
-  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, out, nullptr, after, st);
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, out, nullptr, after, st);
-  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, out, nullptr, after, st);
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, after, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, after, st);
+  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, after, st);
 }
 
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) {
@@ -851,9 +854,9 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn / 2));
   p.status = status;
-  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, {a.h}, nullptr, a.after_producer, st);
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, {a.h}, nullptr, a.after_producer, st);
-  return launch_pair<kKind16, 256, kEpiGated, 1>(p, {a.h}, nullptr, a.after_producer, st);
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, a.after_producer, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, a.after_producer, st);
+  return launch_pair<kKind16, 256, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, a.after_producer, st);
 }
 
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st) {
@@ -879,8 +882,8 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn));
   p.status = status;
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, {a.dg}, a.du, false, st);
-  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, false, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), false, st);
+  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), false, st);
 }
 
 int pair_mx_tile(int T, int N, int K, int act) {
@@ -919,13 +922,13 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   p.n_tiles = (int)(tm * tiles_n);
   p.status = status;
   if (gated) {
-    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, {a.y}, nullptr, true, st);
-    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, {a.y}, nullptr, true, st);
-    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, {a.y}, nullptr, true, st);
+    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, true, st);
+    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, true, st);
+    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, {a.y}, nullptr, 0, true, st);
   }
-  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, {a.y}, nullptr, true, st);
-  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, {a.y}, nullptr, true, st);
-  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, {a.y}, nullptr, true, st);
+  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, true, st);
+  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, true, st);
+  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, {a.y}, nullptr, 0, true, st);
 }
 
 }  // namespace nvfp4moe
