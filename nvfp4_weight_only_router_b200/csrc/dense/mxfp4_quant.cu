@@ -135,9 +135,8 @@ __device__ __forceinline__ uint4 encode_block(const Blk<T>& r, uint32_t& byte) {
 
 // One block of the flattened (row, block) order per thread and step, U steps
 // of kQT blocks per CTA with their loads issued together.
-template <typename T, int ALIGN, bool MMA>
+template <typename T, int ALIGN, bool MMA, int U>
 __device__ __forceinline__ void quant_cta(const QuantArgs& p, int64_t cta) {
-  constexpr int U = 2;
   const int64_t first = cta * (kQT * U);
   const int64_t r0 = first / p.walked;
   const uint32_t b0 = (uint32_t)(first - r0 * p.walked), per = (uint32_t)p.walked;
@@ -168,11 +167,12 @@ __device__ __forceinline__ void quant_cta(const QuantArgs& p, int64_t cta) {
     }
   }
 }
-constexpr int kQBlocks = 2 * kQT;  // blocks per CTA
+constexpr int kSmallBlocks = 4 * 148 * kQT;
+constexpr int kPrepU = 2;  // steps of the kernel that prepares a product
 
-template <typename T, int ALIGN>
+template <typename T, int ALIGN, int U>
 __global__ void __launch_bounds__(kQT) mxfp4_quantize_kernel(QuantArgs p) {
-  quant_cta<T, ALIGN, false>(p, blockIdx.x);
+  quant_cta<T, ALIGN, false, U>(p, blockIdx.x);
 }
 
 struct TileScales {
@@ -190,7 +190,7 @@ template <typename T, int ALIGN>
 __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qblocks, TileScales t) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product sets up meanwhile
   if ((int64_t)blockIdx.x < qblocks) {
-    quant_cta<T, ALIGN, true>(p, blockIdx.x);
+    quant_cta<T, ALIGN, true, kPrepU>(p, blockIdx.x);
     return;
   }
   const int64_t w = ((int64_t)blockIdx.x - qblocks) * kQT + threadIdx.x;
@@ -227,6 +227,7 @@ __device__ __forceinline__ float mx_value(const uint8_t* codes, const uint8_t* s
 // over a warp, from one load of codes and one scale; four such groups with their
 // loads issued together.  Rows of whole groups, 32-byte aligned output.
 constexpr int kDU = 4, kDGroups = kQT * kDU;
+constexpr int kAU = 2, kAGroups = kQT * kAU;  // any length
 
 template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
@@ -289,20 +290,21 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __
 // Any K and alignment: a thread writes 8 consecutive values of the flat output,
 // which is 16-byte aligned.  Their codes lie in two words of the row and their
 // scales in two bytes; a group that runs over the end of its row goes value by
-// value.  (1000 x 2100 f32: 6.3 us; a value per thread and store took 8.0, this
-// form for whole groups 20 us more than the kernel above at 32768 x 2816.)
+// value.  Two groups a thread: one or four take 11% and 22% longer at 30000 x
+// 2817 f32 (76.1 us); a value per thread and store took 8.0 us at 1000 x 2100
+// f32 (5.6), this form for whole groups 83 us at 32768 x 2816 (63.5 above).
 template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
                                                                    int64_t K, T* __restrict__ out) {
-  const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * (kDGroups * 8), n = rows * K;
+  const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * (kAGroups * 8), n = rows * K;
   const uint32_t k = (uint32_t)K, words = (uint32_t)(4 * nb);
   const int64_t r0 = first / K;
   const uint32_t c0 = (uint32_t)(first - r0 * K);
-  uint32_t w[kDU], s0[kDU], s1[kDU], c[kDU];
-  int64_t row[kDU];
+  uint32_t w[kAU], s0[kAU], s1[kAU], c[kAU];
+  int64_t row[kAU];
 #pragma unroll
-  for (int u = 0; u < kDU; ++u) {
+  for (int u = 0; u < kAU; ++u) {
     const uint32_t i = c0 + (u * kQT + threadIdx.x) * 8, dr = i / k;
     row[u] = r0 + dr;
     c[u] = i - dr * k;
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t
     }
   }
 #pragma unroll
-  for (int u = 0; u < kDU; ++u) {
+  for (int u = 0; u < kAU; ++u) {
     const int64_t at = first + (int64_t)(u * kQT + threadIdx.x) * 8;
     if (row[u] >= rows) continue;
     float v[8];
@@ -360,12 +362,21 @@ int row_align(const void* p, int64_t ld, int elsize) {
   return 0;
 }
 
+template <typename T, int U>
+void quantize_u(const QuantArgs& p, cudaStream_t st) {
+  const unsigned grid = blocks_for(p.rows * p.walked, U * kQT);
+  if (p.align == 32) mxfp4_quantize_kernel<T, 32, U><<<grid, kQT, 0, st>>>(p);
+  else if (p.align == 16) mxfp4_quantize_kernel<T, 16, U><<<grid, kQT, 0, st>>>(p);
+  else mxfp4_quantize_kernel<T, 0, U><<<grid, kQT, 0, st>>>(p);
+}
+
+// Two blocks a thread keep more bytes in flight; up to about four CTAs an SM
+// twice the threads do that better (bf16, us, two / one: 1 x 2816 2.5 / 2.1,
+// 1000 x 2816 3.4 / 3.1; 1000 x 2100 f32 5.4 / 5.2).
 template <typename T>
 void quantize_t(const QuantArgs& p, cudaStream_t st) {
-  const unsigned grid = blocks_for(p.rows * p.walked, kQBlocks);
-  if (p.align == 32) mxfp4_quantize_kernel<T, 32><<<grid, kQT, 0, st>>>(p);
-  else if (p.align == 16) mxfp4_quantize_kernel<T, 16><<<grid, kQT, 0, st>>>(p);
-  else mxfp4_quantize_kernel<T, 0><<<grid, kQT, 0, st>>>(p);
+  if (p.rows * p.walked <= (int64_t)kSmallBlocks) quantize_u<T, 1>(p, st);
+  else quantize_u<T, 2>(p, st);
 }
 
 template <typename T>
@@ -374,7 +385,7 @@ void dequantize_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, int
   if (K % G == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0)
     mxfp4_dequantize_kernel<T><<<blocks_for(rows * (K / G), kDGroups), kQT, 0, st>>>(codes, scales, rows, K, out);
   else
-    mxfp4_dequantize_any_kernel<T><<<blocks_for(rows * K, kDGroups * 8), kQT, 0, st>>>(codes, scales, rows, K, out);
+    mxfp4_dequantize_any_kernel<T><<<blocks_for(rows * K, kAGroups * 8), kQT, 0, st>>>(codes, scales, rows, K, out);
 }
 
 }  // namespace
@@ -414,7 +425,7 @@ cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st) {
   p.nb = mx_blocks(a.K);
   p.sf_chunks = mx_sf_chunks(a.K);
   p.walked = (int64_t)p.sf_chunks * 4;
-  const int64_t qb = blocks_for(p.rows * p.walked, kQBlocks);
+  const int64_t qb = blocks_for(p.rows * p.walked, kPrepU * kQT);
   const TileScales t{a.wscales, a.wsf, mx_wsf_blocks(a.N, a.gated, a.bn) * p.sf_chunks * 128, a.N, a.bn, a.gated};
   const unsigned grid = (unsigned)qb + blocks_for(t.words, kQT);
   // x's rows are 16-byte aligned (checked by the entry point)
