@@ -23,7 +23,9 @@
 //           writes dg = dh p and du = dh a, so dh never leaves the chip.
 //
 // Warps: 0 and 2 TMA producers of A and B (in both SMs), 1 MMA issuer (in SM 0
-// of the pair), 4-11 epilogue: a warp per tensor-memory lane quarter and column
+// of the pair), 3 MXFP4 scales into tensor memory (likewise, ahead of the
+// products, whose issue they would delay), 4-11 epilogue: a warp per
+// tensor-memory lane quarter and column
 // half.  Two accumulators, so that a tile's epilogue overlaps the next tile's
 // products (MXFP4 tiles have at most 192 columns: scales need tensor memory
 // too).  Every wait is bounded in wall time; one that gives up records a timeout
@@ -39,7 +41,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kPThreads = 384;
-constexpr int kPProdA = 0, kPMma = 1, kPProdB = 2, kPEpi0 = 4, kPEpiWarps = 8;
+constexpr int kPProdA = 0, kPMma = 1, kPProdB = 2, kPScale = 3, kPEpi0 = 4, kPEpiWarps = 8;
 constexpr int kPTmem = 512;
 constexpr int kPOutB = 4096;  // output buffer of an epilogue warp: 32 rows x 64 columns
 constexpr int kKind16 = 0, kKindMx = 1;
@@ -72,8 +74,9 @@ struct alignas(1024) PSmem {
   uint8_t sfa[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::KS * C::SFA_SUB : 16];
   uint8_t sfb[KIND == kKindMx ? C::NS : 1][KIND == kKindMx ? C::KS * C::SFB_SUB : 16];
   uint64_t full[C::NS], empty[C::NS];  // full: SM 0's barrier counts both SMs' bytes
+  uint64_t scaled[C::NS];              // MXFP4: the stage's scales are in tensor memory
   uint64_t d_full[2], d_empty[2];      // d_empty: SM 0's, arrivals of both SMs' epilogues
-  uint64_t fin;
+  uint64_t fin, fin_sf;
   uint32_t taddr;
   int abort_flag;
   int issued[2];                       // stages of A and of B copied
@@ -154,6 +157,10 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {  // arrives in both
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+__device__ __forceinline__ void commit_here(uint64_t* bar) {  // arrives in this SM
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -376,12 +383,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.scaled[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.d_full[b], 1);
       mbar_init(&sm.d_empty[b], 2 * kPEpiWarps);
     }
     mbar_init(&sm.fin, 1);
+    mbar_init(&sm.fin_sf, 1);
     sm.abort_flag = 0;
     sm.issued[0] = sm.issued[1] = 0;
     fence_mbar_init();
@@ -464,44 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       const uint32_t a0 = smem_u32(sm.a[0][0]), b0 = smem_u32(sm.b[0][0]);
       uint32_t s = 0, parity = 0, titer = 0;
       bool ok = true;
-      // MXFP4: a stage's scales enter tensor memory one stage ahead of its
-      // products, behind which they would otherwise queue
-      uint32_t cs = 0, cparity = 0;
-      int cleft = 0;  // stages whose scales are still to come
-      const uint32_t sf0 = taddr + (uint32_t)C::SF_COL0, sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
-      auto copy_scales = [&]() {  // stage cs, one lane
-#pragma unroll
-        for (int u = 0; u < C::KS; ++u) {
-          const uint32_t ta = sf0 + (cs * C::KS + u) * C::SF_COLS, tb = ta + 8;
-          const uint32_t fa = sfa0 + (cs * C::KS + u) * C::SFA_SUB, fb = sfb0 + (cs * C::KS + u) * C::SFB_SUB;
-#pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            cp_sf_pair(ta + 4 * ch, fa + ch * kSfChunkB);
-#pragma unroll
-            for (int bb = 0; bb < C::SFB_BLK; ++bb)
-              cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), fb + (bb * 2 + ch) * kSfChunkB);
-          }
-        }
-      };
-      auto next_scales = [&]() {
-        --cleft;
-        if (++cs == C::NS) {
-          cs = 0;
-          cparity ^= 1;
-        }
-      };
-      if constexpr (KIND == kKindMx) {
-        if (cluster < p.n_tiles) {
-          cleft = ((p.n_tiles - cluster - 1) / clusters + 1) * p.p[0].kc;
-          ok = swait(sm, &sm.full[0], 0, p.status);
-          if (ok) {
-            tc_fence_after();
-            if (elect_one()) copy_scales();
-            __syncwarp();
-            next_scales();
-          }
-        }
-      }
+      const uint32_t sf0 = taddr + (uint32_t)C::SF_COL0;
       for (int t = cluster; t < p.n_tiles && ok; t += clusters, ++titer) {
         if (t != cluster) tile = ptile<NP>(p, t);
         const PProb& q = p.p[tile.prob];
@@ -526,12 +498,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         const uint64_t ad0 = a_mn ? make_mn_desc(a0) : make_sw128_desc(a0);
         const uint64_t bd0 = b_mn ? make_mn_desc(b0) : make_sw128_desc(b0);
         for (int kc = 0; kc < kc_all; ++kc) {
-          if (KIND == kKind16) ok = swait(sm, &sm.full[s], parity, p.status);
-          else if (cleft > 0) ok = swait(sm, &sm.full[cs], cparity, p.status);
+          ok = swait(sm, &sm.full[s], parity, p.status);
+          if (KIND == kKindMx && ok) ok = swait(sm, &sm.scaled[s], parity, p.status);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            if (KIND == kKindMx && cleft > 0) copy_scales();
 #pragma unroll
             for (int u = 0; u < C::KS; ++u) {
               const uint64_t ad = ad0 + (uint64_t)((s * C::KS + u) * (C::A_SUB >> 4));
@@ -561,7 +532,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             if (kc == kc_all - 1) commit_pair(&sm.d_full[db]);
           }
           __syncwarp();
-          if (KIND == kKindMx && cleft > 0) next_scales();
           if (++s == C::NS) {
             s = 0;
             parity ^= 1;
@@ -573,6 +543,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       if (elect_one()) commit_pair(&sm.fin);
       __syncwarp();
       wait_cluster(&sm.fin, 0);
+      __syncwarp();
+    }
+  } else if (KIND == kKindMx && warp == kPScale) {
+    // ------------------------- scales into tensor memory, ahead of the products
+    if (rank == 0) {
+      const uint32_t sf0 = taddr + (uint32_t)C::SF_COL0, sfa0 = smem_u32(sm.sfa[0]), sfb0 = smem_u32(sm.sfb[0]);
+      uint32_t s = 0, parity = 0;
+      bool ok = true;
+      int left = cluster < p.n_tiles ? ((p.n_tiles - cluster - 1) / clusters + 1) * p.p[0].kc : 0;
+      for (; left > 0; --left) {
+        ok = swait(sm, &sm.full[s], parity, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int u = 0; u < C::KS; ++u) {
+            const uint32_t ta = sf0 + (s * C::KS + u) * C::SF_COLS, tb = ta + 8;
+            const uint32_t fa = sfa0 + (s * C::KS + u) * C::SFA_SUB, fb = sfb0 + (s * C::KS + u) * C::SFB_SUB;
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              cp_sf_pair(ta + 4 * ch, fa + ch * kSfChunkB);
+#pragma unroll
+              for (int bb = 0; bb < C::SFB_BLK; ++bb)
+                cp_sf_pair(tb + 4 * (ch * C::SFB_BLK + bb), fb + (bb * 2 + ch) * kSfChunkB);
+            }
+          }
+          commit_here(&sm.scaled[s]);
+        }
+        __syncwarp();
+        if (++s == C::NS) {
+          s = 0;
+          parity ^= 1;
+        }
+      }
+      // the copies issued have completed before the tear-down
+      if (elect_one()) commit_here(&sm.fin_sf);
+      __syncwarp();
+      wait_cluster(&sm.fin_sf, 0);
       __syncwarp();
     }
   } else if (warp >= kPEpi0) {
