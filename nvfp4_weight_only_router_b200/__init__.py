@@ -33,10 +33,9 @@ __all__ = sorted(_API | _DENSE | _CAPI | {"capi", "dense_capi", "build"})
 def __getattr__(name):
     if name in ("capi", "dense_capi"):
         return importlib.import_module("." + name, __name__)
-    if name in _DENSE:
-        return getattr(importlib.import_module(".dense", __name__), name)
-    if name in _CAPI:
-        return getattr(importlib.import_module(".capi", __name__), name)
-    if name in _API:
-        return getattr(importlib.import_module(".api", __name__), name)
+    for names, module in ((_DENSE, ".dense"), (_CAPI, ".capi"), (_API, ".api")):
+        if name in names:
+            value = getattr(importlib.import_module(module, __name__), name)
+            globals()[name] = value  # found at once from now on
+            return value
     raise AttributeError(name)

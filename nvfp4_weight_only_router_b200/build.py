@@ -111,7 +111,7 @@ def _link_calls(obj: str, verbose: bool) -> None:
     libs = cpp_extension.library_paths()
     # libnvfp4dense.so is found next to the module
     _run(["g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:" + os.path.basename(DENSE_LIB), "-Wl,-rpath,$ORIGIN"] +
-         ["-L" + p for p in libs] + ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"], verbose)
+         ["-L" + p for p in libs] + ["-lc10", "-lc10_cuda", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"], verbose)
     os.replace(tmp, DENSE_CALLS)
 
 

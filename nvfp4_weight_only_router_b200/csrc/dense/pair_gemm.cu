@@ -767,8 +767,11 @@ int pick_bn(const Width (&widths)[NW], const Tiles* g, int n, int clusters) {
   int best = 0;
   int64_t least = INT64_MAX;
   for (const Width& w : widths) {
-    int64_t worst = 0;
-    for (int c = 0; c < clusters; ++c) {
+    // a cluster's load changes with c only at the problems' first tiles
+    int64_t worst = 0, first = 0;
+    for (int k = 0; k < n; ++k) {
+      const int64_t c = first % clusters;
+      first += g[k].m * cdiv(g[k].cols, w.bn);
       int64_t t0 = 0, cycles = 0;
       for (int i = 0; i < n; ++i) {
         const int64_t t1 = t0 + g[i].m * cdiv(g[i].cols, w.bn);

@@ -8,6 +8,7 @@
 // the steps one by one in Python, where the error is raised.  Work goes to
 // torch's current stream of x's device; memory comes from torch's allocator on
 // that stream.
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -44,9 +45,11 @@ bool matrix_ok(const Tensor& t, int64_t r, int64_t c, const Tensor& like) {
          t.scalar_type() == like.scalar_type() && t.get_device() == like.get_device();
 }
 
-Tensor bytes(size_t n, const Tensor& like) {
-  return at::empty({(int64_t)std::max<size_t>(n, 256)}, like.options().dtype(at::kByte));
+// An uninitialised tensor on like's device (at::empty without its dispatch).
+Tensor empty(at::IntArrayRef size, at::ScalarType type, const Tensor& like) {
+  return at::detail::empty_cuda(size, type, like.device(), std::nullopt);
 }
+Tensor bytes(size_t n, const Tensor& like) { return empty({(int64_t)std::max<size_t>(n, 256)}, at::kByte, like); }
 
 void* current_stream(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
 
@@ -56,8 +59,7 @@ py::object quantize(const Tensor& x) {
   if (dt < 0 || !rows_ok(x, ld)) return py::none();
   const c10::cuda::CUDAGuard guard(x.device());
   const int64_t R = x.size(0), K = x.size(1), nb = (K + 31) / 32;
-  const auto u8 = x.options().dtype(at::kByte);
-  Tensor codes = at::empty({R, 16 * nb}, u8), scales = at::empty({R, nb}, u8);
+  Tensor codes = empty({R, 16 * nb}, at::kByte, x), scales = empty({R, nb}, at::kByte, x);
   if (mxfp4_quantize(x.data_ptr(), dt, R, K, ld, codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(),
                      current_stream(x)) != NVFP4_OK)
     return py::none();
@@ -72,7 +74,7 @@ py::object dequantize(const Tensor& codes, const Tensor& scales, int64_t K, bool
   if (K < 0) K = 32 * nb;
   if ((K + 31) / 32 != nb) return py::none();
   const c10::cuda::CUDAGuard guard(codes.device());
-  Tensor out = at::empty({R, K}, codes.options().dtype(bf16 ? at::kBFloat16 : at::kFloat));
+  Tensor out = empty({R, K}, bf16 ? at::kBFloat16 : at::kFloat, codes);
   if (mxfp4_dequantize(codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(), R, K, out.data_ptr(), dtype_of(out),
                        current_stream(codes)) != NVFP4_OK)
     return py::none();
@@ -90,7 +92,7 @@ py::object linear(const Tensor& x, uintptr_t weight, int device, int act, bool a
   const int32_t T = (int32_t)x.size(0);
   const size_t need = a4 ? mxfp4_linear_a4_workspace_bytes(T, w, act) : mxfp4_linear_workspace_bytes(T, w, act);
   if (need == 0) return py::none();  // refused
-  Tensor y = at::empty({T, act ? w->N / 2 : w->N}, x.options()), ws;
+  Tensor y = empty({T, act ? w->N / 2 : w->N}, x.scalar_type(), x), ws;
   if (need > 256) ws = bytes(need, x);
   void* const wp = ws.defined() ? ws.data_ptr() : nullptr;
   const auto call = a4 ? mxfp4_linear_a4 : mxfp4_linear;
@@ -117,7 +119,7 @@ py::object ffn_forward(const Tensor& x, const Tensor& gate, const Tensor& up, co
   const int32_t T = (int32_t)x.size(0);
   const size_t need = save ? gated_ffn_saved_bytes(T, &f) : gated_ffn_forward_workspace_bytes(T, &f);
   if (need == 0) return py::none();
-  Tensor y = at::empty({T, f.H}, x.options()), ws = bytes(need, x);
+  Tensor y = empty({T, f.H}, x.scalar_type(), x), ws = bytes(need, x);
   if (gated_ffn_forward(x.data_ptr(), ld, T, &f, y.data_ptr(), save ? ws.data_ptr() : nullptr,
                         save ? nullptr : ws.data_ptr(), save ? 0 : ws.numel(), current_stream(x)) != NVFP4_OK)
     return py::none();
@@ -145,7 +147,7 @@ py::object ffn_backward(const Tensor& dy, const Tensor& x, const Tensor& gate, c
   void* p[4] = {};
   for (int i = 0; i < 4; ++i)
     if (needs[i]) {
-      out[i] = at::empty(like[i]->sizes(), x.options());
+      out[i] = empty(like[i]->sizes(), x.scalar_type(), x);
       p[i] = out[i]->data_ptr();
     }
   if (gated_ffn_backward(dy.data_ptr(), lddy, x.data_ptr(), ld, saved.data_ptr(), T, &f, p[0], p[1], p[2], p[3],

@@ -157,7 +157,8 @@ class Mxfp4Weight:
             raise ValueError(f"K = {self.K} must be a multiple of 32 and match the scales")
         object.__setattr__(self, "_c", dc.mxfp4_weight(self.codes.data_ptr(), self.scales.data_ptr(),
                                                        self.codes.shape[0], self.K))
-        object.__setattr__(self, "_at", (ctypes.addressof(self._c), self.codes.get_device()))
+        object.__setattr__(self, "_at", ctypes.addressof(self._c))
+        object.__setattr__(self, "_device", self.codes.get_device())
 
     @property
     def N(self) -> int:
@@ -173,12 +174,7 @@ class Mxfp4Weight:
         return mxfp4_dequantize(self.codes, self.scales, self.K, dtype, stream)
 
 
-def _linear(name, call, size, x, weight, activation, stream):
-    act = _act(activation)
-    if stream is None:
-        y = _calls.linear(x, *weight._at, act, call is dc.mxfp4_linear_a4)
-        if y is not None:
-            return y
+def _linear(name, call, size, x, weight, act, stream):
     ld = _rows(x, "x", weight.K)
     if x.dtype not in _DTYPE:
         raise ValueError("x must be bf16 (mxfp4_linear_a4: or f16)")
@@ -198,13 +194,22 @@ def _linear(name, call, size, x, weight, activation, stream):
 def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A16: y [T, N] = x weight^T for bf16 x [T, K]; with an activation the
     gated form y [T, N/2] = act(x Wg^T) * (x Wu^T)."""
-    return _linear("mxfp4_linear", dc.mxfp4_linear, dc.mxfp4_linear_workspace_bytes, x, weight, activation, stream)
+    act = _act(activation)
+    if stream is None:
+        y = _calls.linear(x, weight._at, weight._device, act, False)
+        if y is not None:
+            return y
+    return _linear("mxfp4_linear", dc.mxfp4_linear, dc.mxfp4_linear_workspace_bytes, x, weight, act, stream)
 
 
 def mxfp4_linear_a4(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A4: mxfp4_linear with x (bf16 or f16) quantised to MXFP4 on the way in."""
-    return _linear("mxfp4_linear_a4", dc.mxfp4_linear_a4, dc.mxfp4_linear_a4_workspace_bytes, x, weight, activation,
-                   stream)
+    act = _act(activation)
+    if stream is None:
+        y = _calls.linear(x, weight._at, weight._device, act, True)
+        if y is not None:
+            return y
+    return _linear("mxfp4_linear_a4", dc.mxfp4_linear_a4, dc.mxfp4_linear_a4_workspace_bytes, x, weight, act, stream)
 
 
 # ------------------------------------------------------------- feed-forward
