@@ -6,13 +6,17 @@
 //   value = E2M1 2^X.  A block with a NaN or an infinity gets scale 255 (NaN)
 //   and codes 0; a ragged last block is filled up with zeros.
 //
-// Bound by memory: K (2 + 1/2 + 1/32) bytes per bf16 row.  A thread holds one
-// block: 64 bytes of a 16-bit row by two 32-byte loads, its maximum by packed
-// integer comparisons, its codes by one 16-byte store, so that a block costs
-// no shuffles and neighbouring threads write neighbouring codes and scales.
+// Bound by memory: K (2 + 1/2 + 1/32) bytes per bf16 row.  Two forms:
+//   16-bit types: a thread holds one block, 64 bytes by two 32-byte loads, its
+//   maximum by packed integer comparisons, its codes by one 16-byte store,
+//   without shuffles (32768 x 2816 bf16: 36 us, 6.5 TB/s);
+//   f32: a thread holds 8 elements, four neighbouring lanes a block, whose
+//   maximum takes two shuffles: with a whole block a thread, every lane of a
+//   load touches a line of its own (32768 x 2820: 69 us, 113 that way; 16-bit
+//   rows off the grid the other way round, 32768 x 2813 bf16 47 and 75).
 // Rows off the 16-byte grid (and ragged last blocks) read the aligned 16-byte
-// pieces that hold the block and shift them into place in registers; only
-// pieces that hold an element of the block are read.
+// pieces that hold their elements and shift them into place in registers; only
+// pieces that hold an element of the row are read.
 #include <type_traits>
 
 #include "mxfp4_codec.cuh"
@@ -34,22 +38,22 @@ struct QuantArgs {
   int align;       // bytes that divide every row's address: 32, 16, or less (0)
 };
 
-// The bits of one block.
-template <typename T>
-struct Blk {
-  static constexpr int W = 32 * sizeof(T) / 4;
+// The bits of N elements.
+template <typename T, int N>
+struct Bits {
+  static constexpr int W = N * sizeof(T) / 4;
   uint32_t w[W];
 };
 
-// Valid elements c..min(c + 32, K) of a row whose first element is row0
-// elements past x, zeros behind them.
-template <typename T>
-__device__ __forceinline__ Blk<T> load_block_any(const void* x, int64_t row0, int64_t c, int64_t K) {
-  constexpr int W = Blk<T>::W;
-  Blk<T> r;
-  const int valid = (int)(K - c < 32 ? (K - c > 0 ? K - c : 0) : 32);
+// Elements c..c + N - 1 of a row whose first element is row0 elements past x,
+// zeros past K; only aligned pieces that hold an element of the row are read.
+template <typename T, int N>
+__device__ __forceinline__ Bits<T, N> load_any(const void* x, int64_t row0, int64_t c, int64_t K) {
+  constexpr int W = Bits<T, N>::W;
+  Bits<T, N> r;
+  const int valid = (int)(K - c < N ? (K - c > 0 ? K - c : 0) : N);
   const uintptr_t a = reinterpret_cast<uintptr_t>(x) + (uintptr_t)(row0 + c) * sizeof(T);
-  const int o = (int)(a & 15);                           // bytes before the block in its first piece
+  const int o = (int)(a & 15);  // bytes before the elements in their first piece
   const int bytes = valid * (int)sizeof(T);
   const uint4* src = reinterpret_cast<const uint4*>(a - o);
   uint32_t v[W + 4];
@@ -71,19 +75,20 @@ __device__ __forceinline__ Blk<T> load_block_any(const void* x, int64_t row0, in
   for (int i = 0; i < W; ++i) {
     uint32_t w = v[i];
     if (sizeof(T) == 2 && odd) w = __byte_perm(v[i], v[i + 1], 0x5432);
-    const int left = bytes - 4 * i;                      // valid bytes of this word
+    const int left = bytes - 4 * i;  // valid bytes of this word
     r.w[i] = left >= 4 ? w : (left > 0 ? w & 0xFFFFu : 0u);
   }
   return r;
 }
 
-template <typename T, int ALIGN>
-__device__ __forceinline__ Blk<T> load_block(const void* x, int64_t row0, int64_t c, int64_t K) {
-  constexpr int W = Blk<T>::W;
-  if (ALIGN < 16 || c + 32 > K) return load_block_any<T>(x, row0, c, K);
-  Blk<T> r;
+// The same for rows whose addresses ALIGN (32, 16 or 0) divides.
+template <typename T, int N, int ALIGN>
+__device__ __forceinline__ Bits<T, N> load_bits(const void* x, int64_t row0, int64_t c, int64_t K) {
+  constexpr int W = Bits<T, N>::W;
+  if (ALIGN < 16 || c + N > K) return load_any<T, N>(x, row0, c, K);
+  Bits<T, N> r;
   const char* p = static_cast<const char*>(x) + (row0 + c) * (int64_t)sizeof(T);
-  if (ALIGN == 32) {
+  if (ALIGN == 32 && W % 8 == 0) {
 #pragma unroll
     for (int i = 0; i < W / 8; ++i) {
       uint32_t q[8];
@@ -101,36 +106,35 @@ __device__ __forceinline__ Blk<T> load_block(const void* x, int64_t row0, int64_
   return r;
 }
 
-// The block's scale byte and its 32 codes.
-template <typename T>
-__device__ __forceinline__ uint4 encode_block(const Blk<T>& r, uint32_t& byte) {
-  constexpr bool F16 = std::is_same<T, __half>::value;
+// Bits of the largest magnitude, as fp32.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t max_bits(const Bits<T, N>& r) {
   uint32_t a = 0;
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) a = max(a, r.w[i] & 0x7FFFFFFFu);
+    for (int i = 0; i < N; ++i) a = max(a, r.w[i] & 0x7FFFFFFFu);
+    return a;
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) a = __vmaxu2(a, r.w[i] & 0x7FFF7FFFu);
+    for (int i = 0; i < N / 2; ++i) a = __vmaxu2(a, r.w[i] & 0x7FFF7FFFu);
     float lo, hi;
-    unpack16x2(a, F16, lo, hi);
-    a = max(abs_bits(lo), abs_bits(hi));
+    unpack16x2(a, std::is_same<T, __half>::value, lo, hi);
+    return max(abs_bits(lo), abs_bits(hi));
   }
-  byte = mx_scale_byte(a);
-  uint32_t c[4];
+}
+
+// Codes of elements 8 q..8 q + 7.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t codes8(const Bits<T, N>& r, int q, uint32_t byte) {
+  float v[8];
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float v[8];
-    if constexpr (sizeof(T) == 4) {
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r.w[8 * q + k]);
+  } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(r.w[8 * q + k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) unpack16x2(r.w[4 * q + k], F16, v[2 * k], v[2 * k + 1]);
-    }
-    c[q] = mx_encode8(v, byte);
+    for (int k = 0; k < 4; ++k) unpack16x2(r.w[4 * q + k], std::is_same<T, __half>::value, v[2 * k], v[2 * k + 1]);
   }
-  return make_uint4(c[0], c[1], c[2], c[3]);
+  return mx_encode8(v, byte);
 }
 
 // One block of the flattened (row, block) order per thread and step, U steps
@@ -140,7 +144,7 @@ __device__ __forceinline__ void quant_cta(const QuantArgs& p, int64_t cta) {
   const int64_t first = cta * (kQT * U);
   const int64_t r0 = first / p.walked;
   const uint32_t b0 = (uint32_t)(first - r0 * p.walked), per = (uint32_t)p.walked;
-  Blk<T> blk[U];
+  Bits<T, 32> blk[U];
   int64_t row[U];
   uint32_t b[U];
 #pragma unroll
@@ -149,13 +153,14 @@ __device__ __forceinline__ void quant_cta(const QuantArgs& p, int64_t cta) {
     row[u] = r0 + dr;
     b[u] = i - dr * per;
     // past the last row: nothing is read
-    blk[u] = load_block<T, ALIGN>(p.x, row[u] * p.ldx, (int64_t)b[u] * 32, row[u] < p.rows ? p.K : 0);
+    blk[u] = load_bits<T, 32, ALIGN>(p.x, row[u] * p.ldx, (int64_t)b[u] * 32, row[u] < p.rows ? p.K : 0);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (row[u] >= p.rows) continue;
-    uint32_t byte;
-    const uint4 c = encode_block<T>(blk[u], byte);
+    const uint32_t byte = mx_scale_byte(max_bits(blk[u]));
+    const uint4 c = make_uint4(codes8(blk[u], 0, byte), codes8(blk[u], 1, byte), codes8(blk[u], 2, byte),
+                               codes8(blk[u], 3, byte));
     if (!MMA || b[u] < p.nb) reinterpret_cast<uint4*>(p.codes)[row[u] * p.nb + b[u]] = c;
     if (MMA) {
       // blocks past K: scale 2^-127 on zero codes
@@ -173,6 +178,37 @@ constexpr int kPrepU = 2;  // steps of the kernel that prepares a product
 template <typename T, int ALIGN, int U>
 __global__ void __launch_bounds__(kQT) mxfp4_quantize_kernel(QuantArgs p) {
   quant_cta<T, ALIGN, false, U>(p, blockIdx.x);
+}
+
+// 8 elements per thread and step of the flattened (row, group of 8) order, U
+// steps with their loads issued together; a quad of lanes is in one block.
+template <typename T, int ALIGN, int U>
+__global__ void __launch_bounds__(kQT) mxfp4_quantize_quad_kernel(QuantArgs p) {
+  const uint32_t per = (uint32_t)(4 * p.nb);
+  const int64_t first = (int64_t)blockIdx.x * (kQT * U);
+  const int64_t r0 = first / per;
+  const uint32_t g0 = (uint32_t)(first - r0 * per);
+  Bits<T, 8> grp[U];
+  int64_t row[U];
+  uint32_t g[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = g0 + u * kQT + threadIdx.x, dr = i / per;
+    row[u] = r0 + dr;
+    g[u] = i - dr * per;
+    // past the last row: nothing is read
+    grp[u] = load_bits<T, 8, ALIGN>(p.x, row[u] * p.ldx, (int64_t)g[u] * 8, row[u] < p.rows ? p.K : 0);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t a = max_bits(grp[u]);
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    const uint32_t byte = mx_scale_byte(a), c = codes8(grp[u], 0, byte);
+    if (row[u] >= p.rows) continue;
+    reinterpret_cast<uint32_t*>(p.codes)[row[u] * per + g[u]] = c;
+    if ((threadIdx.x & 3) == 0) p.scales[row[u] * p.nb + (g[u] >> 2)] = (uint8_t)byte;
+  }
 }
 
 struct TileScales {
@@ -364,18 +400,25 @@ int row_align(const void* p, int64_t ld, int elsize) {
 
 template <typename T, int U>
 void quantize_u(const QuantArgs& p, cudaStream_t st) {
-  const unsigned grid = blocks_for(p.rows * p.walked, U * kQT);
-  if (p.align == 32) mxfp4_quantize_kernel<T, 32, U><<<grid, kQT, 0, st>>>(p);
-  else if (p.align == 16) mxfp4_quantize_kernel<T, 16, U><<<grid, kQT, 0, st>>>(p);
-  else mxfp4_quantize_kernel<T, 0, U><<<grid, kQT, 0, st>>>(p);
+  if constexpr (sizeof(T) == 4) {
+    const unsigned grid = blocks_for(p.rows * p.nb * 4, U * kQT);
+    if (p.align == 32) mxfp4_quantize_quad_kernel<T, 32, U><<<grid, kQT, 0, st>>>(p);
+    else if (p.align == 16) mxfp4_quantize_quad_kernel<T, 16, U><<<grid, kQT, 0, st>>>(p);
+    else mxfp4_quantize_quad_kernel<T, 0, U><<<grid, kQT, 0, st>>>(p);
+  } else {
+    const unsigned grid = blocks_for(p.rows * p.nb, U * kQT);
+    if (p.align == 32) mxfp4_quantize_kernel<T, 32, U><<<grid, kQT, 0, st>>>(p);
+    else if (p.align == 16) mxfp4_quantize_kernel<T, 16, U><<<grid, kQT, 0, st>>>(p);
+    else mxfp4_quantize_kernel<T, 0, U><<<grid, kQT, 0, st>>>(p);
+  }
 }
 
-// Two blocks a thread keep more bytes in flight; up to about four CTAs an SM
-// twice the threads do that better (bf16, us, two / one: 1 x 2816 2.5 / 2.1,
-// 1000 x 2816 3.4 / 3.1; 1000 x 2100 f32 5.4 / 5.2).
+// Two steps a thread keep more bytes in flight; up to four CTAs an SM more
+// threads do that better (us, two / one: 1000 x 2816 bf16 3.4 / 2.9, 1000 x 2100
+// f32 4.8 / 3.7, 8192 x 2816 bf16 8.4 / 8.7).
 template <typename T>
 void quantize_t(const QuantArgs& p, cudaStream_t st) {
-  if (p.rows * p.walked <= (int64_t)kSmallBlocks) quantize_u<T, 1>(p, st);
+  if (p.rows * p.nb <= (int64_t)kSmallBlocks) quantize_u<T, 1>(p, st);
   else quantize_u<T, 2>(p, st);
 }
 
