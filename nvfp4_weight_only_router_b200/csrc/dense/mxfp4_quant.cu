@@ -324,11 +324,11 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __
 }
 
 // Any K and alignment: a thread writes 8 consecutive values of the flat output,
-// which is 16-byte aligned.  Their codes lie in two words of the row and their
-// scales in two bytes; a group that runs over the end of its row goes value by
-// value.  Two groups a thread: one or four take 11% and 22% longer at 30000 x
-// 2817 f32 (76.1 us); a value per thread and store took 8.0 us at 1000 x 2100
-// f32 (5.6), this form for whole groups 83 us at 32768 x 2816 (63.5 above).
+// which is 16-byte aligned.  Their codes lie in two words of the row, or end one
+// row and begin the next, and their scales in two bytes or three (K < 8: value
+// by value).  Two groups a thread: one or four take 11% and 22% longer at 30000
+// x 2817 f32 (75 us); a value per thread and store took 8.0 us at 1000 x 2100
+// f32 (5.1), this form for whole groups 83 us at 32768 x 2816 (63.5 above).
 template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
@@ -337,21 +337,29 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t
   const uint32_t k = (uint32_t)K, words = (uint32_t)(4 * nb);
   const int64_t r0 = first / K;
   const uint32_t c0 = (uint32_t)(first - r0 * K);
-  uint32_t w[kAU], s0[kAU], s1[kAU], c[kAU];
+  uint32_t w[kAU], s0[kAU], s1[kAU], s2[kAU], c[kAU];
   int64_t row[kAU];
 #pragma unroll
   for (int u = 0; u < kAU; ++u) {
     const uint32_t i = c0 + (u * kQT + threadIdx.x) * 8, dr = i / k;
     row[u] = r0 + dr;
     c[u] = i - dr * k;
-    w[u] = s0[u] = s1[u] = 0;
-    if (row[u] < rows && c[u] + 8 <= k) {
+    w[u] = s0[u] = s1[u] = s2[u] = 0;
+    if (row[u] < rows && k >= 8) {
       const uint32_t* src = reinterpret_cast<const uint32_t*>(codes) + row[u] * words;
-      const uint32_t at = c[u] >> 3, sh = (c[u] & 7) * 4;
+      const uint8_t* sc = scales + row[u] * nb;
+      const uint32_t at = c[u] >> 3, sh = (c[u] & 7) * 4, valid = min(8u, k - c[u]);
       const uint32_t lo = __ldg(src + at);
-      w[u] = sh ? __funnelshift_r(lo, __ldg(src + at + 1), sh) : lo;
-      s0[u] = __ldg(scales + row[u] * nb + (c[u] >> 5));
-      s1[u] = __ldg(scales + row[u] * nb + ((c[u] + 7) >> 5));
+      w[u] = sh ? __funnelshift_r(lo, at + 1 < words ? __ldg(src + at + 1) : 0u, sh) : lo;
+      s0[u] = __ldg(sc + (c[u] >> 5));
+      s1[u] = __ldg(sc + ((c[u] + valid - 1) >> 5));
+      if (valid < 8) {
+        w[u] &= (1u << (4 * valid)) - 1u;
+        if (row[u] + 1 < rows) {
+          w[u] |= __ldg(src + words) << (4 * valid);
+          s2[u] = __ldg(sc + nb);
+        }
+      }
     }
   }
 #pragma unroll
@@ -359,19 +367,19 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t
     const int64_t at = first + (int64_t)(u * kQT + threadIdx.x) * 8;
     if (row[u] >= rows) continue;
     float v[8];
-    if (c[u] + 8 <= k) {
+    if (k >= 8) {
       uint32_t h[4];
       e2m1x8_to_f16x2(w[u], h);
-      const float a = mx_scale(s0[u]), b = mx_scale(s1[u]);
-      const uint32_t left = 32 - (c[u] & 31);  // values under the first scale
+      const float a = mx_scale(s0[u]), b = mx_scale(s1[u]), d = mx_scale(s2[u]);
+      const uint32_t left = 32 - (c[u] & 31), valid = k - c[u];  // values under the first scale, of this row
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpack16x2(h[i], true, v[2 * i], v[2 * i + 1]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= i < left ? a : b;
+      for (int i = 0; i < 8; ++i) v[i] *= i >= valid ? d : i < left ? a : b;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t j = c[u] + i, dr = j / k;  // K may be less than 8
+        const uint32_t j = c[u] + i, dr = j / k;
         v[i] = row[u] + dr < rows ? mx_value(codes, scales, row[u] + dr, j - dr * k, nb) : 0.f;
       }
     }
