@@ -207,6 +207,12 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
   if (T == 1) ldx = w->K;
   cudaStream_t s = as_stream(stream);
   if (few_tokens(T, w, act, false)) return cuda_status(launch_skinny(skinny_mx(x, ldx, T, w, act, dtype, y, false), s));
+#ifdef W4_FUSED
+  {
+    PairW4 a{x, ldx, w->codes, w->scales, T, act ? w->N / 2 : w->N, w->K, act, y};
+    return cuda_status(launch_pair_w4(a, device_status_ptr(), s));
+  }
+#endif
   cudaError_t e = launch_mxfp4_dequantize(w->codes, w->scales, w->N, w->K, ws, kBf16, s);
   if (e != cudaSuccess) return cuda_fail(e);
   if (act) {

@@ -133,6 +133,16 @@ struct PairGatedBwd {
   void *dg, *du;          // [T, pair_pitch(I)]
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
+// bf16 x MXFP4 weights, decoded on the way into the products
+struct PairW4 {
+  const void* x;
+  int64_t ldx;
+  const uint8_t *codes, *scales;  // [N (gated: 2 N), K]
+  int T, N, K;
+  int act;
+  void* y;
+};
+cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st);
 // MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns);
 // launched just behind launch_mxfp4_prep_a4
 struct PairMx {

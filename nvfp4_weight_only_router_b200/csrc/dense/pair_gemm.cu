@@ -40,15 +40,16 @@ namespace nvfp4moe {
 
 namespace {
 
-constexpr int kPThreads = 384;
 constexpr int kPProdA = 0, kPMma = 1, kPProdB = 2, kPScale = 3, kPEpi0 = 4, kPEpiWarps = 8;
+constexpr int kPConv0 = 12, kPConvWarps = 4;
 constexpr int kPTmem = 512;
 constexpr int kPOutB = 4096;  // output buffer of an epilogue warp: 32 rows x 64 columns
-constexpr int kKind16 = 0, kKindMx = 1;
+constexpr int kKind16 = 0, kKindMx = 1, kKindW4 = 2;
 constexpr int kEpiPlain = 0, kEpiGated = 1, kEpiGatedBwd = 2;
 
 template <int KIND, int BN>
 struct PCfg {
+  static constexpr int THREADS = 32 * (KIND == kKindW4 ? kPConv0 + kPConvWarps : kPConv0);
   // sub-stages of 128 bytes of K per stage: a stage's waits and commits take
   // about 320 cycles, more than the products of 64 x up to 128 columns
   static constexpr int KS = BN <= 128 ? 2 : 1;
@@ -89,6 +90,8 @@ struct alignas(64) PProb {
   int kc0, kc;             // K stages of segment 0 and in all
   int tm, t0;              // tiles along M; first tile in the list
   int a_mn, b_mn;
+  const uint8_t *wq, *ws;  // W4: codes and scales of B's rows (gated: gate, then up)
+  int K;                   // W4
   int tx;                  // bytes of a stage that complete on the barrier, of both SMs
 };
 
@@ -162,27 +165,11 @@ __device__ __forceinline__ void commit_here(uint64_t* bar) {  // arrives in this
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
+// On a barrier of either SM.  What the waiter goes on to touch is ordered by
+// the tcgen05 and proxy fences around, within each SM; a release at cluster
+// scope would order all memory, about 1000 cycles each time.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, uint64_t timeout_ns = kWaitTimeoutNs) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    if (try_wait_cluster(bar, parity)) return true;
-    if (globaltimer_ns() - t0 > timeout_ns) return false;
-  }
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mma16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -226,7 +213,7 @@ __device__ __forceinline__ uint64_t make_mn_desc(uint32_t smem_addr) {
 
 template <int KIND, int BN>
 __device__ __forceinline__ bool pwait(PSmem<KIND, BN>& sm, uint64_t* bar, uint32_t parity, int* status) {
-  if (wait_cluster(bar, parity)) return true;
+  if (mbar_wait_bounded(bar, parity)) return true;
   atomicExch(&sm.abort_flag, 1);
   record_status(status, kStatusTimeout);
   return false;
@@ -323,10 +310,11 @@ __device__ __forceinline__ void pack16(const float* v, bool f16, uint32_t (&w)[8
 
 // Epilogue of 16 hidden units of a row: h packed into w, and p and a written
 // where kept (blk, null where the warp's rows or the units lie outside).
+template <bool KEEP>  // whether e.kept may be given
 __device__ __forceinline__ void gate16(const PEpi& e, uint8_t* blk, int lane, const float* g, const float* u, bool f16,
                                        uint32_t (&w)[8]) {
   float v[16];
-  if (!e.kept) {
+  if (!KEEP || !e.kept) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = act_fwd(g[i], e.act) * u[i];
   } else {
@@ -356,7 +344,7 @@ __device__ __forceinline__ void gate16(const PEpi& e, uint8_t* blk, int lane, co
 }
 
 template <int KIND, int BN, int EPI, int NP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THREADS, 1)
     pair_gemm_kernel(const __grid_constant__ PParams<NP> p) {
   using C = PCfg<KIND, BN>;
   using Smem = PSmem<KIND, BN>;
@@ -370,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   // The first tile's description and descriptors are fetched while the pair
   // sets up: cold, they took 3300 cycles behind it.
   PTile tile = ptile<NP>(p, cluster);
-  if (warp == kPProdA || warp == kPProdB) {
+  if (warp == kPProdA || (KIND != kKindW4 && warp == kPProdB)) {
     const PProb& q = p.p[tile.prob];
     if (elect_one()) {
       prefetch_map(warp == kPProdA ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0]);
@@ -381,7 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(&sm.full[s], 1);
+      // W4: SM 0's producer and the converters of both SMs
+      mbar_init(&sm.full[s], KIND == kKindW4 ? 1 + 2 * kPConvWarps : 1);
       mbar_init(&sm.empty[s], 1);
       mbar_init(&sm.scaled[s], 1);
     }
@@ -407,7 +396,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
   // behind the kernel before, whose results are the operands
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == kPProdA || warp == kPProdB) {
+  if (warp == kPProdA || (KIND != kKindW4 && warp == kPProdB)) {
     // ------------------------------------------- TMA producers of A and of B
     const bool is_a = warp == kPProdA;
     const uint32_t full0 = leader_addr(&sm.full[0]), op0 = smem_u32(is_a ? sm.a[0][0] : sm.b[0][0]);
@@ -427,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       const int row = is_a ? d.m * 256 + (int)rank * 128
                            : EPI == kEpiGated ? d.n * (BN / 2) : d.n * BN + (int)rank * (BN / 2);
       const int sf_row = is_a ? row >> 7 : d.n * C::SFB_BLK;
-      const bool mn = KIND == kKind16 && (is_a ? q.a_mn : BN >= 128 && q.b_mn);
+      const bool mn = KIND != kKindMx && (is_a ? q.a_mn : BN >= 128 && q.b_mn);
       const int boxes = is_a ? 2 : BN / 128;  // 64-row boxes of an operand with K outermost
       const CUtensorMap* map = is_a ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0];
       for (int kc = 0, kk = 0; kc < kc_all; ++kc, kk += C::KS) {
@@ -444,7 +433,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
           for (int u = 0; u < C::KS; ++u) {
             if (!has) break;
             const uint32_t dst = op0 + (s * C::KS + u) * (is_a ? C::A_SUB : C::B_SUB);
-            if constexpr (KIND == kKind16) {
+            if constexpr (KIND != kKindMx) {
               if (mn) {
                 tma_load_pair(dst, map, row, (kk + u) * 64, bar);
                 if (boxes > 1) tma_load_pair(dst + 8192, map, row + 64, (kk + u) * 64, bar);
@@ -482,11 +471,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t dcol = taddr + (uint32_t)(db * BN);
-        const bool a_mn = KIND == kKind16 && q.a_mn, b_mn = KIND == kKind16 && q.b_mn;
+        const bool a_mn = KIND != kKindMx && q.a_mn, b_mn = KIND != kKindMx && q.b_mn;
         const int kc_all = q.kc;
         // D fp32 (kind::f16), M = 256, N = BN
         uint32_t idesc = ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-        if (KIND == kKind16) {
+        if (KIND != kKindMx) {
           idesc |= 1u << 4;
           if (!p.e.f16) idesc |= (1u << 7) | (1u << 10);
           idesc |= (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
@@ -507,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             for (int u = 0; u < C::KS; ++u) {
               const uint64_t ad = ad0 + (uint64_t)((s * C::KS + u) * (C::A_SUB >> 4));
               const uint64_t bd = bd0 + (uint64_t)((s * C::KS + u) * (C::B_SUB >> 4));
-              if constexpr (KIND == kKind16) {
+              if constexpr (KIND != kKindMx) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   mma16_pair(dcol, ad + (uint64_t)(k * astep), bd + (uint64_t)(k * bstep), idesc,
@@ -542,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       // every MMA issued has completed before the tear-down
       if (elect_one()) commit_pair(&sm.fin);
       __syncwarp();
-      wait_cluster(&sm.fin, 0);
+      mbar_wait_bounded(&sm.fin, 0);
       __syncwarp();
     }
   } else if (KIND == kKindMx && warp == kPScale) {
@@ -580,8 +569,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
       // the copies issued have completed before the tear-down
       if (elect_one()) commit_here(&sm.fin_sf);
       __syncwarp();
-      wait_cluster(&sm.fin_sf, 0);
+      mbar_wait_bounded(&sm.fin_sf, 0);
       __syncwarp();
+    }
+  } else if (KIND == kKindW4 && warp >= kPConv0) {
+    // ------------------------- MXFP4 weights into the stages' B tiles as bf16
+    // A thread has one block of 32 in each of NB rows of every stage.  It reads
+    // BATCH stages at once while it converts the BATCH before: loads that
+    // overlap one by one share their few scoreboards, and each wait is then for
+    // the latest (1900 cycles a stage).
+    constexpr int ROWS = BN / 2, BPR = 2 * C::KS;  // rows of this SM, blocks per row and stage
+    constexpr int NB = ROWS * BPR / (32 * kPConvWarps), DR = 32 * kPConvWarps / BPR;
+    constexpr int BATCH = NB == 1 ? 8 : 4;
+    struct Batch {
+      uint4 code[BATCH][NB];
+      uint32_t scale[BATCH][NB];
+    };
+    const int ct = threadIdx.x - kPConv0 * 32, r0 = ct / BPR, kb = ct % BPR;
+    const uint32_t full0 = leader_addr(&sm.full[0]);
+    const PProb& q = p.p[0];
+    const int K = q.K, kc_all = q.kc, N = q.N, units = K / 32;
+    const uint8_t* const wq = q.wq + (EPI == kEpiGated && rank ? (size_t)N * units * 16 : 0);
+    const uint8_t* const ws = q.ws + (EPI == kEpiGated && rank ? (size_t)N * units : 0);
+    // the next stage to read
+    int lt = cluster, lk = 0, lrow = 0;
+    auto first_row = [&](int t) {
+      const int n = ptile<NP>(p, t).n;
+      return (EPI == kEpiGated ? n * (BN / 2) : n * BN + (int)rank * (BN / 2)) + r0;
+    };
+    lrow = first_row(lt);
+    auto read = [&](Batch& b) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        const int unit = lk * BPR + kb;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int row = lrow + i * DR;
+          b.code[j][i] = make_uint4(0u, 0u, 0u, 0u);
+          b.scale[j][i] = 0u;
+          if (lt < p.n_tiles && row < N && unit < units) {
+            b.code[j][i] = ldg_nc_v4(wq + ((size_t)row * units + unit) * 16);
+            b.scale[j][i] = __ldg(ws + (size_t)row * units + unit);
+          }
+        }
+        if (++lk == kc_all) {
+          lk = 0;
+          lt += clusters;
+          if (lt < p.n_tiles) lrow = first_row(lt);
+        }
+      }
+    };
+    uint32_t s = 0, parity = 1;
+    int left = cluster < p.n_tiles ? ((p.n_tiles - cluster - 1) / clusters + 1) * kc_all : 0;
+    bool ok = true;
+    auto convert = [&](const Batch& b) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        if (left == 0 || !ok) break;
+        ok = swait(sm, &sm.empty[s], parity, p.status);
+        if (!ok) break;
+        uint8_t* dst = sm.b[s][kb >> 1];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int r = r0 + i * DR;
+          const MxFactor f = mx_factor(b.scale[j][i]);
+          const uint32_t w[4] = {b.code[j][i].x, b.code[j][i].y, b.code[j][i].z, b.code[j][i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[4];
+            mx_decode8(w[c], f, o);
+            // 128-byte rows, 16-byte pieces exchanged by row as TMA does
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((kb & 1) * 4 + c) ^ (r & 7)) * 16) =
+                make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                           __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+          }
+        }
+        out_ready();  // visible to the products
+        if (lane == 0) arrive_cluster(full0 + 8 * s);
+        if (++s == C::NS) {
+          s = 0;
+          parity ^= 1;
+        }
+        --left;
+      }
+    };
+    Batch even, odd;
+    read(even);
+    while (left > 0 && ok) {
+      read(odd);
+      convert(even);
+      read(even);
+      convert(odd);
     }
   } else if (warp >= kPEpi0) {
     // ------------------------------------------------------------ epilogue
@@ -633,7 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
             float g[16], u[16];
             tmem_ld16(tcol + c + k, g);
             tmem_ld16(tcol + BN / 2 + c + k, u);
-            gate16(p.e, p.e.kept ? kept_blk(n0 + c + k) : nullptr, lane, g, u, f16, w);
+            gate16<KIND == kKind16>(p.e, KIND == kKind16 && p.e.kept ? kept_blk(n0 + c + k) : nullptr, lane, g, u, f16, w);
           } else if constexpr (EPI == kEpiPlain) {
             if (k % 32 == 0) tmem_ld32(tcol + c + k, v32);
             pack16(v32 + k % 32, f16, w);
@@ -679,7 +757,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPThreads, 1)
     // copies in flight land before the pair leaves (SM 1's complete on SM 0's barriers)
     const int issued = max(sm.issued[0], sm.issued[1]);
     for (int it = max(0, issued - C::NS); it < issued; ++it)
-      wait_cluster(&sm.full[it % C::NS], (it / C::NS) & 1, kAbortDrainNs);
+      mbar_wait_bounded(&sm.full[it % C::NS], (it / C::NS) & 1, kAbortDrainNs);
   }
   __syncthreads();
   cluster_sync();
@@ -717,8 +795,8 @@ cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int6
     if (!map_out<EPI, BN>(&q.o[0], out[i], q.M, q.N, ld) ||
         (EPI == kEpiGatedBwd && !map_out<EPI, BN>(&q.o[1], out1, q.M, q.N, ld)))
       return cudaErrorInvalidValue;
-    const int a = q.a_mn ? C::A_SUB : a_box(q.M) * 128;
-    q.tx = C::KS * ((q.M > 128 ? 2 : 1) * (a + C::SFA_SUB) + 2 * (C::B_SUB + C::SFB_SUB));
+    const int a = q.a_mn ? C::A_SUB : a_box(q.M) * 128, b = KIND == kKindW4 ? 0 : C::B_SUB + C::SFB_SUB;
+    q.tx = C::KS * ((q.M > 128 ? 2 : 1) * (a + C::SFA_SUB) + 2 * b);
   }
   constexpr int smem = (int)sizeof(PSmem<KIND, BN>) + 1024;
   static_assert(smem <= 232448, "shared memory budget");
@@ -731,7 +809,7 @@ cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int6
   const int clusters = std::max(1, std::min(p.n_tiles, sms / 2));
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kPThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -758,6 +836,7 @@ struct Width {
 };
 constexpr Width kWidths16[] = {{256, 512, 3000}, {128, 290, 2000}, {64, 200, 1500}};
 constexpr Width kWidths16Mn[] = {{256, 540, 3000}, {128, 430, 2000}};  // an MN-major box is 64 columns of each SM's half
+constexpr Width kWidthsW4[] = {{256, 560, 3000}, {128, 290, 2000}, {64, 200, 1500}};
 constexpr Width kWidthsMx[] = {{192, 560, 3000}, {128, 480, 2000}, {64, 400, 1500}};
 struct Tiles {
   int64_t m, cols, subs;  // tiles along M, columns, sub-stages along K
@@ -895,6 +974,40 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   p.status = status;
   if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), false, st);
   return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), false, st);
+}
+
+cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t err = sm_count(&sms);
+  if (err != cudaSuccess) return err;
+  const bool gated = a.act != kActNone;
+  const int64_t tm = cdiv(a.T, 256);
+  const Tiles tiles{tm, gated ? 2 * (int64_t)a.N : a.N, cdiv(a.K, 64)};
+  const int bn = pick_bn(kWidthsW4, &tiles, 1, sms / 2);
+  PParams<1> p;
+  std::memset(&p, 0, sizeof(p));
+  PProb& q = p.p[0];
+  const PairOperand x{a.x, a.ldx, false};
+  if (!map16(&q.a[0], x, a.T, a.K, kBf16, a_box(a.T))) return cudaErrorInvalidValue;
+  q.wq = a.codes;
+  q.ws = a.scales;
+  q.K = a.K;
+  q.M = a.T;
+  q.N = a.N;
+  q.kc0 = q.kc = stages(cdiv(a.K, 64), bn);
+  q.tm = (int)tm;
+  p.e.act = a.act;
+  p.np = 1;
+  p.n_tiles = (int)(tm * cdiv(a.N, gated ? bn / 2 : bn));
+  p.status = status;
+  if (gated) {
+    if (bn == 64) return launch_pair<kKindW4, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
+    if (bn == 128) return launch_pair<kKindW4, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
+    return launch_pair<kKindW4, 256, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
+  }
+  if (bn == 64) return launch_pair<kKindW4, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
+  if (bn == 128) return launch_pair<kKindW4, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
+  return launch_pair<kKindW4, 256, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
 }
 
 int pair_mx_tile(int T, int N, int K, int act) {
