@@ -77,9 +77,9 @@ bool few_tokens(int32_t T, const mxfp4_weight* w, int32_t act, bool a4) {
   return skinny_fits(T, act ? w->N / 2 : w->N, act != kActNone, true, a4);
 }
 
-// W4A16 above the few-token kernel: the weight as bf16
-size_t linear_bytes(int32_t T, const mxfp4_weight* w, int32_t act) {
-  return few_tokens(T, w, act, false) ? 256 : round_up((size_t)w->N * w->K * 2, 256);
+// W4A16 of many tokens: the weight as bf16
+size_t linear_bytes(int32_t T, const mxfp4_weight* w) {
+  return T <= kPairW4MaxTokens ? 256 : round_up((size_t)w->N * w->K * 2, 256);
 }
 
 LinearLayout a4_layout(int32_t T, const mxfp4_weight* w, int32_t act) {
@@ -194,7 +194,7 @@ nvfp4_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64
 
 // ---------------------------------------------------------------- products
 size_t mxfp4_linear_workspace_bytes(int32_t T, const mxfp4_weight* w, int32_t act) {
-  return check_linear(T, w, act) == NVFP4_OK ? linear_bytes(T, w, act) : 0;
+  return check_linear(T, w, act) == NVFP4_OK ? linear_bytes(T, w) : 0;
 }
 
 nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, const mxfp4_weight* w, int32_t act,
@@ -202,17 +202,15 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
   NvtxRange nv("mxfp4_linear");
   nvfp4_status st = check_linear(T, w, act);
   if (st != NVFP4_OK) return st;
-  st = linear_checks(x, dtype, ldx, T, w, y, ws, ws_bytes, linear_bytes(T, w, act), false);
+  st = linear_checks(x, dtype, ldx, T, w, y, ws, ws_bytes, linear_bytes(T, w), false);
   if (st != NVFP4_OK || T == 0) return st;
   if (T == 1) ldx = w->K;
   cudaStream_t s = as_stream(stream);
   if (few_tokens(T, w, act, false)) return cuda_status(launch_skinny(skinny_mx(x, ldx, T, w, act, dtype, y, false), s));
-#ifdef W4_FUSED
-  {
-    PairW4 a{x, ldx, w->codes, w->scales, T, act ? w->N / 2 : w->N, w->K, act, y};
+  if (T <= kPairW4MaxTokens) {
+    const PairW4 a{x, ldx, w->codes, w->scales, T, act ? w->N / 2 : w->N, w->K, act, y};
     return cuda_status(launch_pair_w4(a, device_status_ptr(), s));
   }
-#endif
   cudaError_t e = launch_mxfp4_dequantize(w->codes, w->scales, w->N, w->K, ws, kBf16, s);
   if (e != cudaSuccess) return cuda_fail(e);
   if (act) {

@@ -133,7 +133,11 @@ struct PairGatedBwd {
   void *dg, *du;          // [T, pair_pitch(I)]
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
-// bf16 x MXFP4 weights, decoded on the way into the products
+// bf16 x MXFP4 weights, decoded on the way into the products: for one tile of
+// rows, since every further one decodes the weights again (us, decoded once into
+// bf16 / here: 2816 x 2112 T = 64 10.8 / 9.9, 4224 x 2816 gated T = 256 14.5 /
+// 12.5, 2816 x 8192 T = 64 26.2 / 23.1; 2816 x 2112 T = 512 12.7 / 15.5)
+constexpr int kPairW4MaxTokens = 256;
 struct PairW4 {
   const void* x;
   int64_t ldx;

@@ -1,8 +1,9 @@
 // Dense products on the 5th-generation tensor cores, two SMs per tile
 // (cta_group::2): D[256 rows, BN columns] += A[256, k] B[BN, k]^T with fp32
 // accumulators in tensor memory.  16-bit operands (kind::f16, 64 elements of K
-// per stage) or MXFP4 operands (kind::mxf4, E2M1 with an E8M0 scale per 32,
-// 256 elements per stage).
+// per sub-stage), 16-bit by MXFP4 weights decoded into the stages (the same
+// products), or MXFP4 operands (kind::mxf4, E2M1 with an E8M0 scale per 32, 256
+// elements per sub-stage).
 //
 // Bound by the tensor pipe, and for MXFP4 by the bytes an SM can draw from L2:
 // a stage's operands are read once per tile, so a pair of SMs shares one
@@ -25,13 +26,14 @@
 // Warps: 0 and 2 TMA producers of A and B (in both SMs), 1 MMA issuer (in SM 0
 // of the pair), 3 MXFP4 scales into tensor memory (likewise, ahead of the
 // products, whose issue they would delay), 4-11 epilogue: a warp per
-// tensor-memory lane quarter and column
-// half.  Two accumulators, so that a tile's epilogue overlaps the next tile's
+// tensor-memory lane quarter and column half, 12-15 (MXFP4 weights by 16-bit
+// rows) converters in place of B's producer.  Two accumulators, so that a tile's epilogue overlaps the next tile's
 // products (MXFP4 tiles have at most 192 columns: scales need tensor memory
 // too).  Every wait is bounded in wall time; one that gives up records a timeout
 // and the pair tears down.
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "../tc_common.cuh"
 #include "mxfp4_codec.cuh"
@@ -369,8 +371,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      // W4: SM 0's producer and the converters of both SMs
-      mbar_init(&sm.full[s], KIND == kKindW4 ? 1 + 2 * kPConvWarps : 1);
+      // W4: SM 0's producer and a converter of each SM
+      mbar_init(&sm.full[s], KIND == kKindW4 ? 3 : 1);
       mbar_init(&sm.empty[s], 1);
       mbar_init(&sm.scaled[s], 1);
     }
@@ -574,92 +576,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
     }
   } else if (KIND == kKindW4 && warp >= kPConv0) {
     // ------------------------- MXFP4 weights into the stages' B tiles as bf16
-    // A thread has one block of 32 in each of NB rows of every stage.  It reads
-    // BATCH stages at once while it converts the BATCH before: loads that
-    // overlap one by one share their few scoreboards, and each wait is then for
-    // the latest (1900 cycles a stage).
-    constexpr int ROWS = BN / 2, BPR = 2 * C::KS;  // rows of this SM, blocks per row and stage
-    constexpr int NB = ROWS * BPR / (32 * kPConvWarps), DR = 32 * kPConvWarps / BPR;
-    constexpr int BATCH = NB == 1 ? 8 : 4;
-    struct Batch {
-      uint4 code[BATCH][NB];
-      uint32_t scale[BATCH][NB];
-    };
-    const int ct = threadIdx.x - kPConv0 * 32, r0 = ct / BPR, kb = ct % BPR;
+    // A warp converts every fourth stage: what a stage costs besides its
+    // arithmetic (the wait, the fence, the arrival) then overlaps among the
+    // warps.  It reads its next stage while it converts one.
+    constexpr int ROWS = BN / 2, BPR = 2 * C::KS;        // rows of this SM, blocks of 32 per row and stage
+    constexpr int NB = ROWS * BPR / 32, DR = 32 / BPR;   // blocks per lane, rows between them
+    const int r0 = lane / BPR, kb = lane % BPR;
     const uint32_t full0 = leader_addr(&sm.full[0]);
     const PProb& q = p.p[0];
     const int K = q.K, kc_all = q.kc, N = q.N, units = K / 32;
     const uint8_t* const wq = q.wq + (EPI == kEpiGated && rank ? (size_t)N * units * 16 : 0);
     const uint8_t* const ws = q.ws + (EPI == kEpiGated && rank ? (size_t)N * units : 0);
-    // the next stage to read
-    int lt = cluster, lk = 0, lrow = 0;
-    auto first_row = [&](int t) {
-      const int n = ptile<NP>(p, t).n;
-      return (EPI == kEpiGated ? n * (BN / 2) : n * BN + (int)rank * (BN / 2)) + r0;
+    const int total = cluster < p.n_tiles ? ((p.n_tiles - cluster - 1) / clusters + 1) * kc_all : 0;
+    struct Stage {
+      uint4 code[NB];
+      uint32_t scale[NB];
     };
-    lrow = first_row(lt);
-    auto read = [&](Batch& b) {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        const int unit = lk * BPR + kb;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const int row = lrow + i * DR;
-          b.code[j][i] = make_uint4(0u, 0u, 0u, 0u);
-          b.scale[j][i] = 0u;
-          if (lt < p.n_tiles && row < N && unit < units) {
-            b.code[j][i] = ldg_nc_v4(wq + ((size_t)row * units + unit) * 16);
-            b.scale[j][i] = __ldg(ws + (size_t)row * units + unit);
-          }
-        }
-        if (++lk == kc_all) {
-          lk = 0;
-          lt += clusters;
-          if (lt < p.n_tiles) lrow = first_row(lt);
-        }
+    // the next stage to read
+    int lt = cluster, lk = warp - kPConv0, lrow = 0;
+    auto settle = [&]() {  // into the tile that holds it
+      while (lk >= kc_all) {
+        lk -= kc_all;
+        lt += clusters;
+      }
+      if (lt < p.n_tiles) {
+        const int n = ptile<NP>(p, lt).n;
+        lrow = (EPI == kEpiGated ? n * (BN / 2) : n * BN + (int)rank * (BN / 2)) + r0;
       }
     };
-    uint32_t s = 0, parity = 1;
-    int left = cluster < p.n_tiles ? ((p.n_tiles - cluster - 1) / clusters + 1) * kc_all : 0;
-    bool ok = true;
-    auto convert = [&](const Batch& b) {
+    settle();
+    auto read = [&](Stage& b) {
+      const int unit = lk * BPR + kb;
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        if (left == 0 || !ok) break;
-        ok = swait(sm, &sm.empty[s], parity, p.status);
-        if (!ok) break;
-        uint8_t* dst = sm.b[s][kb >> 1];
+      for (int i = 0; i < NB; ++i) {
+        const int row = lrow + i * DR;
+        b.code[i] = make_uint4(0u, 0u, 0u, 0u);
+        b.scale[i] = 0u;
+        if (lt < p.n_tiles && row < N && unit < units) {
+          b.code[i] = ldg_nc_v4(wq + ((size_t)row * units + unit) * 16);
+          b.scale[i] = __ldg(ws + (size_t)row * units + unit);
+        }
+      }
+      lk += kPConvWarps;
+      if (lk >= kc_all) settle();
+    };
+    auto convert = [&](const Stage& b, int it) {
+      const int s = it % C::NS;
+      if (!swait(sm, &sm.empty[s], ((it / C::NS) & 1) ^ 1, p.status)) return false;
+      uint8_t* const dst = sm.b[s][kb >> 1];
+      auto decode = [&](auto has_big) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const int r = r0 + i * DR;
-          const MxFactor f = mx_factor(b.scale[j][i]);
-          const uint32_t w[4] = {b.code[j][i].x, b.code[j][i].y, b.code[j][i].z, b.code[j][i].w};
+          const MxFactor f = mx_factor(b.scale[i]);
+          const uint32_t w[4] = {b.code[i].x, b.code[i].y, b.code[i].z, b.code[i].w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int q = 0; q < 4; ++q) {
             uint32_t o[4];
-            mx_decode8(w[c], f, o);
+            mx_decode8<decltype(has_big)::value>(w[q], f, o);
             // 128-byte rows, 16-byte pieces exchanged by row as TMA does
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((kb & 1) * 4 + c) ^ (r & 7)) * 16) =
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((kb & 1) * 4 + q) ^ (r & 7)) * 16) =
                 make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
                            __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
           }
         }
-        out_ready();  // visible to the products
-        if (lane == 0) arrive_cluster(full0 + 8 * s);
-        if (++s == C::NS) {
-          s = 0;
-          parity ^= 1;
-        }
-        --left;
-      }
+      };
+      bool big = false;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) big |= mx_big(b.scale[i]);
+      if (__any_sync(0xffffffffu, big)) decode(std::true_type{});
+      else decode(std::false_type{});
+      out_ready();  // visible to the products
+      if (lane == 0) arrive_cluster(full0 + 8 * s);
+      return true;
     };
-    Batch even, odd;
+    Stage even, odd;
     read(even);
-    while (left > 0 && ok) {
+    for (int it = warp - kPConv0; it < total; it += 2 * kPConvWarps) {
       read(odd);
-      convert(even);
+      if (!convert(even, it) || it + kPConvWarps >= total) break;
       read(even);
-      convert(odd);
+      if (!convert(odd, it + kPConvWarps)) break;
     }
   } else if (warp >= kPEpi0) {
     // ------------------------------------------------------------ epilogue
@@ -836,7 +833,7 @@ struct Width {
 };
 constexpr Width kWidths16[] = {{256, 512, 3000}, {128, 290, 2000}, {64, 200, 1500}};
 constexpr Width kWidths16Mn[] = {{256, 540, 3000}, {128, 430, 2000}};  // an MN-major box is 64 columns of each SM's half
-constexpr Width kWidthsW4[] = {{256, 560, 3000}, {128, 290, 2000}, {64, 200, 1500}};
+constexpr Width kWidthsW4[] = {{128, 400, 2000}, {64, 310, 1500}};
 constexpr Width kWidthsMx[] = {{192, 560, 3000}, {128, 480, 2000}, {64, 400, 1500}};
 struct Tiles {
   int64_t m, cols, subs;  // tiles along M, columns, sub-stages along K
@@ -1002,12 +999,10 @@ cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st) {
   p.status = status;
   if (gated) {
     if (bn == 64) return launch_pair<kKindW4, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
-    if (bn == 128) return launch_pair<kKindW4, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
-    return launch_pair<kKindW4, 256, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
+    return launch_pair<kKindW4, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
   }
   if (bn == 64) return launch_pair<kKindW4, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
-  if (bn == 128) return launch_pair<kKindW4, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
-  return launch_pair<kKindW4, 256, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
+  return launch_pair<kKindW4, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
 }
 
 int pair_mx_tile(int T, int N, int K, int act) {

@@ -23,6 +23,8 @@
 // after_producer: the launch may start while the kernel before it on the
 // stream still runs (programmatic dependent launch); weights are loaded
 // first, x only after that kernel's results are visible.
+#include <type_traits>
+
 #include "mxfp4_codec.cuh"
 
 namespace nvfp4moe {
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
       } else {
         const MxFactor fa = mx_factor(ca[u]), fb = mx_factor(cb[u]);
         MxFactor fx[NT8];
+        uint32_t bx[NT8];
         uint32_t xq[NT8][4];
         if constexpr (QX) {
 #pragma unroll
@@ -141,6 +144,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
             float lo, hi;
             unpack16x2(m2, p.f16, lo, hi);
             const uint32_t byte = mx_scale_byte(max(abs_bits(lo), abs_bits(hi)));
+            bx[j] = byte;
             fx[j] = mx_factor(byte);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -152,27 +156,38 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
           }
         }
         const uint32_t wav[4] = {va[u].x, va[u].y, va[u].z, va[u].w}, wbv[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
+        bool big = mx_big(ca[u]) || mx_big(cb[u]);
+        if constexpr (QX) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t a[4], b[4];
-          mx_decode8(wav[q], fa, a);
-          mx_decode8(wbv[q], fb, b);
-#pragma unroll
-          for (int j = 0; j < NT8; ++j) {
-            uint32_t o[4];
-            if constexpr (QX) {
-              mx_decode8(xq[j][q], fx[j], o);
-            } else {
-              const uint4 xw = xv[j][q];
-              o[0] = __byte_perm(xw.x, xw.z, 0x5410);
-              o[1] = __byte_perm(xw.x, xw.z, 0x7632);
-              o[2] = __byte_perm(xw.y, xw.w, 0x5410);
-              o[3] = __byte_perm(xw.y, xw.w, 0x7632);
-            }
-            mma16<false>(acc[j], a[0], b[0], a[1], b[1], o[0], o[1]);
-            mma16<false>(acc[j], a[2], b[2], a[3], b[3], o[2], o[3]);
-          }
+          for (int j = 0; j < NT8; ++j) big |= mx_big(bx[j]);
         }
+        auto products = [&](auto has_big) {
+          constexpr bool BIG = decltype(has_big)::value;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t a[4], b[4];
+            mx_decode8<BIG>(wav[q], fa, a);
+            mx_decode8<BIG>(wbv[q], fb, b);
+#pragma unroll
+            for (int j = 0; j < NT8; ++j) {
+              uint32_t o[4];
+              if constexpr (QX) {
+                mx_decode8<BIG>(xq[j][q], fx[j], o);
+              } else {
+                const uint4 xw = xv[j][q];
+                o[0] = __byte_perm(xw.x, xw.z, 0x5410);
+                o[1] = __byte_perm(xw.x, xw.z, 0x7632);
+                o[2] = __byte_perm(xw.y, xw.w, 0x5410);
+                o[3] = __byte_perm(xw.y, xw.w, 0x7632);
+              }
+              mma16<false>(acc[j], a[0], b[0], a[1], b[1], o[0], o[1]);
+              mma16<false>(acc[j], a[2], b[2], a[3], b[3], o[2], o[3]);
+            }
+          }
+        };
+        // four groups of tokens leave no registers for both forms
+        if (NT8 == 4 || __any_sync(0xffffffffu, big)) products(std::true_type{});
+        else products(std::false_type{});
       }
     }
   }
