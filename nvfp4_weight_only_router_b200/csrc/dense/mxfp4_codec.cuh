@@ -45,17 +45,17 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&v)[8], uint32_t byt
 // The two factors that turn a code's bits placed at a bf16's sign, two low
 // exponent bits and top mantissa bit (v 2^-126, subnormal codes included)
 // into v 2^X: 2^(126 + X) for X <= 1, and 2^127 followed by 2^(X - 1) above.
-// Scales above 2 are rare, so a warp that has none (mx_big) leaves the second
-// factor out; a branch for every word keeps the compiler from interleaving them.
-__device__ __forceinline__ bool mx_big(uint32_t byte) { return byte > 128u && byte != 255u; }
 struct MxFactor {
-  uint32_t f0, f1;  // bf16x2; f1 is 1 unless mx_big
+  uint32_t f0, f1;  // bf16x2; f1 applies where big
+  bool big;
 };
+__device__ __forceinline__ bool mx_big(uint32_t byte) { return byte > 128u && byte != 255u; }
 __device__ __forceinline__ MxFactor mx_factor(uint32_t byte) {
   MxFactor m;
   const uint32_t h = byte == 255u ? 0x7FFFu : (min(byte, 128u) + 126u) << 7;
   m.f0 = h | (h << 16);
-  const uint32_t b = mx_big(byte) ? (byte - 1u) << 7 : 0x3F80u;
+  m.big = mx_big(byte);
+  const uint32_t b = (byte - 1u) << 7;
   m.f1 = b | (b << 16);
   return m;
 }
@@ -67,10 +67,8 @@ __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
 }
 
 // Eight codes (a 32-bit word) -> four bf16x2 of elements (j, j + 4), j = 0..3,
-// scaled by 2^X (exact: E2M1 times a power of two is a bf16 unless it
-// overflows or lies below 2^-133).
-template <bool BIG>
-__device__ __forceinline__ void mx_decode8(uint32_t w, const MxFactor& m, uint32_t (&o)[4]) {
+// times the first factor.
+__device__ __forceinline__ void mx_place8(uint32_t w, const MxFactor& m, uint32_t (&o)[4]) {
   constexpr uint32_t M = 0x01C001C0u, S = 0x80008000u;
   o[0] = ((w << 6) & M) | ((w << 12) & S);
   o[1] = ((w << 2) & M) | ((w << 8) & S);
@@ -78,7 +76,12 @@ __device__ __forceinline__ void mx_decode8(uint32_t w, const MxFactor& m, uint32
   o[3] = ((w >> 6) & M) | (w & S);
 #pragma unroll
   for (int j = 0; j < 4; ++j) o[j] = bmul2(o[j], m.f0);
-  if (BIG) {
+}
+// The values (exact: E2M1 times a power of two is a bf16 unless it overflows or
+// lies below 2^-133).
+__device__ __forceinline__ void mx_decode8(uint32_t w, const MxFactor& m, uint32_t (&o)[4]) {
+  mx_place8(w, m, o);
+  if (m.big) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = bmul2(o[j], m.f1);
   }

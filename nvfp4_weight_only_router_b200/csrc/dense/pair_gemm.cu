@@ -624,6 +624,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
       const int s = it % C::NS;
       if (!swait(sm, &sm.empty[s], ((it / C::NS) & 1) ^ 1, p.status)) return false;
       uint8_t* const dst = sm.b[s][kb >> 1];
+      // a warp without scales above 2 leaves the second factor out: as a branch
+      // for every word it keeps the compiler from interleaving them
       auto decode = [&](auto has_big) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
@@ -633,7 +635,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t o[4];
-            mx_decode8<decltype(has_big)::value>(w[q], f, o);
+            mx_place8(w[q], f, o);
+            if constexpr (decltype(has_big)::value) {
+              const uint32_t f1 = f.big ? f.f1 : 0x3F803F80u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[j] = bmul2(o[j], f1);
+            }
             // 128-byte rows, 16-byte pieces exchanged by row as TMA does
             *reinterpret_cast<uint4*>(dst + r * 128 + (((kb & 1) * 4 + q) ^ (r & 7)) * 16) =
                 make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),

@@ -23,8 +23,6 @@
 // after_producer: the launch may start while the kernel before it on the
 // stream still runs (programmatic dependent launch); weights are loaded
 // first, x only after that kernel's results are visible.
-#include <type_traits>
-
 #include "mxfp4_codec.cuh"
 
 namespace nvfp4moe {
@@ -132,7 +130,6 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
       } else {
         const MxFactor fa = mx_factor(ca[u]), fb = mx_factor(cb[u]);
         MxFactor fx[NT8];
-        uint32_t bx[NT8];
         uint32_t xq[NT8][4];
         if constexpr (QX) {
 #pragma unroll
@@ -144,7 +141,6 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
             float lo, hi;
             unpack16x2(m2, p.f16, lo, hi);
             const uint32_t byte = mx_scale_byte(max(abs_bits(lo), abs_bits(hi)));
-            bx[j] = byte;
             fx[j] = mx_factor(byte);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -156,38 +152,27 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
           }
         }
         const uint32_t wav[4] = {va[u].x, va[u].y, va[u].z, va[u].w}, wbv[4] = {vb[u].x, vb[u].y, vb[u].z, vb[u].w};
-        bool big = mx_big(ca[u]) || mx_big(cb[u]);
-        if constexpr (QX) {
 #pragma unroll
-          for (int j = 0; j < NT8; ++j) big |= mx_big(bx[j]);
-        }
-        auto products = [&](auto has_big) {
-          constexpr bool BIG = decltype(has_big)::value;
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[4], b[4];
+          mx_decode8(wav[q], fa, a);
+          mx_decode8(wbv[q], fb, b);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t a[4], b[4];
-            mx_decode8<BIG>(wav[q], fa, a);
-            mx_decode8<BIG>(wbv[q], fb, b);
-#pragma unroll
-            for (int j = 0; j < NT8; ++j) {
-              uint32_t o[4];
-              if constexpr (QX) {
-                mx_decode8<BIG>(xq[j][q], fx[j], o);
-              } else {
-                const uint4 xw = xv[j][q];
-                o[0] = __byte_perm(xw.x, xw.z, 0x5410);
-                o[1] = __byte_perm(xw.x, xw.z, 0x7632);
-                o[2] = __byte_perm(xw.y, xw.w, 0x5410);
-                o[3] = __byte_perm(xw.y, xw.w, 0x7632);
-              }
-              mma16<false>(acc[j], a[0], b[0], a[1], b[1], o[0], o[1]);
-              mma16<false>(acc[j], a[2], b[2], a[3], b[3], o[2], o[3]);
+          for (int j = 0; j < NT8; ++j) {
+            uint32_t o[4];
+            if constexpr (QX) {
+              mx_decode8(xq[j][q], fx[j], o);
+            } else {
+              const uint4 xw = xv[j][q];
+              o[0] = __byte_perm(xw.x, xw.z, 0x5410);
+              o[1] = __byte_perm(xw.x, xw.z, 0x7632);
+              o[2] = __byte_perm(xw.y, xw.w, 0x5410);
+              o[3] = __byte_perm(xw.y, xw.w, 0x7632);
             }
+            mma16<false>(acc[j], a[0], b[0], a[1], b[1], o[0], o[1]);
+            mma16<false>(acc[j], a[2], b[2], a[3], b[3], o[2], o[3]);
           }
-        };
-        // four groups of tokens leave no registers for both forms
-        if (NT8 == 4 || __any_sync(0xffffffffu, big)) products(std::true_type{});
-        else products(std::false_type{});
+        }
       }
     }
   }
@@ -244,12 +229,12 @@ cudaError_t launch_nt(const SkinnyParams& p, int T, bool after, cudaStream_t st)
 
 // Measured against the tensor-core kernels (whole calls, us, N x K, `silu`
 // gated): the crossing lies where a group's CTAs no longer fit the SMs at once
-// (2 on each), or, with x quantised in every CTA, where a second group comes.
-//   W4A16  T = 32:  8192 x 2816 17.6 / 21.3, 2816 x 2112  8.1 / 11.8
-//          T = 64:  2816 x 2112 13.6 / 11.8 (two waves), 1024 x 1024 3.5 / 7.7
-//          T = 128: 512 x 2816 silu 6.0 / 11.4 (one wave)
-//   W4A4   T = 8:   4224 x 2816 silu 7.1 / 9.9, 8192 x 2816 11.7 / 10.6 (two waves)
-//          T = 16:  1024 x 1024 3.7 / 6.7, 2816 x 2112 8.6 / 8.4; T = 32: 13.8 / 8.4
+// (2 on each), or, with x quantised in every CTA, where there is more than one.
+//   W4A16  T = 32:  8192 x 2816 17.6 / 18, 2816 x 2112 8.4 / 9.7
+//          T = 64:  2816 x 2112 13.6 / 9.7 (two waves), 1024 x 1024 3.8 / 7.3
+//          T = 128: 512 x 2816 silu 6.4 / 11.0 (one wave)
+//   W4A4   T = 8:   4224 x 2816 silu 7.3 / 8.6, 8192 x 2816 11.7 / 9.2 (two waves)
+//          T = 16:  1024 x 1024 3.7 / 5.8 (a CTA an SM), 2816 x 2112 8.6 / 7.2 (two)
 //   16-bit gated block, H = 2816: T = 16, I = 2112 12.8 / 18.6; T = 64, I = 256
 //          11.8 / 14.1 (one wave); T = 32, I = 8192 / H = 2816 55.1 / 47.1 (two waves)
 bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x) {
@@ -257,9 +242,9 @@ bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x) {
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) sms = 148;
   const int rows = gated ? 8 : 16;
-  const bool one_wave = (int64_t)((N + rows - 1) / rows) * ((T + 31) / 32) <= 2 * sms;
-  if (quant_x) return T <= 16 && one_wave;
-  return T <= (mx ? 32 : 16) || (one_wave && T <= (mx ? 128 : 64));
+  const int64_t ctas = (int64_t)((N + rows - 1) / rows) * ((T + 31) / 32);
+  if (quant_x) return T <= 16 && ctas <= (T <= 8 ? 2 * sms : sms);
+  return T <= (mx ? 32 : 16) || (ctas <= 2 * sms && T <= (mx ? 128 : 64));
 }
 
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
