@@ -23,6 +23,8 @@
 // after_producer: the launch may start while the kernel before it on the
 // stream still runs (programmatic dependent launch); weights are loaded
 // first, x only after that kernel's results are visible.
+#include <algorithm>
+
 #include "mxfp4_codec.cuh"
 
 namespace nvfp4moe {
@@ -46,18 +48,61 @@ struct SkinnyParams {
   int T, N, units;   // units: 16-byte pieces of a weight row
   int act;
   bool f16;          // type of y (and of x)
+  bool after;        // x is written by the kernel before
 };
 
-// CODEC 0: 16-bit weights (bf16, or f16 with F16); 1: MXFP4 (bf16 products;
-// QX quantises x, of either 16-bit type).
-template <int CODEC, int NT8, bool GATED, bool OPT>
+// Steps of K in flight per warp: for one group of tokens the whole K of the
+// layer's sizes, for more what the registers allow.
+template <int CODEC, int NT8, bool XS>
+struct SkCfg {
+  static constexpr int U = CODEC == 1 ? 3 : (NT8 == 1 ? 11 : 6);
+  static constexpr int XW = CODEC == 1 ? 4 : 1;  // 16-byte pieces of x per step and token
+  static constexpr int XPASS = kSkWarps * U * 4 * XW * 16, XPITCH = XPASS + 32;  // bytes of a token
+  static constexpr int RED = kSkWarps * NT8 * 32 * 16;                           // the partial tiles
+  static int smem(int T) { return XS ? std::max(RED, std::min(T, NT8 * 8) * XPITCH) : RED; }
+};
+
+// 8 elements of x in shared memory -> the bf16 values that MXFP4 keeps of them
+// (exact).  A quad of lanes has a block; the whole warp takes part.
+__device__ __forceinline__ void quantize_in_place(uint8_t* at, bool valid, bool f16) {
+  uint4* const p = reinterpret_cast<uint4*>(at);
+  const uint4 x = valid ? *p : make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
+  float lo, hi;
+  unpack16x2(m2, f16, lo, hi);
+  uint32_t m = max(abs_bits(lo), abs_bits(hi));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t byte = mx_scale_byte(m);
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) unpack16x2(w[k], f16, v[2 * k], v[2 * k + 1]);
+  uint32_t o[4];
+  mx_decode8(mx_encode8(v, byte), mx_factor(byte), o);
+  if (valid)
+    *p = make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                    __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+}
+
+// CODEC 0: 16-bit weights (bf16, or f16 with OPT); 1: MXFP4 (bf16 products; OPT
+// quantises x, of either 16-bit type).
+// XS: a pass's part of x is copied to shared memory at once, behind the loads of
+// the weights, instead of one dependent load a step.  For 16-bit weights and up
+// to 8 tokens: a load in each of 11 steps took 2 us more (a block of 2816 x 2112
+// at T = 1: 10.4 and 8.2 us).  With MXFP4 weights there are 3 steps, and the copy
+// takes 0.4 us more than it saves, unless x is to be quantised for one token,
+// which the CTA's threads then share (4224 x 2816 gated: T = 1 7.0 and 6.1 us,
+// T = 4 7.2 and 8.3).
+template <int CODEC, int NT8, bool GATED, bool OPT, bool XS>
 __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
   constexpr bool F16 = CODEC == 0 && OPT, QX = CODEC == 1 && OPT;
-  // steps of K in flight per warp: for one group of tokens the whole K of the
-  // layer's sizes, for more what the registers allow
-  constexpr int U = CODEC == 1 ? 3 : (NT8 == 1 ? 11 : 6);
-  constexpr int XW = CODEC == 1 ? 4 : 1;  // 16-byte pieces of x per step and token
-  __shared__ float4 red[kSkWarps][NT8][32];
+  using C = SkCfg<CODEC, NT8, XS>;
+  constexpr int U = C::U, XW = C::XW;
+  extern __shared__ __align__(16) uint8_t xs[];
+  auto red = reinterpret_cast<float4(*)[NT8][32]>(xs);  // behind the last pass
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -84,7 +129,20 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
 
   const int steps = (p.units + 3) / 4;
   bool first = true;
-  for (int s0 = warp; s0 < steps; s0 += kSkWarps * U) {
+  for (int base = 0; base < steps; base += kSkWarps * U) {
+    const int s0 = base + warp;
+    // pieces of a token in this pass
+    const int u0 = 4 * base, n = min((p.units - u0) * XW, C::XPASS / 16), nt = min(T, NT8 * 8);
+    auto copy_x = [&]() {
+      for (int i = threadIdx.x; i < nt * n; i += kSkThreads) {
+        const int t = i / n, k = i - t * n;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(xs + t * C::XPITCH + k * 16)),
+                     "l"(px + (size_t)t * p.ldx_bytes + ((size_t)u0 * XW + k) * 16)
+                     : "memory");
+      }
+    };
+    if (XS && !first) __syncthreads();  // the pass before has read its part
+    if (XS && (!first || !p.after)) copy_x();
     uint4 va[U], vb[U];
     uint32_t ca[U], cb[U];
 #pragma unroll
@@ -101,10 +159,20 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
         }
       }
     }
-    if (first) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      first = false;
+    if (first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (XS) {
+      if (first && p.after) copy_x();
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncthreads();
+      if constexpr (QX) {
+        for (int i0 = 0; i0 < nt * n; i0 += kSkThreads) {
+          const int i = i0 + threadIdx.x, t = i / n, k = i - t * n;
+          quantize_in_place(xs + t * C::XPITCH + k * 16, i < nt * n, p.f16);
+        }
+        __syncthreads();
+      }
     }
+    first = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int unit = 4 * (s0 + u * kSkWarps) + c;
@@ -117,7 +185,9 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
         for (int i = 0; i < XW; ++i) {
           xv[j][i] = make_uint4(0u, 0u, 0u, 0u);
           // plain loads: x may have been written by the kernel before
-          if (t < T && unit < p.units)
+          if (XS && t < T && unit < p.units)
+            xv[j][i] = *reinterpret_cast<const uint4*>(xs + t * C::XPITCH + ((unit - u0) * XW + i) * 16);
+          if (!XS && t < T && unit < p.units)
             xv[j][i] = *reinterpret_cast<const uint4*>(px + (size_t)t * p.ldx_bytes + ((size_t)unit * XW + i) * 16);
         }
       }
@@ -131,7 +201,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
         const MxFactor fa = mx_factor(ca[u]), fb = mx_factor(cb[u]);
         MxFactor fx[NT8];
         uint32_t xq[NT8][4];
-        if constexpr (QX) {
+        if constexpr (QX && !XS) {
 #pragma unroll
           for (int j = 0; j < NT8; ++j) {
             const uint32_t* w = reinterpret_cast<const uint32_t*>(&xv[j][0]);
@@ -160,7 +230,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
 #pragma unroll
           for (int j = 0; j < NT8; ++j) {
             uint32_t o[4];
-            if constexpr (QX) {
+            if constexpr (QX && !XS) {
               mx_decode8(xq[j][q], fx[j], o);
             } else {
               const uint4 xw = xv[j][q];
@@ -176,9 +246,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
       }
     }
   }
-  // y may still be read by the kernel before (a user's buffer): no store ahead of it
-  if (first) asm volatile("griddepcontrol.wait;" ::: "memory");
-
+  if (XS) __syncthreads();
 #pragma unroll
   for (int j = 0; j < NT8; ++j) red[warp][j][lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
   __syncthreads();
@@ -208,21 +276,36 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
   }
 }
 
-template <int CODEC, bool GATED, bool OPT>
-cudaError_t launch_nt(const SkinnyParams& p, int T, bool after, cudaStream_t st) {
+template <int CODEC, int NT8, bool GATED, bool OPT, bool XS>
+cudaError_t launch_one(const SkinnyParams& p, cudaStream_t st) {
+  auto fn = skinny_kernel<CODEC, NT8, GATED, OPT, XS>;
+  using C = SkCfg<CODEC, NT8, XS>;
+  cudaError_t err = configure_kernel_once((const void*)fn, C::smem(NT8 * 8));
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   const int rows = GATED ? 8 : 16;
-  cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows), (unsigned)((T + 31) / 32));
+  cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows), (unsigned)((p.T + 31) / 32));
   cfg.blockDim = dim3(kSkThreads);
+  cfg.dynamicSmemBytes = C::smem(p.T);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
-  if (T <= 8) return cudaLaunchKernelEx(&cfg, skinny_kernel<CODEC, 1, GATED, OPT>, p);
-  if (T <= 16) return cudaLaunchKernelEx(&cfg, skinny_kernel<CODEC, 2, GATED, OPT>, p);
-  return cudaLaunchKernelEx(&cfg, skinny_kernel<CODEC, 4, GATED, OPT>, p);
+  cfg.numAttrs = p.after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, p);
+}
+
+template <int CODEC, bool GATED, bool OPT>
+cudaError_t launch_nt(const SkinnyParams& p, cudaStream_t st) {
+  constexpr bool QX = CODEC == 1 && OPT;
+  if constexpr (QX) {
+    if (p.T == 1) return launch_one<CODEC, 1, GATED, OPT, true>(p, st);
+  }
+  if (p.T <= 8) return launch_one<CODEC, 1, GATED, OPT, CODEC == 0>(p, st);
+  if (p.T <= 16) return launch_one<CODEC, 2, GATED, OPT, false>(p, st);
+  if constexpr (QX) return cudaErrorInvalidValue;  // skinny_fits: at most 16 tokens
+  else return launch_one<CODEC, 4, GATED, OPT, false>(p, st);
 }
 
 }  // namespace
@@ -265,13 +348,14 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   p.N = a.N;
   p.act = a.act;
   p.f16 = a.dtype == kF16;
+  p.after = a.after_producer;
   const bool opt = a.mx ? a.quant_x : p.f16;
   if (a.mx) {
-    if (gated) return opt ? launch_nt<1, true, true>(p, a.T, a.after_producer, st) : launch_nt<1, true, false>(p, a.T, a.after_producer, st);
-    return opt ? launch_nt<1, false, true>(p, a.T, a.after_producer, st) : launch_nt<1, false, false>(p, a.T, a.after_producer, st);
+    if (gated) return opt ? launch_nt<1, true, true>(p, st) : launch_nt<1, true, false>(p, st);
+    return opt ? launch_nt<1, false, true>(p, st) : launch_nt<1, false, false>(p, st);
   }
-  if (gated) return opt ? launch_nt<0, true, true>(p, a.T, a.after_producer, st) : launch_nt<0, true, false>(p, a.T, a.after_producer, st);
-  return opt ? launch_nt<0, false, true>(p, a.T, a.after_producer, st) : launch_nt<0, false, false>(p, a.T, a.after_producer, st);
+  if (gated) return opt ? launch_nt<0, true, true>(p, st) : launch_nt<0, true, false>(p, st);
+  return opt ? launch_nt<0, false, true>(p, st) : launch_nt<0, false, false>(p, st);
 }
 
 }  // namespace nvfp4moe
