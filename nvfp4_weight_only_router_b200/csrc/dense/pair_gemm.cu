@@ -489,8 +489,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
         const uint64_t ad0 = a_mn ? make_mn_desc(a0) : make_sw128_desc(a0);
         const uint64_t bd0 = b_mn ? make_mn_desc(b0) : make_sw128_desc(b0);
         for (int kc = 0; kc < kc_all; ++kc) {
-          ok = swait(sm, &sm.full[s], parity, p.status);
-          if (KIND == kKindMx && ok) ok = swait(sm, &sm.scaled[s], parity, p.status);
+          // MXFP4: the warp that copies the scales has waited for the stage
+          ok = swait(sm, KIND == kKindMx ? &sm.scaled[s] : &sm.full[s], parity, p.status);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
