@@ -20,8 +20,8 @@
  * valid: nothing is read, and only outputs that do not depend on tokens are
  * written (weight gradients: zeros).  Row strides (ldx) are in elements: at
  * least the row length and, except in mxfp4_quantize, a multiple of 8.
- * Results do not depend on other rows of the call, and two equal calls give
- * equal bits.
+ * A row's results do not depend on the values of other rows of the call, and two
+ * equal calls give equal bits.
  */
 #ifndef NVFP4DENSE_H
 #define NVFP4DENSE_H
@@ -77,7 +77,8 @@ typedef struct {
 
 /* ---------------------------------------------------------------------------
  * mxfp4_linear (W4A16): y = x W^T, bf16 x [T, K] and y, products of the exact
- * weight values with fp32 accumulation, one rounding.  With an activation W
+ * weight values (magnitudes of 2^128 and above, which mxfp4_quantize does not
+ * write, are infinite) with fp32 accumulation, one rounding.  With an activation W
  * stacks N/2 gate rows over N/2 up rows and y [T, N/2] = act(x Wg^T) * (x Wu^T).
  * dtype: BF16.  T <= 2^20.
  * mxfp4_linear_a4 (W4A4): x (bf16 or f16, y alike) is first quantised as by

@@ -22,8 +22,13 @@ import dataclasses
 import torch
 
 from . import dense_capi as dc
-from . import _dense_calls as _calls  # after dense_capi, which loads its library
 from .dense_capi import check
+
+try:
+    from . import _dense_calls as _calls  # after dense_capi, which loads its library
+except ImportError as e:
+    raise ImportError("_dense_calls is missing or was built for another torch: build it with "
+                      "`python -m nvfp4_weight_only_router_b200.build --force`") from e
 
 _DTYPE = {torch.bfloat16: dc.BF16, torch.float16: dc.F16, torch.float32: dc.F32}
 _ACT = {None: dc.ACT_NONE, "gelu_tanh": dc.ACT_GELU_TANH, "silu": dc.ACT_SILU}
@@ -160,6 +165,9 @@ class Mxfp4Weight:
         object.__setattr__(self, "_at", ctypes.addressof(self._c))
         object.__setattr__(self, "_device", self.codes.get_device())
 
+    def __reduce__(self):  # copies point to their own arrays
+        return Mxfp4Weight, (self.codes, self.scales, self.K)
+
     @property
     def N(self) -> int:
         return self.codes.shape[0]
@@ -193,7 +201,7 @@ def _linear(name, call, size, x, weight, act, stream):
 
 def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A16: y [T, N] = x weight^T for bf16 x [T, K]; with an activation the
-    gated form y [T, N/2] = act(x Wg^T) * (x Wu^T)."""
+    gated form y [T, N/2] = act(x Wg^T) * (x Wu^T).  Not differentiable."""
     act = _act(activation)
     if stream is None:
         y = _calls.linear(x, weight._at, weight._device, act, False)
@@ -302,6 +310,8 @@ class _GatedFfn(torch.autograd.Function):
 def gated_ffn(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
               activation: str = "gelu_tanh") -> torch.Tensor:
     """gated_ffn_forward as a differentiable torch operation, for x [..., H].
-    First derivatives only."""
+    First derivatives only.  As with every torch operation, a backward pass can
+    be captured into a graph only where no earlier autograd graph of the same
+    leaves is alive; gated_ffn_forward and gated_ffn_backward have no such limit."""
     y = _GatedFfn.apply(x.reshape(-1, x.shape[-1]).contiguous(), gate, up, down, activation)
     return y.view(x.shape)

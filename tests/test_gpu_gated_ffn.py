@@ -36,7 +36,8 @@ def _check_step(x, gate, up, down, dy, act):
 
 @pytest.mark.parametrize("dtype", [BF, F16])
 @pytest.mark.parametrize("T,H,I", [(1, 64, 64), (7, 8, 8), (9, 72, 136), (32, 256, 200), (33, 256, 200), (100, 520, 264),
-                                   (129, 128, 1000), (255, 640, 64), (300, 2816, 704)])
+                                   (129, 128, 1000), (255, 640, 64), (300, 2816, 704), (1, 4000, 72), (6, 5000, 3400),
+                                   (13, 4000, 72), (25, 2832, 3000), (60, 4000, 72), (100, 2000, 6000)])
 def test_forward(dev, T, H, I, dtype):
     x, gate, up, down, _ = _make(T, T, H, I, dtype, dev)
     for act in ("gelu_tanh", "silu"):
@@ -139,6 +140,41 @@ def test_autograd(dev):
     assert torch.equal(xi.grad, ref[0])
     with torch.no_grad():
         assert not lib.gated_ffn(xi, gate, up, down, "silu").requires_grad
+
+
+def test_shared_weights(dev):
+    """One tensor as gate and up: its gradient is the sum of both."""
+    x, w, _, down, dy = _make(10, 50, 72, 136, BF, dev)
+    leaf = w.clone().requires_grad_()
+    lib.gated_ffn(x, leaf, leaf, down).backward(dy)
+    y, saved = lib.gated_ffn_forward(x, w, w, down, save=True)
+    _, dgate, dup, _ = lib.gated_ffn_backward(dy, x, w, w, down, saved)
+    assert torch.equal(leaf.grad, dgate + dup)
+
+
+def test_refusals(dev):
+    x, gate, up, down, dy = _make(11, 40, 64, 48, BF, dev)
+    y, saved = lib.gated_ffn_forward(x, gate, up, down, save=True)
+    bad = (lambda: lib.gated_ffn_forward(x[:, :32], gate, up, down), lambda: lib.gated_ffn_forward(x.to(F16), gate, up, down),
+           lambda: lib.gated_ffn_forward(x, gate, up, down.T), lambda: lib.gated_ffn_forward(x, gate, up[:40], down),
+           lambda: lib.gated_ffn_forward(x, gate.T.contiguous().T, up, down), lambda: lib.gated_ffn_forward(x, gate, up, down, None),
+           lambda: lib.gated_ffn_forward(x[:1].expand(40, 64), gate, up, down),
+           lambda: lib.gated_ffn_forward(x.cpu(), gate, up, down), lambda: lib.gated_ffn_forward(x[0], gate, up, down),
+           lambda: lib.gated_ffn_backward(dy[:39], x, gate, up, down, saved),
+           lambda: lib.gated_ffn_backward(dy, x, gate, up, down, saved[:-1]),
+           lambda: lib.gated_ffn_backward(dy, x, gate, up, down, saved.view(torch.int8)),
+           lambda: lib.gated_ffn_backward(dy, x[:33], gate, up, down, saved))
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: lib.gated_ffn_forward(x.reshape(-1)[8 * 64 - 60:][:64 * 30].view(30, 64), gate, up, down),  # rows off the grid
+                 lambda: lib.gated_ffn_forward(x[:, :60].contiguous(), gate[:, :60].contiguous(), up[:, :60].contiguous(),
+                                               down[:60].contiguous())):
+        with pytest.raises(lib.NVFP4Error):
+            call()
+    # nothing was enqueued, and the library still answers
+    assert lib.device_status() == 0
+    assert torch.equal(lib.gated_ffn_forward(x, gate, up, down, save=True)[0], y)
 
 
 @pytest.mark.parametrize("T", [3, 200])

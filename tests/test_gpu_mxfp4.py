@@ -66,6 +66,23 @@ def test_quantize_strided_and_unaligned(dev):
     assert lib.mxfp4_quantize(base[:0])[0].shape == (0, 112)
 
 
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("rows,K", [(2500, 2112), (2500, 2104), (2500, 2100), (2311, 2101), (160001, 37), (700001, 5)])
+def test_quantize_many_blocks(dev, dtype, rows, K):
+    """Whole and ragged rows on and off the 32- and 16-byte grids, with the steps
+    that a large tensor takes; and back, across the ends of rows."""
+    x = _randn(rows + K, (rows, K), dtype, dev)
+    codes, scales = lib.mxfp4_quantize(x)
+    v = lib.mxfp4_dequantize(codes, scales, K)
+    assert torch.equal(v.double(), R.mx_round(x))
+    assert torch.equal(lib.mxfp4_dequantize(codes, scales, K, BF), v.to(BF))
+    # the part past K of each row's last block holds zeros
+    if K % 32:
+        last = codes.view(rows, -1, 16)[:, -1].to(torch.int32)
+        nibbles = torch.stack((last & 15, last >> 4), -1).view(rows, 32)
+        assert (nibbles[:, K % 32:] == 0).all()
+
+
 def test_quantize_past_32_bit_offsets(dev):
     """More than 2^31 elements: the last rows as their own call gives them."""
     rows, K = (1 << 31) // 2048 + 64, 2048
@@ -127,6 +144,49 @@ def test_linear_large(dev, T, N, K, act):
     _check(x, weight, w64, act, True)
 
 
+@pytest.mark.parametrize("T,N,K,act", [(200, 9472, 160, None), (200, 9472, 160, "silu"), (1000, 3456, 288, None),
+                                       (100, 12000, 96, None), (70, 12032, 224, "gelu_tanh")])
+def test_linear_tile_widths(dev, T, N, K, act):
+    """Sizes at which each tile width is taken that the others do not reach, and
+    several tiles of one row block on a cluster."""
+    weight, w64 = _weight(N, N, K, dev, K ** -0.5)
+    x = _randn(T, (T, K), BF, dev)
+    _check(x, weight, w64, act, False)
+    _check(x, weight, w64, act, True)
+    _check(x.to(F16), weight, w64, act, True)
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+@pytest.mark.parametrize("N,K", [(48, 4128), (208, 6400)])
+@pytest.mark.parametrize("T", [1, 2, 5, 12, 30, 60])
+def test_linear_long_rows(dev, T, N, K, act):
+    """Rows of weights longer than a CTA keeps in flight at once."""
+    weight, w64 = _weight(N + K, N, K, dev, K ** -0.5)
+    x = _randn(T, (T, K), BF, dev)
+    _check(x, weight, w64, act, False)
+    _check(x, weight, w64, act, True)
+    _check(x.to(F16), weight, w64, act, True)
+
+
+@pytest.mark.parametrize("T", [1, 7, 20, 100, 300])
+def test_linear_every_scale(dev, T):
+    """Every scale byte that the quantiser writes (0 to 252), the smallest with
+    large activations, the largest with small ones."""
+    N, K = 256, 64
+    gen = torch.Generator(dev).manual_seed(T)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=dev, generator=gen)
+    byte = torch.arange(N, device=dev, dtype=torch.int32).clamp(max=252)
+    scales = byte.to(torch.uint8)[:, None].expand(N, K // 32).contiguous()
+    weight = lib.Mxfp4Weight(codes, scales, K)
+    w64 = torch.from_numpy(R.mx_decode(codes.cpu().numpy(), scales.cpu().numpy(), K)).to(dev)
+    for rows, s in ((slice(0, 128), 2.0 ** 60), (slice(128, 256), 2.0 ** -60)):
+        x = _randn(T, (T, K), BF, dev, s)
+        for a4, f in ((False, lib.mxfp4_linear), (True, lib.mxfp4_linear_a4)):
+            y = f(x, weight)[:, rows]
+            ref, bound = R.linear64(R.mx_round(x) if a4 else x.double(), w64[rows], None, BF)
+            R.assert_within(y, ref, bound, f"a4 {a4} {s}")
+
+
 @pytest.mark.parametrize("T", [3, 70])
 def test_linear_scale_range(dev, T):
     """Block scales over most of the byte's range, above and below the point
@@ -169,6 +229,8 @@ def test_linear_strides_streams_and_repeats(dev, T):
     wide = _randn(11, (T + 2, 400), BF, dev)
     x = wide[1:T + 1, 16:144]
     for a4, f in ((False, lib.mxfp4_linear), (True, lib.mxfp4_linear_a4)):
+        odd = wide[1:T + 1, 24:152]                                    # rows on the 16-byte grid alone
+        assert torch.equal(_check(odd, weight, w64, None, a4), f(odd.contiguous(), weight))
         y = _check(x, weight, w64, None, a4)
         assert torch.equal(y, f(x.contiguous(), weight)) and torch.equal(y, f(x, weight))
         s = torch.cuda.Stream()
@@ -195,3 +257,18 @@ def test_linear_strides_streams_and_repeats(dev, T):
         lib.mxfp4_linear(x, weight, activation="relu")
     with pytest.raises(ValueError):
         lib.mxfp4_linear(x[:, :96], weight)
+
+
+def test_weight_copies(dev):
+    """Copies of a weight hold their own arrays."""
+    import copy
+    import pickle
+    weight, _ = _weight(12, 64, 96, dev)
+    x = _randn(13, (40, 96), BF, dev)
+    y = lib.mxfp4_linear(x, weight)
+    for other in (copy.deepcopy(weight), pickle.loads(pickle.dumps(weight))):
+        assert other.codes.data_ptr() != weight.codes.data_ptr()
+        before = other.codes.clone()
+        weight.codes.zero_()
+        assert torch.equal(other.codes, before) and torch.equal(lib.mxfp4_linear(x, other), y)
+        weight.codes.copy_(before)
