@@ -98,7 +98,7 @@ inline int64_t pair_pitch(int64_t I) { return (I + 63) / 64 * 64; }
 // outermost, edges padded) as an epilogue warp holds them, a row per lane:
 // 32 x 32 bytes of p's upper 16 bits, as many of a's, 32 x 16 bytes of p's
 // lower 8 bits and of a's.
-constexpr int kKeptBlockB = 3072;
+constexpr int kKeptBlockB = 32 * 16 * 6;
 struct PairKept {
   uint8_t *h, *blocks;
   size_t bytes;

@@ -124,8 +124,8 @@ def test_ffn_refusals(dc, codes):
     assert bwd(T=100, n=n - 1) == c.NVFP4_ERR_WORKSPACE
     assert bwd(saved=P + 16) == c.NVFP4_ERR_ALIGNMENT
     # h in 16 bits with rows of whole 128-byte lines, and blocks of 32 rows x 16 hidden units in 2 x 24
-    assert dc.gated_ffn_saved_bytes(100, ctypes.byref(_f(dc))) == 12800 + 4 * 4 * 3072
-    assert dc.gated_ffn_saved_bytes(3, ctypes.byref(_f(dc, I=8))) == 512 + 3072
+    assert dc.gated_ffn_saved_bytes(100, ctypes.byref(_f(dc))) == 12800 + 4 * 4 * (32 * 16 * 6)
+    assert dc.gated_ffn_saved_bytes(3, ctypes.byref(_f(dc, I=8))) == 512 + 32 * 16 * 6
     assert dc.gated_ffn_saved_bytes(0, ctypes.byref(_f(dc))) == 256
     assert dc.gated_ffn_saved_bytes(100, ctypes.byref(_f(dc, I=4))) == 0
     assert dc.gated_ffn_backward_workspace_bytes(100, ctypes.byref(_f(dc, I=4))) == 0
