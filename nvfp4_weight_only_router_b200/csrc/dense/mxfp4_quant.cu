@@ -177,6 +177,8 @@ constexpr int kPrepU = 2;  // steps of the kernel that prepares a product
 
 template <typename T, int ALIGN, int U>
 __global__ void __launch_bounds__(kQT) mxfp4_quantize_kernel(QuantArgs p) {
+  after_previous();
+  let_next();
   quant_cta<T, ALIGN, false, U>(p, blockIdx.x);
 }
 
@@ -184,6 +186,8 @@ __global__ void __launch_bounds__(kQT) mxfp4_quantize_kernel(QuantArgs p) {
 // steps with their loads issued together; a quad of lanes is in one block.
 template <typename T, int ALIGN, int U>
 __global__ void __launch_bounds__(kQT) mxfp4_quantize_quad_kernel(QuantArgs p) {
+  after_previous();
+  let_next();
   const uint32_t per = (uint32_t)(4 * p.nb);
   const int64_t first = (int64_t)blockIdx.x * (kQT * U);
   const int64_t r0 = first / per;
@@ -224,7 +228,8 @@ struct TileScales {
 // scales of 4 blocks of one row).
 template <typename T, int ALIGN>
 __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qblocks, TileScales t) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product sets up meanwhile
+  after_previous();
+  let_next();
   if ((int64_t)blockIdx.x < qblocks) {
     quant_cta<T, ALIGN, true, kPrepU>(p, blockIdx.x);
     return;
@@ -269,7 +274,8 @@ template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ scales, int64_t rows,
                                                                int64_t K, T* __restrict__ out) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // a product may set up meanwhile
+  after_previous();
+  let_next();
   constexpr int G = 32 / sizeof(T);
   const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * kDGroups;
   const uint32_t gpr = (uint32_t)(K / G);
@@ -333,6 +339,8 @@ template <typename T>
 __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t* __restrict__ codes,
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
                                                                    int64_t K, T* __restrict__ out) {
+  after_previous();
+  let_next();
   const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * (kAGroups * 8), n = rows * K;
   const uint32_t k = (uint32_t)K, words = (uint32_t)(4 * nb);
   const int64_t r0 = first / K;
@@ -407,17 +415,19 @@ int row_align(const void* p, int64_t ld, int elsize) {
 }
 
 template <typename T, int U>
-void quantize_u(const QuantArgs& p, cudaStream_t st) {
+cudaError_t quantize_u(const QuantArgs& p, cudaStream_t st) {
   if constexpr (sizeof(T) == 4) {
     const unsigned grid = blocks_for(p.rows * p.nb * 4, U * kQT);
-    if (p.align == 32) mxfp4_quantize_quad_kernel<T, 32, U><<<grid, kQT, 0, st>>>(p);
-    else if (p.align == 16) mxfp4_quantize_quad_kernel<T, 16, U><<<grid, kQT, 0, st>>>(p);
-    else mxfp4_quantize_quad_kernel<T, 0, U><<<grid, kQT, 0, st>>>(p);
+    auto fn = p.align == 32   ? mxfp4_quantize_quad_kernel<T, 32, U>
+              : p.align == 16 ? mxfp4_quantize_quad_kernel<T, 16, U>
+                              : mxfp4_quantize_quad_kernel<T, 0, U>;
+    return launch_overlapped(fn, grid, 1, kQT, 0, st, p);
   } else {
     const unsigned grid = blocks_for(p.rows * p.nb, U * kQT);
-    if (p.align == 32) mxfp4_quantize_kernel<T, 32, U><<<grid, kQT, 0, st>>>(p);
-    else if (p.align == 16) mxfp4_quantize_kernel<T, 16, U><<<grid, kQT, 0, st>>>(p);
-    else mxfp4_quantize_kernel<T, 0, U><<<grid, kQT, 0, st>>>(p);
+    auto fn = p.align == 32   ? mxfp4_quantize_kernel<T, 32, U>
+              : p.align == 16 ? mxfp4_quantize_kernel<T, 16, U>
+                              : mxfp4_quantize_kernel<T, 0, U>;
+    return launch_overlapped(fn, grid, 1, kQT, 0, st, p);
   }
 }
 
@@ -425,18 +435,18 @@ void quantize_u(const QuantArgs& p, cudaStream_t st) {
 // threads do that better (us, two / one: 1000 x 2816 bf16 3.4 / 2.9, 1000 x 2100
 // f32 4.8 / 3.7, 8192 x 2816 bf16 8.4 / 8.7).
 template <typename T>
-void quantize_t(const QuantArgs& p, cudaStream_t st) {
-  if (p.rows * p.nb <= (int64_t)kSmallBlocks) quantize_u<T, 1>(p, st);
-  else quantize_u<T, 2>(p, st);
+cudaError_t quantize_t(const QuantArgs& p, cudaStream_t st) {
+  return p.rows * p.nb <= (int64_t)kSmallBlocks ? quantize_u<T, 1>(p, st) : quantize_u<T, 2>(p, st);
 }
 
 template <typename T>
-void dequantize_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, T* out, cudaStream_t st) {
+cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, T* out, cudaStream_t st) {
   constexpr int G = 32 / sizeof(T);
   if (K % G == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0)
-    mxfp4_dequantize_kernel<T><<<blocks_for(rows * (K / G), kDGroups), kQT, 0, st>>>(codes, scales, rows, K, out);
-  else
-    mxfp4_dequantize_any_kernel<T><<<blocks_for(rows * K, kAGroups * 8), kQT, 0, st>>>(codes, scales, rows, K, out);
+    return launch_overlapped(mxfp4_dequantize_kernel<T>, blocks_for(rows * (K / G), kDGroups), 1, kQT, 0, st, codes,
+                             scales, rows, K, out);
+  return launch_overlapped(mxfp4_dequantize_any_kernel<T>, blocks_for(rows * K, kAGroups * 8), 1, kQT, 0, st, codes,
+                           scales, rows, K, out);
 }
 
 }  // namespace
@@ -452,17 +462,14 @@ cudaError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_
   p.scales = scales;
   p.nb = p.walked = mx_blocks(K);
   p.align = row_align(x, ldx, dtype == kF32 ? 4 : 2);
-  if (dtype == kF32) quantize_t<float>(p, st);
-  else if (dtype == kF16) quantize_t<__half>(p, st);
-  else quantize_t<__nv_bfloat16>(p, st);
-  return cudaGetLastError();
+  if (dtype == kF32) return quantize_t<float>(p, st);
+  return dtype == kF16 ? quantize_t<__half>(p, st) : quantize_t<__nv_bfloat16>(p, st);
 }
 
 cudaError_t launch_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t K, void* out,
                                     int dtype, cudaStream_t st) {
-  if (dtype == kF32) dequantize_t(codes, scales, rows, K, static_cast<float*>(out), st);
-  else dequantize_t(codes, scales, rows, K, static_cast<__nv_bfloat16*>(out), st);
-  return cudaGetLastError();
+  return dtype == kF32 ? dequantize_t(codes, scales, rows, K, static_cast<float*>(out), st)
+                       : dequantize_t(codes, scales, rows, K, static_cast<__nv_bfloat16*>(out), st);
 }
 
 cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st) {
@@ -480,14 +487,10 @@ cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st) {
   const TileScales t{a.wscales, a.wsf, mx_wsf_blocks(a.N, a.gated, a.bn) * p.sf_chunks * 128, a.N, a.bn, a.gated};
   const unsigned grid = (unsigned)qb + blocks_for(t.words, kQT);
   // x's rows are 16-byte aligned (checked by the entry point)
-  if (row_align(a.x, a.ldx, 2) == 32) {
-    if (a.dtype == kF16) mxfp4_prep_kernel<__half, 32><<<grid, kQT, 0, st>>>(p, qb, t);
-    else mxfp4_prep_kernel<__nv_bfloat16, 32><<<grid, kQT, 0, st>>>(p, qb, t);
-  } else {
-    if (a.dtype == kF16) mxfp4_prep_kernel<__half, 16><<<grid, kQT, 0, st>>>(p, qb, t);
-    else mxfp4_prep_kernel<__nv_bfloat16, 16><<<grid, kQT, 0, st>>>(p, qb, t);
-  }
-  return cudaGetLastError();
+  const bool wide = row_align(a.x, a.ldx, 2) == 32;
+  auto fn = a.dtype == kF16 ? (wide ? mxfp4_prep_kernel<__half, 32> : mxfp4_prep_kernel<__half, 16>)
+                            : (wide ? mxfp4_prep_kernel<__nv_bfloat16, 32> : mxfp4_prep_kernel<__nv_bfloat16, 16>);
+  return launch_overlapped(fn, grid, 1, kQT, 0, st, p, qb, t);
 }
 
 }  // namespace nvfp4moe

@@ -357,7 +357,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // The first tile's description and descriptors are fetched while the pair
   // sets up: cold, they took 3300 cycles behind it.
@@ -397,8 +396,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
   cluster_sync();
   tc_fence_after();
   const uint32_t taddr = sm.taddr;
-  // behind the kernel before, whose results are the operands
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
+  let_next();
 
   if (warp == kPProdA || (KIND != kKindW4 && warp == kPProdB)) {
     // ------------------------------------------- TMA producers of A and of B
@@ -790,10 +789,8 @@ bool map_out(CUtensorMap* m, void* out, int M, int N, int64_t ld) {
 }
 
 // ldo: the outputs' row pitch in elements, 0 for N.
-// `after`: behind the kernel launched just before on the stream, whose tail this
-// one's set-up may overlap
 template <int KIND, int BN, int EPI, int NP>
-cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int64_t ldo, bool after, cudaStream_t st) {
+cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int64_t ldo, cudaStream_t st) {
   using C = PCfg<KIND, BN>;
   for (int i = 0; i < p.np; ++i) {
     PProb& q = p.p[i];
@@ -813,17 +810,7 @@ cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int6
   err = sm_count(&sms);
   if (err != cudaSuccess) return err;
   const int clusters = std::max(1, std::min(p.n_tiles, sms / 2));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fn, p);
+  return launch_overlapped(fn, 2 * clusters, 1, C::THREADS, smem, st, p);
 }
 
 bool map16(CUtensorMap* m, const PairOperand& o, int rows, int K, int dtype, int box_rows) {
@@ -881,7 +868,7 @@ int stages(int64_t subs, int bn) { return (int)(bn <= 128 ? cdiv(subs, 2) : subs
 
 }  // namespace
 
-cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, int* status, cudaStream_t st) {
+cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st) {
   if (n < 1 || n > kPairMaxProblems) return cudaErrorInvalidValue;
   int sms = 0;
   cudaError_t err = sm_count(&sms);
@@ -921,9 +908,9 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, bool after, in
   p.np = n;
   p.n_tiles = t0;
   p.status = status;
-  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, after, st);
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, after, st);
-  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, after, st);
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, st);
+  return launch_pair<kKind16, 256, kEpiPlain, kPairMaxProblems>(p, out, nullptr, 0, st);
 }
 
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) {
@@ -950,9 +937,9 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn / 2));
   p.status = status;
-  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, a.after_producer, st);
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, a.after_producer, st);
-  return launch_pair<kKind16, 256, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, a.after_producer, st);
+  if (bn == 64) return launch_pair<kKind16, 64, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, st);
+  return launch_pair<kKind16, 256, kEpiGated, 1>(p, {a.h}, nullptr, a.ldh, st);
 }
 
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st) {
@@ -978,8 +965,8 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
   p.np = 1;
   p.n_tiles = (int)(tm * cdiv(a.I, bn));
   p.status = status;
-  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), false, st);
-  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), false, st);
+  if (bn == 128) return launch_pair<kKind16, 128, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), st);
+  return launch_pair<kKind16, 256, kEpiGatedBwd, 1>(p, {a.dg}, a.du, pair_pitch(a.I), st);
 }
 
 cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st) {
@@ -1007,11 +994,11 @@ cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st) {
   p.n_tiles = (int)(tm * cdiv(a.N, gated ? bn / 2 : bn));
   p.status = status;
   if (gated) {
-    if (bn == 64) return launch_pair<kKindW4, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
-    return launch_pair<kKindW4, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, false, st);
+    if (bn == 64) return launch_pair<kKindW4, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, st);
+    return launch_pair<kKindW4, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, st);
   }
-  if (bn == 64) return launch_pair<kKindW4, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
-  return launch_pair<kKindW4, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, false, st);
+  if (bn == 64) return launch_pair<kKindW4, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, st);
+  return launch_pair<kKindW4, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, st);
 }
 
 int pair_mx_tile(int T, int N, int K, int act) {
@@ -1050,13 +1037,13 @@ cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {
   p.n_tiles = (int)(tm * tiles_n);
   p.status = status;
   if (gated) {
-    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, true, st);
-    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, true, st);
-    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, {a.y}, nullptr, 0, true, st);
+    if (bn == 64) return launch_pair<kKindMx, 64, kEpiGated, 1>(p, {a.y}, nullptr, 0, st);
+    if (bn == 128) return launch_pair<kKindMx, 128, kEpiGated, 1>(p, {a.y}, nullptr, 0, st);
+    return launch_pair<kKindMx, 192, kEpiGated, 1>(p, {a.y}, nullptr, 0, st);
   }
-  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, true, st);
-  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, true, st);
-  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, {a.y}, nullptr, 0, true, st);
+  if (bn == 64) return launch_pair<kKindMx, 64, kEpiPlain, 1>(p, {a.y}, nullptr, 0, st);
+  if (bn == 128) return launch_pair<kKindMx, 128, kEpiPlain, 1>(p, {a.y}, nullptr, 0, st);
+  return launch_pair<kKindMx, 192, kEpiPlain, 1>(p, {a.y}, nullptr, 0, st);
 }
 
 }  // namespace nvfp4moe

@@ -20,9 +20,8 @@
 // block of x per token: it quantises it to MXFP4 and back in registers (the
 // values are bf16 exactly), so the W4A4 product of few tokens is this kernel too.
 //
-// after_producer: the launch may start while the kernel before it on the
-// stream still runs (programmatic dependent launch); weights are loaded
-// first, x only after that kernel's results are visible.
+// after_producer: weights are loaded while the kernel before on the stream still
+// runs, x once its results are visible.
 #include <algorithm>
 
 #include "mxfp4_codec.cuh"
@@ -105,7 +104,8 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
   auto red = reinterpret_cast<float4(*)[NT8][32]>(xs);  // behind the last pass
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!p.after) after_previous();
+  let_next();
 
   // this CTA's tokens
   const uint8_t* px = p.x + (size_t)blockIdx.y * (NT8 * 8) * p.ldx_bytes;
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
         }
       }
     }
-    if (first) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (first && p.after) after_previous();
     if constexpr (XS) {
       if (first && p.after) copy_x();
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -282,18 +282,9 @@ cudaError_t launch_one(const SkinnyParams& p, cudaStream_t st) {
   using C = SkCfg<CODEC, NT8, XS>;
   cudaError_t err = configure_kernel_once((const void*)fn, C::smem(NT8 * 8));
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
   const int rows = GATED ? 8 : 16;
-  cfg.gridDim = dim3((unsigned)((p.N + rows - 1) / rows), (unsigned)((p.T + 31) / 32));
-  cfg.blockDim = dim3(kSkThreads);
-  cfg.dynamicSmemBytes = C::smem(p.T);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.after ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, fn, p);
+  return launch_overlapped(fn, (unsigned)((p.N + rows - 1) / rows), (unsigned)((p.T + 31) / 32), kSkThreads,
+                           C::smem(p.T), st, p);
 }
 
 template <int CODEC, bool GATED, bool OPT>

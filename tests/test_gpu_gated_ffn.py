@@ -195,3 +195,31 @@ def test_train_quantise_serve(dev, T):
         yref, yb = R.linear64(q(h), dn.dequantize().double(), None, BF)   # from the served h
         R.assert_within(y, yref, yb, "y")
     assert lib.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 6, 40, 300])
+def test_back_to_back_calls(dev, T):
+    """Calls in a row overlap at their ends: weights and tokens written by the
+    kernel just before, outputs in memory that the call before still reads."""
+    sets = [_make(20 + i, T, 256, 192, BF, dev) for i in range(4)]
+
+    def chain(x, gate, up, down):
+        gu, dn = lib.Mxfp4Weight.quantize(torch.cat((gate, up))), lib.Mxfp4Weight.quantize(down)
+        h = lib.mxfp4_linear(x, gu, "silu")
+        y = lib.mxfp4_linear_a4(h, dn)
+        z = lib.gated_ffn_forward(y, gate, up, down)                  # h, y and the codes are freed as they are used
+        return lib.mxfp4_linear(lib.gated_ffn_forward(z, gate, up, down), gu, "silu")
+    ref = []
+    for x, gate, up, down, _ in sets:
+        ref.append(chain(x, gate, up, down))
+        torch.cuda.synchronize()
+    xs, gs, us, ds = (torch.empty_like(t) for t in sets[0][:4])
+    got = []
+    for i in range(60):
+        for dst, src in zip((xs, gs, us, ds), sets[i % 4]):
+            dst.copy_(src)
+        got.append(chain(xs, gs, us, ds))
+        lib.mxfp4_dequantize(*lib.mxfp4_quantize(got[-1]))            # its memory is the next call's
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, ref[i % 4]), i
