@@ -3,6 +3,7 @@
 // include/nvfp4dense.h.
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../../include/nvfp4dense.h"
@@ -39,6 +40,17 @@ int* nvfp4moe::device_status_ptr() {
     g_status_ptr[dev] = static_cast<int*>(p);
   }
   return g_status_ptr[dev];
+}
+
+int nvfp4moe::sms() {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  if (sm_count(&n) != cudaSuccess) return 148;
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 namespace {

@@ -48,6 +48,10 @@ inline int64_t mx_wsf_blocks(int N, bool gated, int bn) {
 }
 cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
 
+// SMs of the current device, asked for once per device (148 where there is none:
+// workspace queries answer without a GPU)
+int sms();
+
 // ---------------------------------------------------------------- skinny.cu
 // whether launch_skinny is the faster kernel for a product (N: output columns)
 bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x);

@@ -806,10 +806,7 @@ cudaError_t launch_pair(PParams<NP>& p, void* const (&out)[NP], void* out1, int6
   auto fn = pair_gemm_kernel<KIND, BN, EPI, NP>;
   cudaError_t err = configure_kernel_once((const void*)fn, smem);
   if (err != cudaSuccess) return err;
-  int sms = 0;
-  err = sm_count(&sms);
-  if (err != cudaSuccess) return err;
-  const int clusters = std::max(1, std::min(p.n_tiles, sms / 2));
+  const int clusters = std::max(1, std::min(p.n_tiles, sms() / 2));
   return launch_overlapped(fn, 2 * clusters, 1, C::THREADS, smem, st, p);
 }
 
@@ -870,9 +867,6 @@ int stages(int64_t subs, int bn) { return (int)(bn <= 128 ? cdiv(subs, 2) : subs
 
 cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, cudaStream_t st) {
   if (n < 1 || n > kPairMaxProblems) return cudaErrorInvalidValue;
-  int sms = 0;
-  cudaError_t err = sm_count(&sms);
-  if (err != cudaSuccess) return err;
   bool mn = false;
   for (int i = 0; i < n; ++i)
     for (int s = 0; s < g[i].nseg; ++s) mn |= g[i].seg[s].b.mn;
@@ -881,7 +875,7 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
     tiles[i] = Tiles{cdiv(g[i].M, 256), g[i].N, 0};
     for (int s = 0; s < g[i].nseg; ++s) tiles[i].subs += cdiv(g[i].seg[s].K, 64);
   }
-  const int bn = mn ? pick_bn(kWidths16Mn, tiles, n, sms / 2) : pick_bn(kWidths16, tiles, n, sms / 2);
+  const int bn = mn ? pick_bn(kWidths16Mn, tiles, n, sms() / 2) : pick_bn(kWidths16, tiles, n, sms() / 2);
   PParams<kPairMaxProblems> p;
   std::memset(&p, 0, sizeof(p));
   void* out[kPairMaxProblems] = {};
@@ -914,12 +908,9 @@ cudaError_t launch_pair_gemm(const PairGemm* g, int n, int dtype, int* status, c
 }
 
 cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) {
-  int sms = 0;
-  cudaError_t err = sm_count(&sms);
-  if (err != cudaSuccess) return err;
   const int64_t tm = cdiv(a.T, 256);
   const Tiles tiles{tm, 2 * (int64_t)a.I, cdiv(a.K, 64)};
-  const int bn = pick_bn(kWidths16, &tiles, 1, sms / 2);
+  const int bn = pick_bn(kWidths16, &tiles, 1, sms() / 2);
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
@@ -943,12 +934,9 @@ cudaError_t launch_pair_gated(const PairGated& a, int* status, cudaStream_t st) 
 }
 
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st) {
-  int sms = 0;
-  cudaError_t err = sm_count(&sms);
-  if (err != cudaSuccess) return err;
   const int64_t tm = cdiv(a.T, 256);
   const Tiles tiles{tm, a.I, cdiv(a.H, 64)};
-  const int bn = pick_bn(kWidths16Mn, &tiles, 1, sms / 2);
+  const int bn = pick_bn(kWidths16Mn, &tiles, 1, sms() / 2);
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
@@ -970,13 +958,10 @@ cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream
 }
 
 cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st) {
-  int sms = 0;
-  cudaError_t err = sm_count(&sms);
-  if (err != cudaSuccess) return err;
   const bool gated = a.act != kActNone;
   const int64_t tm = cdiv(a.T, 256);
   const Tiles tiles{tm, gated ? 2 * (int64_t)a.N : a.N, cdiv(a.K, 64)};
-  const int bn = pick_bn(kWidthsW4, &tiles, 1, sms / 2);
+  const int bn = pick_bn(kWidthsW4, &tiles, 1, sms() / 2);
   PParams<1> p;
   std::memset(&p, 0, sizeof(p));
   PProb& q = p.p[0];
@@ -1002,10 +987,8 @@ cudaError_t launch_pair_w4(const PairW4& a, int* status, cudaStream_t st) {
 }
 
 int pair_mx_tile(int T, int N, int K, int act) {
-  int sms = 0;
-  if (sm_count(&sms) != cudaSuccess) sms = 148;
   const Tiles tiles{cdiv(T, 256), act != kActNone ? 2 * (int64_t)N : N, cdiv(K, 256)};
-  return pick_bn(kWidthsMx, &tiles, 1, sms / 2);
+  return pick_bn(kWidthsMx, &tiles, 1, sms() / 2);
 }
 
 cudaError_t launch_pair_mx(const PairMx& a, int* status, cudaStream_t st) {

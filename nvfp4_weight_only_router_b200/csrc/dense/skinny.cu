@@ -313,12 +313,10 @@ cudaError_t launch_nt(const SkinnyParams& p, cudaStream_t st) {
 //          11.8 / 14.1 (one wave); T = 32, I = 8192 / H = 2816 55.1 / 47.1 (two waves)
 bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x) {
   if (T > 128) return false;
-  int sms = 0;
-  if (sm_count(&sms) != cudaSuccess) sms = 148;
-  const int rows = gated ? 8 : 16;
+  const int n = sms(), rows = gated ? 8 : 16;
   const int64_t ctas = (int64_t)((N + rows - 1) / rows) * ((T + 31) / 32);
-  if (quant_x) return T <= 16 && ctas <= (T <= 8 ? 2 * sms : sms);
-  return T <= (mx ? 32 : 16) || (ctas <= 2 * sms && T <= (mx ? 128 : 64));
+  if (quant_x) return T <= 16 && ctas <= (T <= 8 ? 2 * n : n);
+  return T <= (mx ? 32 : 16) || (ctas <= 2 * n && T <= (mx ? 128 : 64));
 }
 
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
