@@ -3,8 +3,8 @@
 // Through ctypes the same steps take 9 to 18 us of host time, more than the
 // kernels of few tokens take on the GPU.
 //
-// Every function returns None where an argument is not as the call needs it or
-// the call is refused; nothing has been enqueued then, and the caller repeats
+// Every function returns None where an argument is not as the call needs it, memory
+// is short or the call is refused; nothing has been enqueued then, and the caller repeats
 // the steps one by one in Python, where the error is raised.  Work goes to
 // torch's current stream of x's device; memory comes from torch's allocator on
 // that stream.
@@ -156,12 +156,24 @@ py::object ffn_backward(const Tensor& dy, const Tensor& x, const Tensor& gate, c
   return py::make_tuple(out[0], out[1], out[2], out[3]);
 }
 
+// An allocation that fails is the Python steps' to report, with torch's own error.
+template <typename... A>
+auto guarded(py::object (*f)(A...)) {
+  return [f](A... a) -> py::object {
+    try {
+      return f(a...);
+    } catch (const c10::Error&) {
+      return py::none();
+    }
+  };
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
-  m.def("quantize", &quantize);
-  m.def("dequantize", &dequantize);
-  m.def("linear", &linear);
-  m.def("ffn_forward", &ffn_forward);
-  m.def("ffn_backward", &ffn_backward);
+  m.def("quantize", guarded(&quantize));
+  m.def("dequantize", guarded(&dequantize));
+  m.def("linear", guarded(&linear));
+  m.def("ffn_forward", guarded(&ffn_forward));
+  m.def("ffn_backward", guarded(&ffn_backward));
 }

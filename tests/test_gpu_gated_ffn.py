@@ -172,6 +172,9 @@ def test_refusals(dev):
                                                down[:60].contiguous())):
         with pytest.raises(lib.NVFP4Error):
             call()
+    with pytest.raises(torch.OutOfMemoryError):
+        wide = torch.zeros((1 << 18, 8), dtype=BF, device=dev)          # 2 TB to keep
+        lib.gated_ffn_forward(torch.zeros((1 << 20, 8), dtype=BF, device=dev), wide, wide, wide.view(8, -1), save=True)
     # nothing was enqueued, and the library still answers
     assert lib.device_status() == 0
     assert torch.equal(lib.gated_ffn_forward(x, gate, up, down, save=True)[0], y)
@@ -223,3 +226,63 @@ def test_back_to_back_calls(dev, T):
     torch.cuda.synchronize()
     for i, g in enumerate(got):
         assert torch.equal(g, ref[i % 4]), i
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_fork_and_join(dev, T, captured):
+    """Calls that follow copies, memsets, other streams' work and several
+    predecessors at once, eager and in a graph."""
+    x, gate, up, down, dy = _make(30, T, 256, 192, BF, dev)
+    gu = lib.Mxfp4Weight.quantize(torch.cat((gate, up)))
+    xin, buf = torch.zeros_like(x), torch.empty_like(x)
+    side = torch.cuda.Stream()
+
+    def work():
+        main = torch.cuda.current_stream()
+        buf.copy_(xin)                                     # a copy as predecessor
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            a = lib.gated_ffn_forward(buf, gate, up, down)
+        b = lib.mxfp4_linear_a4(buf, gu, "silu")
+        main.wait_stream(side)
+        c, saved = lib.gated_ffn_forward(a, gate, up, down, save=True)   # two predecessors
+        z = torch.zeros_like(c)
+        grads = lib.gated_ffn_backward(z.add_(1), a, gate, up, down, saved)
+        q = lib.mxfp4_quantize(b)
+        return (a, b, c, *grads, *q, lib.mxfp4_dequantize(*q), lib.mxfp4_linear(a, gu, stream=None))
+    xin.copy_(x)
+    ref = work()
+    torch.cuda.synchronize()
+    ref = [t.clone() for t in ref]
+    xin.zero_()
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = work()
+        xin.copy_(x)
+        for _ in range(3):
+            g.replay()
+    else:
+        xin.copy_(x)
+        for _ in range(3):
+            out = work()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, r) for o, r in zip(out, ref))
+
+
+def test_past_32_bit_offsets(dev):
+    """Intermediates of more than 2^31 elements: tokens that are zero but for the
+    last, whose outputs and gradients are those of a batch of their own."""
+    T, H, I, n = (1 << 20) - 3, 8, 2112, 61
+    x, gate, up, down, dy = _make(12, n, H, I, BF, dev)
+    xl, dyl = (torch.zeros((T, H), dtype=BF, device=dev) for _ in range(2))
+    xl[-n:], dyl[-n:] = x, dy
+    y, saved = lib.gated_ffn_forward(xl, gate, up, down, save=True)
+    grads = lib.gated_ffn_backward(dyl, xl, gate, up, down, saved)
+    ref = _reference(x, gate, up, down, dy, "gelu_tanh")
+    assert lib.device_status() == 0
+    assert (y[:-n] == 0).all() and (grads[0][:-n] == 0).all()
+    for name, got in zip(("y", "dx", "dgate", "dup", "ddown"), (y[-n:], grads[0][-n:], *grads[1:])):
+        R.assert_within(got, *ref[name], name)
+    R.assert_within(lib.gated_ffn_forward(xl, gate, up, down)[-n:], *ref["y"], "y, not kept")

@@ -259,6 +259,19 @@ def test_linear_strides_streams_and_repeats(dev, T):
         lib.mxfp4_linear(x[:, :96], weight)
 
 
+def test_linear_past_32_bit_offsets(dev):
+    """Outputs of more than 2^31 elements: the last rows of many."""
+    T, N, K, n = (1 << 20) - 3, 4096, 32, 61
+    weight, w64 = _weight(14, N, K, dev)
+    x = torch.zeros((T, K), dtype=BF, device=dev)
+    x[-n:] = _randn(15, (n, K), BF, dev)
+    for a4, f in ((False, lib.mxfp4_linear), (True, lib.mxfp4_linear_a4)):
+        y = f(x, weight)
+        ref, bound = R.linear64(R.mx_round(x[-n:]) if a4 else x[-n:].double(), w64, None, BF)
+        assert lib.device_status() == 0 and (y[:n] == 0).all() and (y[-2 * n:-n] == 0).all()
+        R.assert_within(y[-n:], ref, bound, f"a4 {a4}")
+
+
 def test_weight_copies(dev):
     """Copies of a weight hold their own arrays."""
     import copy
