@@ -9,8 +9,10 @@
 // 2816 in 58.7 us, 1.66 PFLOP/s), at fewer by what issues a stage and by the
 // copies: a pair of SMs shares one B tile (each loads half of it), so that every
 // byte of A and B feeds 256 rows or BN columns, and a copy takes about 1.3
-// cycles per line and SM.  MXFP4 at 192 columns takes about 450 cycles per 256
-// of K where the tensor pipe needs 384.
+// cycles per line and SM.  MXFP4 at 192 columns takes 480 to 530 cycles per 256
+// of K: 384 for the products and about 24 for each of the six copies of scales,
+// which share the tensor pipe (a warp of their own for the scales' loads, or one
+// for each side's copies, changed nothing).
 //
 // Forms:
 //   plain   out = sum over K segments A B^T, 16-bit; several products in one
