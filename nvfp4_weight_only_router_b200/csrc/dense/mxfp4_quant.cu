@@ -59,7 +59,7 @@ __device__ __forceinline__ Bits<T, N> load_any(const void* x, int64_t row0, int6
   uint32_t v[W + 4];
 #pragma unroll
   for (int i = 0; i < W / 4 + 1; ++i) {
-    const uint4 q = 16 * i < o + bytes && valid > 0 ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 q = 16 * i < o + bytes && valid > 0 ? ld_v4(src + i) : make_uint4(0u, 0u, 0u, 0u);
     v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
   }
   if (o & 8) {
@@ -92,14 +92,14 @@ __device__ __forceinline__ Bits<T, N> load_bits(const void* x, int64_t row0, int
 #pragma unroll
     for (int i = 0; i < W / 8; ++i) {
       uint32_t q[8];
-      ld_nc_v8(p + 32 * i, q);
+      ld_v8_stream(p + 32 * i, q);
 #pragma unroll
       for (int k = 0; k < 8; ++k) r.w[8 * i + k] = q[k];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < W / 4; ++i) {
-      const uint4 q = ldg_nc_v4(p + 16 * i);
+      const uint4 q = ld_v4_stream(p + 16 * i);
       r.w[4 * i] = q.x; r.w[4 * i + 1] = q.y; r.w[4 * i + 2] = q.z; r.w[4 * i + 3] = q.w;
     }
   }
@@ -256,12 +256,12 @@ __global__ void __launch_bounds__(kQT) mxfp4_prep_kernel(QuantArgs p, int64_t qb
 
 // The value of element c of a row.
 __device__ __forceinline__ float mx_value(const uint8_t* codes, const uint8_t* scales, int64_t row, uint32_t c, int64_t nb) {
-  const uint32_t code = ((uint32_t)__ldg(codes + row * (16 * nb) + (c >> 1)) >> (4 * (c & 1))) & 15u;
+  const uint32_t code = (ld_u8(codes + row * (16 * nb) + (c >> 1)) >> (4 * (c & 1))) & 15u;
   uint32_t h[4];
   e2m1x8_to_f16x2(code, h);
   float lo, hi;
   unpack16x2(h[0], true, lo, hi);
-  return lo * mx_scale(__ldg(scales + row * nb + (c >> 5)));
+  return lo * mx_scale(ld_u8(scales + row * nb + (c >> 5)));
 }
 
 // 32 bytes of output per thread (G = 8 values of f32, 16 of bf16), contiguous
@@ -271,9 +271,8 @@ constexpr int kDU = 4, kDGroups = kQT * kDU;
 constexpr int kAU = 2, kAGroups = kQT * kAU;  // any length
 
 template <typename T>
-__global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes,
-                                                               const uint8_t* __restrict__ scales, int64_t rows,
-                                                               int64_t K, T* __restrict__ out) {
+__global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                               int64_t rows, int64_t K, T* out) {
   after_previous();
   let_next();
   constexpr int G = 32 / sizeof(T);
@@ -292,13 +291,13 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __
     if (row < rows) {
       const uint32_t* src = reinterpret_cast<const uint32_t*>(codes) + row * (4 * nb) + g * (G / 8);
       if constexpr (G == 16) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 q = ld_v2(src);
         w[u][0] = q.x;
         w[u][1] = q.y;
       } else {
-        w[u][0] = __ldg(src);
+        w[u][0] = ld_u32(src);
       }
-      sc[u] = __ldg(scales + row * nb + g / (32 / G));
+      sc[u] = ld_u8(scales + row * nb + g / (32 / G));
     }
   }
 #pragma unroll
@@ -336,9 +335,8 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_kernel(const uint8_t* __
 // x 2817 f32 (75 us); a value per thread and store took 8.0 us at 1000 x 2100
 // f32 (5.1), this form for whole groups 83 us at 32768 x 2816 (63.5 above).
 template <typename T>
-__global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t* __restrict__ codes,
-                                                                   const uint8_t* __restrict__ scales, int64_t rows,
-                                                                   int64_t K, T* __restrict__ out) {
+__global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                   int64_t rows, int64_t K, T* out) {
   after_previous();
   let_next();
   const int64_t nb = (K + 31) / 32, first = (int64_t)blockIdx.x * (kAGroups * 8), n = rows * K;
@@ -357,15 +355,15 @@ __global__ void __launch_bounds__(kQT) mxfp4_dequantize_any_kernel(const uint8_t
       const uint32_t* src = reinterpret_cast<const uint32_t*>(codes) + row[u] * words;
       const uint8_t* sc = scales + row[u] * nb;
       const uint32_t at = c[u] >> 3, sh = (c[u] & 7) * 4, valid = min(8u, k - c[u]);
-      const uint32_t lo = __ldg(src + at);
-      w[u] = sh ? __funnelshift_r(lo, at + 1 < words ? __ldg(src + at + 1) : 0u, sh) : lo;
-      s0[u] = __ldg(sc + (c[u] >> 5));
-      s1[u] = __ldg(sc + ((c[u] + valid - 1) >> 5));
+      const uint32_t lo = ld_u32(src + at);
+      w[u] = sh ? __funnelshift_r(lo, at + 1 < words ? ld_u32(src + at + 1) : 0u, sh) : lo;
+      s0[u] = ld_u8(sc + (c[u] >> 5));
+      s1[u] = ld_u8(sc + ((c[u] + valid - 1) >> 5));
       if (valid < 8) {
         w[u] &= (1u << (4 * valid)) - 1u;
         if (row[u] + 1 < rows) {
-          w[u] |= __ldg(src + words) << (4 * valid);
-          s2[u] = __ldg(sc + nb);
+          w[u] |= ld_u32(src + words) << (4 * valid);
+          s2[u] = ld_u8(sc + nb);
         }
       }
     }

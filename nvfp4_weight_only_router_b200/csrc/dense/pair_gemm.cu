@@ -296,9 +296,9 @@ struct Kept16 {
 };
 // the lane's part of a kept block
 __device__ __forceinline__ void kept_load(const uint8_t* blk, int lane, Kept16& k) {
-  ld_nc_v8(blk + lane * 32, k.ph);
-  ld_nc_v8(blk + 1024 + lane * 32, k.ah);
-  const uint4 a = ldg_nc_v4(blk + 2048 + lane * 16), b = ldg_nc_v4(blk + 2560 + lane * 16);
+  ld_v8_stream(blk + lane * 32, k.ph);
+  ld_v8_stream(blk + 1024 + lane * 32, k.ah);
+  const uint4 a = ld_v4_stream(blk + 2048 + lane * 16), b = ld_v4_stream(blk + 2560 + lane * 16);
   k.pl[0] = a.x; k.pl[1] = a.y; k.pl[2] = a.z; k.pl[3] = a.w;
   k.al[0] = b.x; k.al[1] = b.y; k.al[2] = b.z; k.al[3] = b.w;
 }
@@ -616,8 +616,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
         b.code[i] = make_uint4(0u, 0u, 0u, 0u);
         b.scale[i] = 0u;
         if (lt < p.n_tiles && row < N && unit < units) {
-          b.code[i] = ldg_nc_v4(wq + ((size_t)row * units + unit) * 16);
-          b.scale[i] = __ldg(ws + (size_t)row * units + unit);
+          b.code[i] = ld_v4_stream(wq + ((size_t)row * units + unit) * 16);
+          b.scale[i] = ld_u8(ws + (size_t)row * units + unit);
         }
       }
       lk += kPConvWarps;

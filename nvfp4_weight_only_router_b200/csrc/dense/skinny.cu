@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
       va[u] = vb[u] = make_uint4(0u, 0u, 0u, 0u);
       ca[u] = cb[u] = 0u;
       if (unit < p.units) {
-        va[u] = ldg_nc_v4(wa + (size_t)unit * 16);
-        vb[u] = ldg_nc_v4(wb + (size_t)unit * 16);
+        va[u] = ld_v4_stream(wa + (size_t)unit * 16);
+        vb[u] = ld_v4_stream(wb + (size_t)unit * 16);
         if (CODEC == 1) {
-          ca[u] = __ldg(sa + unit);
-          cb[u] = __ldg(sb + unit);
+          ca[u] = ld_u8(sa + unit);
+          cb[u] = ld_u8(sb + unit);
         }
       }
     }
