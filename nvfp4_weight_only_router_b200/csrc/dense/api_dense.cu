@@ -86,7 +86,7 @@ nvfp4_status check_linear(int32_t T, const mxfp4_weight* w, int32_t act) {
 }
 
 bool few_tokens(int32_t T, const mxfp4_weight* w, int32_t act, bool a4) {
-  return skinny_fits(T, act ? w->N / 2 : w->N, act != kActNone, true, a4);
+  return skinny_fits_mx(T, act ? w->N / 2 : w->N, w->K, act != kActNone, a4);
 }
 
 // W4A16 of many tokens: the weight as bf16
@@ -322,7 +322,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   cudaStream_t s = as_stream(stream);
   int* status = device_status_ptr();
   void* const h = saved ? saved : ws;
-  const bool few = !saved && skinny_fits(T, f->I, true, false, false);
+  const bool fits = skinny_fits_ffn(T, f->H, f->I), few = fits && !saved;  // what is kept: only by the other kernel
   const int64_t ldh = few ? f->I : pair_pitch(f->I);
   cudaError_t e;
   if (few) {
@@ -357,7 +357,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
     e = launch_pair_gated(a, status, s);
   }
   if (e != cudaSuccess) return cuda_fail(e);
-  if (skinny_fits(T, f->H, false, false, false)) {
+  if (fits) {
     SkinnyArgs a{};
     a.x = h;
     a.ldx = ldh;

@@ -53,8 +53,10 @@ cudaError_t launch_mxfp4_prep_a4(const MxPrepArgs& a, cudaStream_t st);
 int sms();
 
 // ---------------------------------------------------------------- skinny.cu
-// whether launch_skinny is the faster kernel for a product (N: output columns)
-bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x);
+// whether launch_skinny is the faster kernel for an MXFP4 product (N: output
+// columns), or for both products of a gated block
+bool skinny_fits_mx(int T, int N, int K, bool gated, bool quant_x);
+bool skinny_fits_ffn(int T, int H, int I);
 struct SkinnyArgs {
   const void* x;      // [T, K]
   int64_t ldx;        // elements

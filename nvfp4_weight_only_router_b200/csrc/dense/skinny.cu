@@ -295,28 +295,40 @@ cudaError_t launch_nt(const SkinnyParams& p, cudaStream_t st) {
   }
   if (p.T <= 8) return launch_one<CODEC, 1, GATED, OPT, CODEC == 0>(p, st);
   if (p.T <= 16) return launch_one<CODEC, 2, GATED, OPT, false>(p, st);
-  if constexpr (QX) return cudaErrorInvalidValue;  // skinny_fits: at most 16 tokens
+  if constexpr (QX) return cudaErrorInvalidValue;  // skinny_fits_mx: at most 16 tokens
   else return launch_one<CODEC, 4, GATED, OPT, false>(p, st);
 }
 
 }  // namespace
 
-// Measured against the tensor-core kernels (whole calls, us, N x K, `silu`
-// gated): the crossing lies where a group's CTAs no longer fit the SMs at once
-// (2 on each), or, with x quantised in every CTA, where there is more than one.
-//   W4A16  T = 32:  8192 x 2816 17.6 / 18, 2816 x 2112 8.4 / 9.7
-//          T = 64:  2816 x 2112 13.6 / 9.7 (two waves), 1024 x 1024 3.8 / 7.3
-//          T = 128: 512 x 2816 silu 6.4 / 11.0 (one wave)
-//   W4A4   T = 8:   4224 x 2816 silu 7.3 / 8.6, 8192 x 2816 11.7 / 9.2 (two waves)
-//          T = 16:  1024 x 1024 3.7 / 5.8 (a CTA an SM), 2816 x 2112 8.6 / 7.2 (two)
-//   16-bit gated block, H = 2816: T = 16, I = 2112 12.8 / 18.6; T = 64, I = 256
-//          11.8 / 14.1 (one wave); T = 32, I = 8192 / H = 2816 55.1 / 47.1 (two waves)
-bool skinny_fits(int T, int N, bool gated, bool mx, bool quant_x) {
+// Measured against the tensor-core kernels (whole calls in a graph, us, few-token
+// kernel / the other, N x K, `silu` gated).  With MXFP4 weights the crossing lies
+// where the CTAs no longer fit the SMs at once (2 on each), or, with x quantised in
+// every CTA, where there is more than one on an SM or K is long.
+//   W4A16  T = 32:  8192 x 2816 17.5 / 18.4, 2816 x 2112 8.2 / 8.5, 2816 x 8192 22.8 / 21.1
+//          T = 64:  2816 x 2112 14.3 / 8.8 (two waves), 1024 x 1024 3.5 / 6.1
+//          T = 128: 512 x 2816 silu 6.2 / 10.1 (one wave)
+//   W4A4   T = 1:   2816 x 8192 12.0 / 12.2
+//          T = 8:   4224 x 2816 silu 7.1 / 8.1, 8192 x 2816 11.9 / 8.8 (two waves),
+//                   2816 x 8192 15.1 / 12.2 (long)
+//          T = 16:  1024 x 1024 3.5 / 5.7 (a CTA an SM), 2816 x 2112 8.3 / 6.9 (two)
+bool skinny_fits_mx(int T, int N, int K, bool gated, bool quant_x) {
   if (T > 128) return false;
   const int n = sms(), rows = gated ? 8 : 16;
   const int64_t ctas = (int64_t)((N + rows - 1) / rows) * ((T + 31) / 32);
-  if (quant_x) return T <= 16 && ctas <= (T <= 8 ? 2 * n : n);
-  return T <= (mx ? 32 : 16) || (ctas <= 2 * n && T <= (mx ? 128 : 64));
+  if (quant_x) return T <= 16 && ctas <= (T <= 8 ? 2 * n : n) && (T == 1 || K <= 4096);
+  return T <= 32 || ctas <= 2 * n;
+}
+
+// The gated block, both products by one kernel or both by the other (a mixture
+// is slower than either: the second then waits for the first).  T H I at the
+// crossing, in millions, for I x H: 1024 x 8192 180, 2112 x 2816 190, 2816 x 2112
+// 110, 4096 x 1024 125, 4096 x 2816 138, 5632 x 2816 150.  At T = 16: 2112 x 2816
+// 12.7 / 16.1, 1024 x 8192 21.4 / 24.0, 5632 x 2816 35.4 / 34.1.  At T = 8 the
+// few-token kernel always (8192 x 2816 40.0 / 42.4), above 64 never (1024 x 1024
+// at 96: 10.8 / 10.1).
+bool skinny_fits_ffn(int T, int H, int I) {
+  return T <= 8 || (T <= 64 && (int64_t)T * H * I <= 140000000);
 }
 
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
