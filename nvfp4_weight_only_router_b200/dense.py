@@ -5,7 +5,8 @@ block with its backward pass.
 Every function runs on torch's current stream of the tensors' device, or on
 `stream`; outputs and workspaces are allocated on that stream, per call, so
 that calls may overlap and be captured freely.  Tensors are [rows, features]
-with contiguous features; x (and dy) may be row-strided views.
+with contiguous features, on 16-byte boundaries (what is quantised: of its
+elements); x (and dy) may be row-strided views.
 
 A call on the current stream is made whole by `_dense_calls` (the same C calls,
 with checks and allocations in C++: 5 us of host time instead of 9 to 18).  It
@@ -287,6 +288,12 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up
     return tuple(outs)
 
 
+def _own_rows(t: torch.Tensor) -> torch.Tensor:
+    """t, or a copy of it, with contiguous rows from a 16-byte boundary."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, up, down, activation):
@@ -302,7 +309,7 @@ class _GatedFfn(torch.autograd.Function):
     def backward(ctx, dy):
         x, gate, up, down, saved = ctx.saved_tensors
         # an expanded gradient (of a sum) has no rows of its own
-        grads = gated_ffn_backward(dy.contiguous(), x, gate, up, down, saved, ctx.activation,
+        grads = gated_ffn_backward(_own_rows(dy), x, gate, up, down, saved, ctx.activation,
                                    ctx.needs_input_grad[:4])
         return (*grads, None)
 
@@ -313,5 +320,5 @@ def gated_ffn(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch
     First derivatives only.  As with every torch operation, a backward pass can
     be captured into a graph only where no earlier autograd graph of the same
     leaves is alive; gated_ffn_forward and gated_ffn_backward have no such limit."""
-    y = _GatedFfn.apply(x.reshape(-1, x.shape[-1]).contiguous(), gate, up, down, activation)
+    y = _GatedFfn.apply(_own_rows(x.reshape(-1, x.shape[-1])), gate, up, down, activation)
     return y.view(x.shape)

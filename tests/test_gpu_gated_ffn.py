@@ -134,6 +134,15 @@ def test_autograd(dev):
     assert torch.equal(y.view(60, 136), yf)
     for leaf, g in zip(leaves, ref):
         assert torch.equal(leaf.grad.view(g.shape), g)
+    # tokens and an incoming gradient off the 16-byte grid
+    flat = torch.empty(1 + x.numel(), dtype=BF, device=dev)
+    off = flat[1:].view(60, 136)
+    off.copy_(x)
+    xo = off.detach().requires_grad_()
+    yo = lib.gated_ffn(xo, gate, up, down, "silu")
+    go = torch.ones_like(flat)[1:].view(60, 136)
+    yo.backward(go)
+    assert torch.equal(yo, yf) and torch.equal(xo.grad, ref[0])
     # frozen weights: the input's gradient alone
     xi = x.clone().requires_grad_()
     lib.gated_ffn(xi, gate, up, down, "silu").sum().backward()
