@@ -47,7 +47,7 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kPProdA = 0, kPMma = 1, kPProdB = 2, kPScale = 3, kPEpi0 = 4, kPEpiWarps = 8;
-constexpr int kPConv0 = 12, kPConvWarps = 4;
+constexpr int kPConv0 = 12, kPConvWarps = 8, kPConvPer = 2;  // W4: warps, and warps of a stage
 constexpr int kPTmem = 512;
 constexpr int kPOutB = 4096;  // output buffer of an epilogue warp: 32 rows x 64 columns
 constexpr int kKind16 = 0, kKindMx = 1, kKindW4 = 2;
@@ -374,8 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      // W4: SM 0's producer and a converter of each SM
-      mbar_init(&sm.full[s], KIND == kKindW4 ? 3 : 1);
+      // W4: SM 0's producer and the converters of each SM
+      mbar_init(&sm.full[s], KIND == kKindW4 ? 1 + 2 * kPConvPer : 1);
       mbar_init(&sm.empty[s], 1);
       mbar_init(&sm.scaled[s], 1);
     }
@@ -583,8 +583,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
     // arithmetic (the wait, the fence, the arrival) then overlaps among the
     // warps.  It reads its next stage while it converts one.
     constexpr int ROWS = BN / 2, BPR = 2 * C::KS;        // rows of this SM, blocks of 32 per row and stage
-    constexpr int NB = ROWS * BPR / 32, DR = 32 / BPR;   // blocks per lane, rows between them
-    const int r0 = lane / BPR, kb = lane % BPR;
+    constexpr int NB = ROWS * BPR / (32 * kPConvPer), DR = 32 / BPR;  // blocks per lane, rows between them
+    constexpr int GROUPS = kPConvWarps / kPConvPer;
+    const int cw = warp - kPConv0, group = cw / kPConvPer;
+    const int r0 = (cw % kPConvPer) * (NB * DR) + lane / BPR, kb = lane % BPR;
     const uint32_t full0 = leader_addr(&sm.full[0]);
     const PProb& q = p.p[0];
     const int K = q.K, kc_all = q.kc, N = q.N, units = K / 32;
@@ -596,7 +598,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
       uint32_t scale[NB];
     };
     // the next stage to read
-    int lt = cluster, lk = warp - kPConv0, lrow = 0;
+    int lt = cluster, lk = group, lrow = 0;
     auto settle = [&]() {  // into the tile that holds it
       while (lk >= kc_all) {
         lk -= kc_all;
@@ -620,7 +622,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
           b.scale[i] = ld_u8(ws + (size_t)row * units + unit);
         }
       }
-      lk += kPConvWarps;
+      lk += GROUPS;
       if (lk >= kc_all) settle();
     };
     auto convert = [&](const Stage& b, int it) {
@@ -662,11 +664,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
     };
     Stage even, odd;
     read(even);
-    for (int it = warp - kPConv0; it < total; it += 2 * kPConvWarps) {
+    for (int it = group; it < total; it += 2 * GROUPS) {
       read(odd);
-      if (!convert(even, it) || it + kPConvWarps >= total) break;
+      if (!convert(even, it) || it + GROUPS >= total) break;
       read(even);
-      if (!convert(odd, it + kPConvWarps)) break;
+      if (!convert(odd, it + GROUPS)) break;
     }
   } else if (warp >= kPEpi0) {
     // ------------------------------------------------------------ epilogue
