@@ -137,11 +137,13 @@ struct PairGatedBwd {
   void *dg, *du;          // [T, pair_pitch(I)]
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
-// bf16 x MXFP4 weights, decoded on the way into the products: for one tile of
-// rows, since every further one decodes the weights again (us, decoded once into
-// bf16 / here: 2816 x 2112 T = 64 10.8 / 9.9, 4224 x 2816 gated T = 256 14.5 /
-// 12.5, 2816 x 8192 T = 64 26.2 / 23.1; 2816 x 2112 T = 512 12.7 / 15.5)
-constexpr int kPairW4MaxTokens = 256;
+// bf16 x MXFP4 weights, decoded on the way into the products.  Every tile of rows
+// decodes them again, in tiles of at most 128 columns; above some tokens decoding
+// once into bf16 for 256-column tiles is faster (us, that / here: 2816 x 2112 T =
+// 512 14.6 / 11.2, T = 2048 27.2 / 25.1, T = 4096 40.8 / 38.6; 4224
+// x 2816 gated T = 512 18.4 / 13.8, T = 2048 39.7 / 38.6, T = 4096 66.7 / 72.1; 8192 x
+// 2816 T = 2048 72.4 / 67.4, T = 4096 118.8 / 132.8)
+constexpr int kPairW4MaxTokens = 2048;
 struct PairW4 {
   const void* x;
   int64_t ldx;

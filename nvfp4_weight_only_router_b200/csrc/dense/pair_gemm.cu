@@ -579,9 +579,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
     }
   } else if (KIND == kKindW4 && warp >= kPConv0) {
     // ------------------------- MXFP4 weights into the stages' B tiles as bf16
-    // A warp converts every fourth stage: what a stage costs besides its
+    // Two warps convert every fourth stage: what a stage costs besides its
     // arithmetic (the wait, the fence, the arrival) then overlaps among the
-    // warps.  It reads its next stage while it converts one.
+    // pairs.  A warp reads its next stage while it converts one.
     constexpr int ROWS = BN / 2, BPR = 2 * C::KS;        // rows of this SM, blocks of 32 per row and stage
     constexpr int NB = ROWS * BPR / (32 * kPConvPer), DR = 32 / BPR;  // blocks per lane, rows between them
     constexpr int GROUPS = kPConvWarps / kPConvPer;
@@ -830,7 +830,7 @@ struct Width {
 };
 constexpr Width kWidths16[] = {{256, 512, 3000}, {128, 290, 2000}, {64, 200, 1500}};
 constexpr Width kWidths16Mn[] = {{256, 540, 3000}, {128, 430, 2000}};  // an MN-major box is 64 columns of each SM's half
-constexpr Width kWidthsW4[] = {{128, 400, 2000}, {64, 310, 1500}};
+constexpr Width kWidthsW4[] = {{128, 400, 2000}, {64, 310, 1500}};  // 256 was measured at T = 512 to 4096: never faster
 constexpr Width kWidthsMx[] = {{192, 560, 3000}, {128, 480, 2000}, {64, 400, 1500}};
 struct Tiles {
   int64_t m, cols, subs;  // tiles along M, columns, sub-stages along K

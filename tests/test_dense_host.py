@@ -88,9 +88,9 @@ def test_linear_refusals(dc, codes, a4):
     assert run(x=P + 2) == run(y=P + 8) == run(ldx=68) == run(w=_w(dc, s=P + 4)) == c.NVFP4_ERR_ALIGNMENT
     assert run(ws=P + 16) == c.NVFP4_ERR_ALIGNMENT
     assert size(4, ctypes.byref(w), 0) == 256                           # few tokens: none is used
-    n = size(500, ctypes.byref(w), 0)
+    n = size(5000, ctypes.byref(w), 0)
     assert n > 256
-    assert run(T=500, n=n - 1) == run(T=500, ws=None) == c.NVFP4_ERR_WORKSPACE
+    assert run(T=5000, n=n - 1) == run(T=5000, ws=None) == c.NVFP4_ERR_WORKSPACE
     assert run(T=0, x=None, y=None) == c.NVFP4_OK
 
 

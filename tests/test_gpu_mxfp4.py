@@ -135,7 +135,8 @@ def test_linear_gated(dev, T, N, K, act):
 
 
 @pytest.mark.parametrize("T,N,K,act", [(4096, 4224, 2816, "gelu_tanh"), (1111, 2816, 2112, None), (64, 4224, 2816, "silu"),
-                                       (2000, 1000, 544, None), (700, 8192, 512, None)])
+                                       (2000, 1000, 544, None), (700, 8192, 512, None), (2300, 2816, 704, None),
+                                       (2100, 528, 160, "silu")])
 def test_linear_large(dev, T, N, K, act):
     """The layer's sizes and others that take each tile width."""
     weight, w64 = _weight(1, N, K, dev, K ** -0.5)
