@@ -303,10 +303,14 @@ cudaError_t launch_nt(const SkinnyParams& p, cudaStream_t st) {
 
 // Measured against the tensor-core kernels (whole calls in a graph, us, few-token
 // kernel / the other, N x K, `silu` gated).  With MXFP4 weights the crossing lies
-// where the CTAs no longer fit the SMs at once (2 on each), or, with x quantised in
-// every CTA, where there is more than one on an SM or K is long.
-//   W4A16  T = 32:  8192 x 2816 17.5 / 18.4, 2816 x 2112 8.2 / 8.5, 2816 x 8192 22.8 / 21.1
-//          T = 64:  2816 x 2112 14.3 / 8.8 (two waves), 1024 x 1024 3.5 / 6.1
+// where the CTAs no longer fit the SMs at once (2 on each; up to 16 tokens not even
+// there, the weights then being most of the time), or, with x quantised in every
+// CTA, where there is more than one on an SM or K is long.
+//   W4A16  T = 16:  2816 x 8192 14.2 / 20.9, 16384 x 2816 19.6 / 21.0 (four waves),
+//                   8192 x 8192 26.8 / 26.4, 32768 x 1024 17.1 / 15.9
+//          T = 24:  8192 x 2816 14.9 / 12.0 (two waves), 2816 x 8192 19.0 / 20.9
+//          T = 32:  8192 x 2816 17.3 / 11.9, 2816 x 2112 8.2 / 8.2, 2816 x 8192 23.2 / 20.9
+//          T = 64:  2816 x 2112 14.0 / 8.2 (two waves), 1024 x 1024 3.5 / 6.1
 //          T = 128: 512 x 2816 silu 6.2 / 10.1 (one wave)
 //   W4A4   T = 1:   2816 x 8192 12.0 / 12.2
 //          T = 8:   4224 x 2816 silu 7.1 / 8.1, 8192 x 2816 11.9 / 8.8 (two waves),
@@ -317,7 +321,7 @@ bool skinny_fits_mx(int T, int N, int K, bool gated, bool quant_x) {
   const int n = sms(), rows = gated ? 8 : 16;
   const int64_t ctas = (int64_t)((N + rows - 1) / rows) * ((T + 31) / 32);
   if (quant_x) return T <= 16 && ctas <= (T <= 8 ? 2 * n : n) && (T == 1 || K <= 4096);
-  return T <= 32 || ctas <= 2 * n;
+  return T <= 16 || ctas <= 2 * n;
 }
 
 // The gated block, both products by one kernel or both by the other (a mixture
