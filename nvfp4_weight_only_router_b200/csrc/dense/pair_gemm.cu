@@ -30,8 +30,8 @@
 // Warps: 0 and 2 TMA producers of A and B (in both SMs), 1 MMA issuer (in SM 0
 // of the pair), 3 MXFP4 scales into tensor memory (likewise, ahead of the
 // products, whose issue they would delay), 4-11 epilogue: a warp per
-// tensor-memory lane quarter and column half, 12-15 (MXFP4 weights by 16-bit
-// rows) converters in place of B's producer.  Two accumulators, so that a
+// tensor-memory lane quarter and column half, 12-19 (MXFP4 weights by 16-bit
+// rows) converters of B, whose producer then shares A's work.  Two accumulators, so that a
 // tile's epilogue overlaps the next tile's products (MXFP4 tiles have at most
 // 192 columns: scales need tensor memory too).  Every wait is bounded in wall
 // time; one that gives up records a timeout and the pair tears down.
@@ -86,7 +86,7 @@ struct alignas(1024) PSmem {
   uint64_t fin, fin_sf;
   uint32_t taddr;
   int abort_flag;
-  int issued[2];                       // stages of A and of B copied
+  int issued[2];                       // stages behind the producers
 };
 
 struct alignas(64) PProb {
@@ -363,10 +363,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
   // The first tile's description and descriptors are fetched while the pair
   // sets up: cold, they took 3300 cycles behind it.
   PTile tile = ptile<NP>(p, cluster);
-  if (warp == kPProdA || (KIND != kKindW4 && warp == kPProdB)) {
+  if (warp == kPProdA || warp == kPProdB) {
     const PProb& q = p.p[tile.prob];
     if (elect_one()) {
-      prefetch_map(warp == kPProdA ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0]);
+      prefetch_map(warp == kPProdA || KIND == kKindW4 ? &q.a[0] : &q.b[EPI == kEpiGated ? rank : 0]);
       if (KIND == kKindMx) prefetch_map(warp == kPProdA ? &p.sfa : &p.sfb);
     }
     __syncwarp();
@@ -401,9 +401,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
   after_previous();
   let_next();
 
-  if (warp == kPProdA || (KIND != kKindW4 && warp == kPProdB)) {
+  if (warp == kPProdA || warp == kPProdB) {
     // ------------------------------------------- TMA producers of A and of B
-    const bool is_a = warp == kPProdA;
+    // W4: both of A, a stage each in turn.  A warp takes 550 cycles for a stage's
+    // wait, arrival and two copies, whatever their size; the rest of a stage of 64
+    // columns takes less (2816 x 8192, T = 64: 21.5 -> 19.7 us).
+    const bool is_a = warp == kPProdA || KIND == kKindW4;
+    const int turn = warp == kPProdB;
     const uint32_t full0 = leader_addr(&sm.full[0]), op0 = smem_u32(is_a ? sm.a[0][0] : sm.b[0][0]);
     const uint32_t sf0 = smem_u32(is_a ? sm.sfa[0] : sm.sfb[0]);
     uint32_t s = 0, parity = 1;  // the first pass finds every stage free
@@ -429,10 +433,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
           map = is_a ? &q.a[1] : &q.b[1];
           kk = 0;
         }
-        ok = swait(sm, &sm.empty[s], parity, p.status);
+        const bool mine = KIND != kKindW4 || (issued & 1) == turn;
+        if (mine) ok = swait(sm, &sm.empty[s], parity, p.status);
         if (!ok) break;
         const uint32_t bar = full0 + 8 * s;
-        if (elect_one()) {
+        if (mine && elect_one()) {
           if (is_a && rank == 0) mbar_arrive_expect_tx(&sm.full[s], tx);
 #pragma unroll
           for (int u = 0; u < C::KS; ++u) {
@@ -460,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
         }
       }
     }
-    if (lane == 0) sm.issued[is_a ? 0 : 1] = issued;
+    if (lane == 0) sm.issued[turn] = issued;
   } else if (warp == kPMma) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
