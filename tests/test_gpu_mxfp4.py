@@ -169,7 +169,7 @@ def test_linear_long_rows(dev, T, N, K, act):
     _check(x.to(F16), weight, w64, act, True)
 
 
-@pytest.mark.parametrize("T", [1, 7, 20, 100, 300])
+@pytest.mark.parametrize("T", [1, 7, 20, 100, 300, 2200])
 def test_linear_every_scale(dev, T):
     """Every scale byte that the quantiser writes (0 to 252), the smallest with
     large activations, the largest with small ones."""
@@ -188,7 +188,26 @@ def test_linear_every_scale(dev, T):
             R.assert_within(y, ref, bound, f"a4 {a4} {s}")
 
 
-@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("T,N,act", [(40, 9472, None), (40, 9472, "silu"), (600, 4736, None)])
+def test_linear_scales_wide(dev, T, N, act):
+    """Scales on both sides of the second factor next to one another, in the
+    tiles that wide weights take; NaN scales reach their columns alone."""
+    K = 160
+    gen = torch.Generator(dev).manual_seed(T + N)
+    codes = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=dev, generator=gen)
+    scales = torch.randint(120, 136, (N, K // 32), dtype=torch.uint8, device=dev, generator=gen)
+    w64 = torch.from_numpy(R.mx_decode(codes.cpu().numpy(), scales.cpu().numpy(), K)).to(dev)
+    x = _randn(T, (T, K), BF, dev, 2.0 ** -8)
+    for a4 in (False, True):
+        _check(x, lib.Mxfp4Weight(codes, scales, K), w64, act, a4)
+    rows = [0, 77, N // 2 - 1]   # with an activation: of the gate
+    scales[rows, 3] = 255
+    for f in (lib.mxfp4_linear, lib.mxfp4_linear_a4):
+        y = f(x, lib.Mxfp4Weight(codes, scales, K), act)
+        assert torch.isnan(y[:, rows]).all() and torch.isnan(y).sum() == T * len(rows)
+
+
+@pytest.mark.parametrize("T", [3, 70, 2050])
 def test_linear_scale_range(dev, T):
     """Block scales over most of the byte's range, above and below the point
     where the bf16 decoding takes its second factor; NaN scales reach exactly
@@ -209,7 +228,7 @@ def test_linear_scale_range(dev, T):
         assert torch.isnan(y[:, 5]).all() and torch.isnan(y).sum() == T
 
 
-@pytest.mark.parametrize("T", [6, 140])
+@pytest.mark.parametrize("T", [6, 100, 140, 2200])
 def test_linear_non_finite_rows(dev, T):
     """A NaN or infinity in one token reaches that token's outputs alone."""
     weight, _ = _weight(8, 64, 96, dev)
@@ -224,7 +243,7 @@ def test_linear_non_finite_rows(dev, T):
         assert torch.isnan(y[1]).all() and not torch.isfinite(y[T - 1]).any()
 
 
-@pytest.mark.parametrize("T", [5, 150])
+@pytest.mark.parametrize("T", [5, 60, 150, 2100])
 def test_linear_strides_streams_and_repeats(dev, T):
     weight, w64 = _weight(10, 96, 128, dev)
     wide = _randn(11, (T + 2, 400), BF, dev)
