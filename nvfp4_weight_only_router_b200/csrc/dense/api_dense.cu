@@ -303,7 +303,9 @@ size_t gated_ffn_saved_bytes(int32_t T, const gated_ffn_weights* f) {
 }
 
 size_t gated_ffn_forward_workspace_bytes(int32_t T, const gated_ffn_weights* f) {
-  return check_ffn(T, f) == NVFP4_OK ? round_up((size_t)T * pair_pitch(f->I) * 2 + 1, 256) : 0;
+  // h, in two parts for few tokens
+  return check_ffn(T, f) == NVFP4_OK
+             ? round_up((size_t)T * pair_pitch(f->I) * (skinny_splits_hidden(T, f->I) ? 4 : 2) + 1, 256) : 0;
 }
 
 nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gated_ffn_weights* f, void* y, void* saved,
@@ -323,6 +325,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   int* status = device_status_ptr();
   void* const h = saved ? saved : ws;
   const bool fits = skinny_fits_ffn(T, f->H, f->I), few = fits && !saved;  // what is kept: only by the other kernel
+  const bool split = few && skinny_splits_hidden(T, f->I);
   const int64_t ldh = few ? f->I : pair_pitch(f->I);
   cudaError_t e;
   if (few) {
@@ -337,6 +340,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
     a.K = f->H;
     a.act = f->act;
     a.dtype = f->dtype;
+    a.split_y = split;
     e = launch_skinny(a, s);
   } else {
     PairGated a{};
@@ -369,6 +373,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
     a.act = kActNone;
     a.dtype = f->dtype;
     a.after_producer = true;
+    a.split_x = split;
     return cuda_status(launch_skinny(a, s));
   }
   PairGemm g{};

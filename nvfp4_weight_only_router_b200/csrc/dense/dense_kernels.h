@@ -57,6 +57,7 @@ int sms();
 // columns), or for both products of a gated block
 bool skinny_fits_mx(int T, int N, int K, bool gated, bool quant_x);
 bool skinny_fits_ffn(int T, int H, int I);
+bool skinny_splits_hidden(int T, int I);
 struct SkinnyArgs {
   const void* x;      // [T, K]
   int64_t ldx;        // elements
@@ -70,6 +71,9 @@ struct SkinnyArgs {
   bool mx;            // MXFP4 weights
   bool quant_x;       // x through MXFP4 first
   bool after_producer;  // x, and no weight, is written by the kernel launched just before on the stream
+  // 16-bit weights: values kept as two, each rounded to 16 bits, the second of what
+  // the first leaves.  T counts tokens; the second follows in a row of its own.
+  bool split_x, split_y;  // plain: of x; gated: of y
 };
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st);
 

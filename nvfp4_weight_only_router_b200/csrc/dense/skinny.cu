@@ -48,6 +48,7 @@ struct SkinnyParams {
   int act;
   bool f16;          // type of y (and of x)
   bool after;        // x is written by the kernel before
+  bool split;        // plain: rows 2t, 2t + 1 of x are a token; gated: of y
 };
 
 // Steps of K in flight per warp: for one group of tokens the whole K of the
@@ -86,6 +87,10 @@ __device__ __forceinline__ void quantize_in_place(uint8_t* at, bool valid, bool 
                     __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
 }
 
+// The product with a value's first part, with that of the rest (which is 0 where the
+// first is infinite: times an infinite weight it would make a NaN of an infinity).
+__device__ __forceinline__ float with_rest(float head, float rest) { return isfinite(head) ? head + rest : head; }
+
 // CODEC 0: 16-bit weights (bf16, or f16 with OPT); 1: MXFP4 (bf16 products; OPT
 // quantises x, of either 16-bit type).
 // XS: a pass's part of x is copied to shared memory at once, behind the loads of
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
 
   // this CTA's tokens
   const uint8_t* px = p.x + (size_t)blockIdx.y * (NT8 * 8) * p.ldx_bytes;
-  uint16_t* py = p.y + (size_t)blockIdx.y * (NT8 * 8) * p.N;
+  uint16_t* py = p.y + (size_t)blockIdx.y * (NT8 * 8) * p.N;  // split: only one block of tokens
   const int T = p.T - (int)blockIdx.y * (NT8 * 8);
 
   const int row_a = GATED ? blockIdx.x * 8 + r : blockIdx.x * 16 + r;
@@ -259,6 +264,15 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
       d.x += e.x; d.y += e.y; d.z += e.z; d.w += e.w;
     }
     const int t0 = j * 8 + 2 * c;
+    if (CODEC == 0 && !GATED && p.split) {  // one token's two parts
+      if (t0 < T) {
+        uint16_t* y = py + (size_t)(t0 >> 1) * p.N;
+        const uint32_t v = pack16x2(with_rest(d.x, d.y), with_rest(d.z, d.w), p.f16);
+        if (ok_a) y[row_a] = (uint16_t)v;
+        if (ok_b) y[row_b] = (uint16_t)(v >> 16);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = t0 + i;
@@ -266,7 +280,15 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
       const float v0 = i ? d.y : d.x, v1 = i ? d.w : d.z;
       uint16_t* y = py + (size_t)t * p.N;
       if (GATED) {
-        if (ok_a) y[row_a] = (uint16_t)pack16x2(act_fwd(v0, p.act) * v1, 0.f, p.f16);
+        const float h = act_fwd(v0, p.act) * v1;
+        const uint32_t v = pack16x2(h, 0.f, p.f16);
+        if (CODEC == 0 && p.split) {
+          float head, zero;
+          unpack16x2(v, p.f16, head, zero);
+          y += (size_t)t * p.N;
+          if (ok_a) y[p.N + row_a] = (uint16_t)pack16x2(isfinite(head) ? h - head : 0.f, 0.f, p.f16);
+        }
+        if (ok_a) y[row_a] = (uint16_t)v;
       } else {
         const uint32_t v = pack16x2(v0, v1, p.f16);
         if (ok_a) y[row_a] = (uint16_t)v;
@@ -335,7 +357,18 @@ bool skinny_fits_ffn(int T, int H, int I) {
   return T <= 8 || (T <= 64 && (int64_t)T * H * I <= 140000000);
 }
 
+// Whether the block keeps h in two 16-bit parts, so that y is off by its own
+// rounding alone.  Rounded once to 16 bits, h leaves y 1.4 times that far from the
+// exact one, and where few hidden units make up its sums up to 1.8 times.  Up to four
+// tokens the second parts are columns that the tensor instruction has anyway (us, one
+// part / two, weights not in L2: 2816 x 2112 T = 1 10.6 / 10.7, T = 4 11.0 / 11.5, 1024
+// x 4096 T = 4 12.5 / 13.7); for more the second product takes twice the tokens
+// (T = 8: 2816 x 512 8.4 / 7.4, 1024 x 512 4.7 / 4.9, 2816 x 2112 12.3 / 14.8; T = 16:
+// 2816 x 512 8.8 / 9.3).
+bool skinny_splits_hidden(int T, int I) { return T <= 4 || (T <= 16 && I <= 512); }
+
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
+  if (a.split_x && a.split_y) return cudaErrorInvalidValue;
   const bool gated = a.act != kActNone;
   SkinnyParams p{};
   p.x = static_cast<const uint8_t*>(a.x);
@@ -354,6 +387,8 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   p.act = a.act;
   p.f16 = a.dtype == kF16;
   p.after = a.after_producer;
+  p.split = a.split_x || a.split_y;
+  if (a.split_x) p.T = 2 * a.T;
   const bool opt = a.mx ? a.quant_x : p.f16;
   if (a.mx) {
     if (gated) return opt ? launch_nt<1, true, true>(p, st) : launch_nt<1, true, false>(p, st);

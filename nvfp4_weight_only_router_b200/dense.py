@@ -240,7 +240,9 @@ def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dow
                       activation: str = "gelu_tanh", save: bool = False, stream=None):
     """y [T, H] = (act(x gate^T) * (x up^T)) down^T, for bf16 or f16 x [T, H],
     gate, up [I, H], down [H, I]; with save, (y, saved) where saved (8 T I bytes and
-    padding) is what gated_ffn_backward takes."""
+    padding) is what gated_ffn_backward takes.  The hidden activations are rounded
+    to the 16-bit type, but not for a few tokens without save, where y may so
+    differ by that rounding."""
     if stream is None:
         out = _calls.ffn_forward(x, gate, up, down, _act(activation, gated=True), save)
         if out is not None:

@@ -114,8 +114,10 @@ def gate64(g, dg, up, dup, act):
     return a * up, da * up.abs() + (a.abs() + da) * dup + FAST * (a * up).abs()
 
 
-def ffn64(x, gate, up, down, dy, act, dtype):
-    """{name: (value, bound)} of the forward and backward pass."""
+def ffn64(x, gate, up, down, dy, act, dtype, hidden_parts=1):
+    """{name: (value, bound)} of the forward and backward pass; hidden_parts 2: of
+    the forward pass with h in two 16-bit parts, the second rounded as a value of
+    at most half a step of the first."""
     r, tiny = HALF_STEP[dtype], TINY[dtype]
 
     def stored(v, e):
@@ -124,8 +126,9 @@ def ffn64(x, gate, up, down, dy, act, dtype):
     g, eg = dot(x, gate)
     u, eu = dot(x, up)
     h, eh = gate64(g, eg, u, eu, act)
-    eh = stored(h, eh)
+    eh = stored(h, eh) if hidden_parts == 1 else eh + r * r * (h.abs() + eh) + tiny
     y, ey = dot(h, down)
+    ey = ey * (1 if hidden_parts == 1 else 1 + r)   # the second parts' products
     out = {"y": (y, stored(y, ey + eh @ down.abs().T))}
     if dy is None:
         return out

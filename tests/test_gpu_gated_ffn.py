@@ -47,6 +47,34 @@ def test_forward(dev, T, H, I, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("T,H,I", [(T, H, I) for T in (1, 2, 3, 4) for H, I in ((352, 160), (8, 8), (136, 4000), (2816, 2112))]
+                                  + [(5, 8, 8), (8, 352, 160), (9, 136, 512), (16, 2816, 512)])
+def test_few_tokens_round_once(dev, T, H, I, dtype):
+    """For few tokens y is off by its own rounding, not by that of h as well."""
+    x, gate, up, down, _ = _make(T + I, T, H, I, dtype, dev)
+    for act, k in (("gelu_tanh", 1.0), ("silu", 1.0), ("silu", 2.0 ** -7)):   # k: h among f16's smallest numbers
+        z = x * k
+        y = lib.gated_ffn_forward(z, gate, up, down, act)
+        ref = R.ffn64(z.double(), gate.double(), up.double(), down.double(), None, act, dtype, hidden_parts=2)["y"]
+        assert lib.device_status() == 0
+        R.assert_within(y, *ref, f"y {T} {H} {I} {act} {k}")
+
+
+@pytest.mark.parametrize("T", [3, 10])
+def test_few_tokens_beyond_f16(dev, T):
+    """An h past f16's range is the infinity that it is with more tokens, and
+    reaches its token alone."""
+    x, gate, up, down, _ = _make(5, T, 64, 48, F16, dev)
+    clean = lib.gated_ffn_forward(x, gate, up, down)
+    x[1] *= 3000
+    y = lib.gated_ffn_forward(x, gate, up, down)
+    many = lib.gated_ffn_forward(x.repeat(20, 1), gate, up, down)[:T]
+    assert torch.equal(y[0], clean[0]) and torch.equal(y[2:], clean[2:])
+    assert not torch.isfinite(many[1]).all()
+    assert torch.equal(torch.isnan(y[1]), torch.isnan(many[1])) and torch.equal(torch.isinf(y[1]), torch.isinf(many[1]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
 @pytest.mark.parametrize("T,H,I", [(1, 64, 64), (5, 8, 8), (31, 72, 136), (64, 256, 256), (65, 264, 200), (130, 520, 264),
                                    (257, 128, 1000), (1000, 640, 64), (513, 1024, 768)])
 def test_step(dev, T, H, I, dtype):
