@@ -123,9 +123,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 // Execution order only: barrier initialisation has its own fence, and at the
-// end nothing is handed over (the releasing form takes 1000 cycles).
+// end each SM has waited for every arrival that the other, or a commit, sends to
+// its barriers (the releasing form takes 1000 cycles, and would not order the
+// commits' arrivals).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A pair that gave up has not: this one orders what its threads did before.
+__device__ __forceinline__ void cluster_sync_ordered() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // shared::cluster address of `p` in SM 0 of the pair
 __device__ __forceinline__ uint32_t leader_addr(const void* p) {
@@ -466,6 +472,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
       }
     }
     if (lane == 0) sm.issued[turn] = issued;
+    // The last products' commits arrive on the stages' barriers of both SMs: an SM
+    // leaves behind them (a stage that was never used is free at once).
+    for (int i = 0; i < C::NS && ok; ++i) {
+      ok = swait(sm, &sm.empty[s], parity, p.status);
+      if (++s == C::NS) {
+        s = 0;
+        parity ^= 1;
+      }
+    }
   } else if (warp == kPMma) {
     // ---------------------------------------------------------- MMA issuer
     if (rank == 0) {
@@ -541,9 +556,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
       // every MMA issued has completed before the tear-down
       if (elect_one()) commit_pair(&sm.fin);
       __syncwarp();
-      mbar_wait_bounded(&sm.fin, 0);
-      __syncwarp();
+      // as have the arrivals of both SMs' epilogues, of each accumulator's last tile
+      for (uint32_t db = 0; db < 2 && ok; ++db)
+        if (titer > db) ok = __all_sync(0xffffffffu, pwait(sm, &sm.d_empty[db], ((titer - 1 - db) >> 1) & 1, p.status));
     }
+    mbar_wait_bounded(&sm.fin, 0);
+    __syncwarp();
   } else if (KIND == kKindMx && warp == kPScale) {
     // ------------------------- scales into tensor memory, ahead of the products
     if (rank == 0) {
@@ -774,7 +792,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
       mbar_wait_bounded(&sm.full[it % C::NS], (it / C::NS) & 1, kAbortDrainNs);
   }
   __syncthreads();
-  cluster_sync();
+  if (sm.abort_flag) cluster_sync_ordered();
+  else cluster_sync();
   if (warp == kPMma) {
     tc_fence_after();
     tmem_dealloc2(taddr, kPTmem);
