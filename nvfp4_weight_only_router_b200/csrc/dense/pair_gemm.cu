@@ -177,11 +177,27 @@ __device__ __forceinline__ void commit_here(uint64_t* bar) {  // arrives in this
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-// On a barrier of either SM.  What the waiter goes on to touch is ordered by
-// the tcgen05 and proxy fences around, within each SM; a release at cluster
-// scope would order all memory, about 1000 cycles each time.
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// On a barrier of either SM, of an epilogue that has read its accumulator: what is
+// ordered is tensor memory alone, by the tcgen05 fences on both sides; a release
+// at cluster scope would order all memory, about 1000 cycles each time.
+__device__ __forceinline__ void arrive_read(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same of a converter that has written shared memory for products which a
+// thread of the other SM issues: a release that this thread observes.
+__device__ __forceinline__ void arrive_written(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 __device__ __forceinline__ void mma16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -240,6 +256,13 @@ template <int KIND, int BN>
 __device__ __forceinline__ bool swait(PSmem<KIND, BN>& sm, uint64_t* bar, uint32_t parity, int* status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, pwait(sm, bar, parity, status));
+}
+// The same for a stage that converters of both SMs have written: the phase has
+// completed, so that the acquiring test succeeds at once.
+template <int KIND, int BN>
+__device__ __forceinline__ bool swait_written(PSmem<KIND, BN>& sm, uint64_t* bar, uint32_t parity, int* status) {
+  if (__all_sync(0xffffffffu, try_wait_cluster(bar, parity))) return true;
+  return swait(sm, bar, parity, status) && __all_sync(0xffffffffu, try_wait_cluster(bar, parity));
 }
 
 template <int NP>
@@ -513,7 +536,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
         const uint64_t bd0 = b_mn ? make_mn_desc(b0) : make_sw128_desc(b0);
         for (int kc = 0; kc < kc_all; ++kc) {
           // MXFP4: the warp that copies the scales has waited for the stage
-          ok = swait(sm, KIND == kKindMx ? &sm.scaled[s] : &sm.full[s], parity, p.status);
+          if constexpr (KIND == kKindW4) ok = swait_written(sm, &sm.full[s], parity, p.status);
+          else ok = swait(sm, KIND == kKindMx ? &sm.scaled[s] : &sm.full[s], parity, p.status);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -682,7 +706,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
       if (__any_sync(0xffffffffu, big)) decode(std::true_type{});
       else decode(std::false_type{});
       out_ready();  // visible to the products
-      if (lane == 0) arrive_cluster(full0 + 8 * s);
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&sm.full[s]);
+        else arrive_written(full0 + 8 * s);
+      }
       return true;
     };
     Stage even, odd;
@@ -767,7 +794,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
         if (c + CW == HC) {  // all read: the accumulator is free
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_cluster(leader_addr(&sm.d_empty[db]));
+          if (lane == 0) arrive_read(leader_addr(&sm.d_empty[db]));
         }
         out_ready();
         if (lane == 0) {

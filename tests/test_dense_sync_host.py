@@ -54,3 +54,18 @@ def test_every_stage_is_drained_once():
                 if s == ns:
                     s, parity = 0, parity ^ 1
             assert len(seen) == ns
+
+
+def test_remote_arrivals_name_their_scope():
+    """An arrival on the other SM's barrier without a scope is ordered for its own
+    block alone.  Converters publish shared memory: a cluster-wide release, and the
+    issuer's wait acquires at that scope."""
+    forms = re.findall(r"mbarrier\.arrive\.[\w.:]*shared::cluster\.b64", KERNEL)
+    assert sorted(set(forms)) == ["mbarrier.arrive.relaxed.cluster.shared::cluster.b64",
+                                  "mbarrier.arrive.release.cluster.shared::cluster.b64"]
+    convert = _between("auto convert = ", "Stage even, odd;")
+    assert "arrive_written(full0" in convert and "arrive_read" not in convert
+    assert "mbarrier.arrive.release" in _between("void arrive_written", "\n}")
+    issue = _between("MMA issuer", "every MMA issued has completed")
+    assert "if constexpr (KIND == kKindW4) ok = swait_written(sm, &sm.full[s]" in issue
+    assert "mbarrier.try_wait.parity.acquire.cluster" in _between("bool try_wait_cluster", "\n}")
