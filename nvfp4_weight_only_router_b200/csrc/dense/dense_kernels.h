@@ -142,12 +142,13 @@ struct PairGatedBwd {
 };
 cudaError_t launch_pair_gated_bwd(const PairGatedBwd& a, int* status, cudaStream_t st);
 // bf16 x MXFP4 weights, decoded on the way into the products.  Every tile of rows
-// decodes them again, in tiles of at most 128 columns; above some tokens decoding
-// once into bf16 for 256-column tiles is faster (us, that / here: 2816 x 2112 T =
-// 512 14.6 / 11.2, T = 2048 27.2 / 25.1, T = 4096 40.8 / 38.6; 4224
-// x 2816 gated T = 512 18.4 / 13.8, T = 2048 39.7 / 38.6, T = 4096 66.7 / 72.1; 8192 x
-// 2816 T = 2048 72.4 / 67.4, T = 4096 118.8 / 132.8)
-constexpr int kPairW4MaxTokens = 2048;
+// decodes them again, in tiles of at most 128 columns; above two tiles of rows
+// decoding once into bf16 for 256-column tiles is faster for most weights (us, that /
+// here: 2816 x 2112 T = 256 12.8 / 10.9, T = 512 14.1 / 13.5, T = 1024 19.5 / 22.5; 4224
+// x 2816 gated 16.2 / 13.7, 18.6 / 17.1, 26.1 / 28.4; 8192 x 2816 19.7 / 16.6, 27.5 /
+// 28.1, 41.2 / 51.3; 32768 x 1024 32.3 / 24.0, 50.0 / 38.3, 61.8 / 69.6; rows as long as
+// 8192 with 2816 columns 27.7 / 30.6, 32.8 / 37.1, 50.2 / 69.2)
+constexpr int kPairW4MaxTokens = 512;
 struct PairW4 {
   const void* x;
   int64_t ldx;

@@ -433,8 +433,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PCfg<KIND, BN>::THRE
   if (warp == kPProdA || warp == kPProdB) {
     // ------------------------------------------- TMA producers of A and of B
     // W4: both of A, a stage each in turn.  A warp takes 550 cycles for a stage's
-    // wait, arrival and two copies, whatever their size; the rest of a stage of 64
-    // columns takes less (2816 x 8192, T = 64: 21.5 -> 19.7 us).
+    // wait, arrival and two copies, whatever their size, nearly as long as the
+    // converters (64 columns: about 600 cycles a stage, the release of SM 1's part
+    // 1000 of the 2400 that a stage's four are shared by).
     const bool is_a = warp == kPProdA || KIND == kKindW4;
     const int turn = warp == kPProdB;
     const uint32_t full0 = leader_addr(&sm.full[0]), op0 = smem_u32(is_a ? sm.a[0][0] : sm.b[0][0]);

@@ -328,12 +328,12 @@ cudaError_t launch_nt(const SkinnyParams& p, cudaStream_t st) {
 // where the CTAs no longer fit the SMs at once (2 on each; up to 16 tokens not even
 // there, the weights then being most of the time), or, with x quantised in every
 // CTA, where there is more than one on an SM or K is long.
-//   W4A16  T = 16:  2816 x 8192 14.2 / 20.9, 16384 x 2816 19.6 / 21.0 (four waves),
-//                   8192 x 8192 26.8 / 26.4, 32768 x 1024 17.1 / 15.9
-//          T = 24:  8192 x 2816 14.9 / 12.0 (two waves), 2816 x 8192 19.0 / 20.9
-//          T = 32:  8192 x 2816 17.3 / 11.9, 2816 x 2112 8.2 / 8.2, 2816 x 8192 23.2 / 20.9
-//          T = 64:  2816 x 2112 14.0 / 8.2 (two waves), 1024 x 1024 3.5 / 6.1
-//          T = 128: 512 x 2816 silu 6.2 / 10.1 (one wave)
+//   W4A16  T = 16:  2816 x 8192 14.0 / 24.4, 16384 x 2816 18.2 / 23.8 (four waves),
+//                   8192 x 8192 27.1 / 35.3, 32768 x 1024 16.5 / 20.6
+//          T = 24:  8192 x 2816 14.6 / 13.9 (two waves), 2816 x 8192 18.7 / 24.5
+//          T = 32:  8192 x 2816 17.0 / 13.9, 2816 x 2112 7.9 / 9.1, 2816 x 8192 22.8 / 24.5
+//          T = 64:  2816 x 2112 14.1 / 9.3 (two waves), 1024 x 1024 3.4 / 6.2
+//          T = 128: 512 x 2816 silu 5.9 / 10.9 (one wave)
 //   W4A4   T = 1:   2816 x 8192 12.0 / 12.2
 //          T = 8:   4224 x 2816 silu 7.1 / 8.1, 8192 x 2816 11.9 / 8.8 (two waves),
 //                   2816 x 8192 15.1 / 12.2 (long)
