@@ -298,8 +298,9 @@ def _own_rows(t: torch.Tensor) -> torch.Tensor:
 
 class _GatedFfn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, gate, up, down, activation):
-        if not any(ctx.needs_input_grad[:4]):
+    def forward(ctx, x, gate, up, down, activation, recorded):
+        # needs_input_grad goes by the tensors alone, also where no graph is recorded
+        if not recorded or not any(ctx.needs_input_grad[:4]):
             return gated_ffn_forward(x, gate, up, down, activation)
         y, saved = gated_ffn_forward(x, gate, up, down, activation, save=True)
         ctx.save_for_backward(x, gate, up, down, saved)
@@ -313,7 +314,7 @@ class _GatedFfn(torch.autograd.Function):
         # an expanded gradient (of a sum) has no rows of its own
         grads = gated_ffn_backward(_own_rows(dy), x, gate, up, down, saved, ctx.activation,
                                    ctx.needs_input_grad[:4])
-        return (*grads, None)
+        return (*grads, None, None)
 
 
 def gated_ffn(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor,
@@ -322,5 +323,5 @@ def gated_ffn(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, down: torch
     First derivatives only.  As with every torch operation, a backward pass can
     be captured into a graph only where no earlier autograd graph of the same
     leaves is alive; gated_ffn_forward and gated_ffn_backward have no such limit."""
-    y = _GatedFfn.apply(_own_rows(x.reshape(-1, x.shape[-1])), gate, up, down, activation)
+    y = _GatedFfn.apply(_own_rows(x.reshape(-1, x.shape[-1])), gate, up, down, activation, torch.is_grad_enabled())
     return y.view(x.shape)
