@@ -81,13 +81,17 @@ py::object dequantize(const Tensor& codes, const Tensor& scales, int64_t K, bool
   return py::cast(std::move(out));
 }
 
-// weight: the address of an mxfp4_weight whose arrays live on `device`
-py::object linear(const Tensor& x, uintptr_t weight, int device, int act, bool a4) {
-  const auto* w = reinterpret_cast<const mxfp4_weight*>(weight);
+// codes [N, 16 B], scales [N, B] of a weight
+py::object linear(const Tensor& x, const Tensor& codes, const Tensor& scales, int act, bool a4) {
   int64_t ld;
   const int dt = dtype_of(x);
-  if (dt < 0 || !rows_ok(x, ld) || x.size(1) != w->K || x.get_device() != device) return py::none();
-  if (x.size(0) > INT32_MAX) return py::none();
+  if (dt < 0 || !rows_ok(x, ld) || scales.dim() != 2 || codes.scalar_type() != at::kByte) return py::none();
+  const int64_t N = scales.size(0), nb = scales.size(1);
+  if (!matrix_ok(codes, N, 16 * nb, codes) || !matrix_ok(scales, N, nb, codes)) return py::none();
+  if (x.size(1) != 32 * nb || x.get_device() != codes.get_device()) return py::none();
+  if (x.size(0) > INT32_MAX || N > INT32_MAX || 32 * nb > INT32_MAX) return py::none();
+  const mxfp4_weight weight{codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(), (int32_t)N, (int32_t)(32 * nb)};
+  const mxfp4_weight* const w = &weight;
   const c10::cuda::CUDAGuard guard(x.device());
   const int32_t T = (int32_t)x.size(0);
   const size_t need = a4 ? mxfp4_linear_a4_workspace_bytes(T, w, act) : mxfp4_linear_workspace_bytes(T, w, act);

@@ -158,16 +158,12 @@ class Mxfp4Weight:
     K: int
 
     def __post_init__(self):
+        self._check()
+
+    def _check(self):
         _check_codes(self.codes, self.scales)
         if self.K != 32 * self.scales.shape[1]:
             raise ValueError(f"K = {self.K} must be a multiple of 32 and match the scales")
-        object.__setattr__(self, "_c", dc.mxfp4_weight(self.codes.data_ptr(), self.scales.data_ptr(),
-                                                       self.codes.shape[0], self.K))
-        object.__setattr__(self, "_at", ctypes.addressof(self._c))
-        object.__setattr__(self, "_device", self.codes.get_device())
-
-    def __reduce__(self):  # copies point to their own arrays
-        return Mxfp4Weight, (self.codes, self.scales, self.K)
 
     @property
     def N(self) -> int:
@@ -190,7 +186,8 @@ def _linear(name, call, size, x, weight, act, stream):
     if x.device != weight.codes.device:
         raise ValueError("x and the weight are on different devices")
     T = x.shape[0]
-    c = _byref(weight._c)
+    weight._check()   # as it is now: its arrays' memory may have been exchanged since
+    c = _byref(dc.mxfp4_weight(weight.codes.data_ptr(), weight.scales.data_ptr(), weight.N, weight.K))
     with _on(stream, x, weight.codes, weight.scales):
         y = x.new_empty((T, weight.N // 2 if act else weight.N))
         need = size(T, c, act)
@@ -205,7 +202,7 @@ def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = 
     gated form y [T, N/2] = act(x Wg^T) * (x Wu^T).  Not differentiable."""
     act = _act(activation)
     if stream is None:
-        y = _calls.linear(x, weight._at, weight._device, act, False)
+        y = _calls.linear(x, weight.codes, weight.scales, act, False)
         if y is not None:
             return y
     return _linear("mxfp4_linear", dc.mxfp4_linear, dc.mxfp4_linear_workspace_bytes, x, weight, act, stream)
@@ -215,7 +212,7 @@ def mxfp4_linear_a4(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None
     """W4A4: mxfp4_linear with x (bf16 or f16) quantised to MXFP4 on the way in."""
     act = _act(activation)
     if stream is None:
-        y = _calls.linear(x, weight._at, weight._device, act, True)
+        y = _calls.linear(x, weight.codes, weight.scales, act, True)
         if y is not None:
             return y
     return _linear("mxfp4_linear_a4", dc.mxfp4_linear_a4, dc.mxfp4_linear_a4_workspace_bytes, x, weight, act, stream)

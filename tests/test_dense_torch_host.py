@@ -27,3 +27,21 @@ def test_gated_ffn_keeps_only_what_a_backward_pass_needs(dense, monkeypatch, gra
     with mode():
         y = dense.gated_ffn(x, *w)
     assert asked == [kept] and y.requires_grad == kept and y.shape == x.shape
+
+
+@pytest.mark.parametrize("a4", [False, True])
+def test_products_read_the_arrays_that_a_weight_has_now(dense, monkeypatch, a4):
+    """Memory exchanged under a weight (set_, resize_) leaves no old address in use."""
+    monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
+    seen = []
+
+    def linear(x, *args):
+        seen.append(args)
+        return x
+    monkeypatch.setattr(dense, "_calls", type("Calls", (), {"linear": staticmethod(linear)}))
+    weight = dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64)
+    codes = torch.ones(8, 32, dtype=torch.uint8)
+    weight.codes.set_(codes)
+    (dense.mxfp4_linear_a4 if a4 else dense.mxfp4_linear)(torch.zeros(1, 64), weight)
+    assert seen[0][0].data_ptr() == codes.data_ptr() and seen[0][1].data_ptr() == weight.scales.data_ptr()
+    assert seen[0][2:] == (0, a4)

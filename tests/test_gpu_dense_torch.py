@@ -26,3 +26,25 @@ def test_gated_ffn_serving_from_parameters(dev, T, mode):
     with mode():
         y = lib.gated_ffn(x, *params)
     assert torch.equal(y, ref) and not y.requires_grad
+
+
+@pytest.mark.parametrize("T", [1, 40, 600])
+def test_weight_arrays_exchanged(dev, T):
+    """Arrays that take other memory (set_): products go by the new one."""
+    gen = torch.Generator(dev).manual_seed(T)
+    x, a, b = (torch.randn(s, generator=gen, device=dev).to(BF) for s in ((T, 96), (64, 96), (64, 96)))
+    first, second = lib.Mxfp4Weight.quantize(a), lib.Mxfp4Weight.quantize(b)
+    old = first.codes.detach()[:], first.scales.detach()[:]       # keeps the first memory allocated
+    for f in (lib.mxfp4_linear, lib.mxfp4_linear_a4):
+        ref = f(x, second)
+        assert not torch.equal(f(x, first), ref)
+    first.codes.set_(second.codes)
+    first.scales.set_(second.scales)
+    for f in (lib.mxfp4_linear, lib.mxfp4_linear_a4):
+        assert torch.equal(f(x, first), f(x, second))
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        y = f(x, first, stream=s)
+        s.synchronize()
+        assert torch.equal(y, f(x, second))
+    del old
