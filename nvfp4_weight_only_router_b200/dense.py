@@ -148,7 +148,7 @@ def _check_codes(codes: torch.Tensor, scales: torch.Tensor) -> None:
     _contiguous("codes and scales", codes, scales)
 
 
-@dataclasses.dataclass(frozen=True)
+@dataclasses.dataclass(frozen=True, eq=False)
 class Mxfp4Weight:
     """An MXFP4 weight matrix [N, K] on the device: codes uint8 [N, K/2] and
     scales uint8 [N, K/32] (K a multiple of 32).  For a gated product the

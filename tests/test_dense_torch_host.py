@@ -45,3 +45,9 @@ def test_products_read_the_arrays_that_a_weight_has_now(dense, monkeypatch, a4):
     (dense.mxfp4_linear_a4 if a4 else dense.mxfp4_linear)(torch.zeros(1, 64), weight)
     assert seen[0][0].data_ptr() == codes.data_ptr() and seen[0][1].data_ptr() == weight.scales.data_ptr()
     assert seen[0][2:] == (0, a4)
+
+
+def test_weights_compare_by_identity(dense, monkeypatch):
+    monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
+    a, b = (dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64) for _ in "ab")
+    assert a == a and a != b and a in [b, a] and len({a, b, a}) == 2
