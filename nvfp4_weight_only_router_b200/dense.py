@@ -22,6 +22,7 @@ import dataclasses
 
 import torch
 
+from . import capi
 from . import dense_capi as dc
 from .dense_capi import check
 
@@ -60,6 +61,12 @@ def _rows(t: torch.Tensor, what: str, features: int | None = None) -> int:
     if ld < f:
         raise ValueError(f"{what} has overlapping rows")
     return ld
+
+
+def _int32(name: str, *sizes: int) -> None:
+    """Refuses sizes that the C call's 32-bit arguments cannot hold (ctypes would cut them)."""
+    if max(sizes) > 0x7FFFFFFF:
+        check(capi.NVFP4_ERR_UNSUPPORTED, name)
 
 
 def _same(what: str, *tensors: torch.Tensor) -> None:
@@ -186,6 +193,7 @@ def _linear(name, call, size, x, weight, act, stream):
     if x.device != weight.codes.device:
         raise ValueError("x and the weight are on different devices")
     T = x.shape[0]
+    _int32(name, T, weight.N, weight.K)
     weight._check()   # as it is now: its arrays' memory may have been exchanged since
     c = _byref(dc.mxfp4_weight(weight.codes.data_ptr(), weight.scales.data_ptr(), weight.N, weight.K))
     with _on(stream, x, weight.codes, weight.scales):
@@ -230,6 +238,7 @@ def _ffn_weights(gate, up, down, activation) -> dc.gated_ffn_weights:
     if gate.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("weights must be bf16 or f16")
     I, H = gate.shape
+    _int32("gated_ffn", I, H)
     return dc.gated_ffn_weights(gate.data_ptr(), up.data_ptr(), down.data_ptr(), H, I, act, _DTYPE[gate.dtype])
 
 
@@ -248,6 +257,7 @@ def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dow
     ld = _rows(x, "x", f.H)
     _same("x and the weights", x, gate)
     T = x.shape[0]
+    _int32("gated_ffn_forward", T)
     with _on(stream, x, gate, up, down):
         y = x.new_empty((T, f.H))
         if save:
@@ -273,6 +283,7 @@ def gated_ffn_backward(dy: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up
     f = _ffn_weights(gate, up, down, activation)
     ld, lddy = _rows(x, "x", f.H), _rows(dy, "dy", f.H)
     T = x.shape[0]
+    _int32("gated_ffn_backward", T)
     _same("dy, x and the weights", dy, x, gate)
     if (dy.shape[0] != T or saved.dtype != torch.uint8 or saved.device != x.device
             or saved.shape != (max(dc.gated_ffn_saved_bytes(T, _byref(f)), 256),)):

@@ -51,3 +51,38 @@ def test_weights_compare_by_identity(dense, monkeypatch):
     monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
     a, b = (dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64) for _ in "ab")
     assert a == a and a != b and a in [b, a] and len({a, b, a}) == 2
+
+
+@pytest.mark.parametrize("which", ["linear T", "linear N", "linear_a4 T", "linear_a4 N", "forward", "forward save", "backward",
+                                   "weights H"])
+def test_sizes_past_32_bits_are_refused(dense, monkeypatch, which):
+    """They would reach the C call cut to their low 32 bits."""
+    import contextlib
+    from nvfp4_weight_only_router_b200 import capi
+    for name in ("_check_codes", "_same", "_contiguous"):
+        monkeypatch.setattr(dense, name, lambda *t: None)
+    monkeypatch.setattr(dense, "_rows", lambda t, *a: t.shape[1])
+    monkeypatch.setattr(dense, "_on", lambda *t: contextlib.nullcontext())
+    monkeypatch.setattr(dense, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(dense, "_calls", type("Calls", (), {n: staticmethod(lambda *a: None)
+                                                            for n in ("linear", "ffn_forward", "ffn_backward")}))
+
+    class Weights(torch.Tensor):
+        is_cuda = True
+
+    def meta(*s, dtype=torch.bfloat16):
+        return torch.Tensor._make_subclass(Weights, torch.empty(s, dtype=dtype, device="meta"))
+    big = 2 ** 32 + 8
+    with pytest.raises(capi.NVFP4Error) as e:
+        if which.startswith("linear"):
+            N, T = (big, 4) if which.endswith("N") else (8, big)
+            w = dense.Mxfp4Weight(meta(N, 16, dtype=torch.uint8), meta(N, 1, dtype=torch.uint8), 32)
+            getattr(dense, "mxfp4_" + which.split()[0])(meta(T, 32), w)
+        else:
+            H, T = (big, 4) if which == "weights H" else (16, big)
+            gate, up, down, x = meta(8, H), meta(8, H), meta(H, 8), meta(T, H)
+            if which == "backward":
+                dense.gated_ffn_backward(x, x, gate, up, down, meta(1 << 40, dtype=torch.uint8))
+            else:
+                dense.gated_ffn_forward(x, gate, up, down, save=which.endswith("save"))
+    assert e.value.status == capi.NVFP4_ERR_UNSUPPORTED
