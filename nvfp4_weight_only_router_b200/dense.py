@@ -104,6 +104,26 @@ def _bytes(n: int, t: torch.Tensor) -> torch.Tensor:
     return t.new_empty(max(n, 256), dtype=torch.uint8)
 
 
+class _Undifferentiated(torch.autograd.Function):
+    """The output of `call`, computed from tensors that a graph is being recorded for:
+    a backward pass that comes to it raises, instead of losing their gradients."""
+    @staticmethod
+    def forward(ctx, call, advice, *inputs):
+        ctx.advice = advice
+        return call()
+
+    @staticmethod
+    def backward(ctx, dy):
+        raise RuntimeError(ctx.advice)
+
+
+def _recorded(*tensors: torch.Tensor) -> bool:
+    for t in tensors:
+        if t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
+
+
 # ------------------------------------------------------------------- MXFP4
 def mxfp4_quantize(x: torch.Tensor, stream=None):
     """bf16, f16 or f32 [R, K] -> (codes uint8 [R, 16 ceil(K/32)], scales uint8
@@ -207,8 +227,12 @@ def _linear(name, call, size, x, weight, act, stream):
 
 def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A16: y [T, N] = x weight^T for bf16 x [T, K]; with an activation the
-    gated form y [T, N/2] = act(x Wg^T) * (x Wu^T).  Not differentiable."""
+    gated form y [T, N/2] = act(x Wg^T) * (x Wu^T).  Not differentiable: a backward
+    pass through y raises."""
     act = _act(activation)
+    if _recorded(x):
+        return _Undifferentiated.apply(lambda: mxfp4_linear(x, weight, activation, stream),
+                                       "mxfp4_linear has no backward pass: give it x.detach()", x)
     if stream is None:
         y = _calls.linear(x, weight.codes, weight.scales, act, False)
         if y is not None:
@@ -219,6 +243,9 @@ def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = 
 def mxfp4_linear_a4(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A4: mxfp4_linear with x (bf16 or f16) quantised to MXFP4 on the way in."""
     act = _act(activation)
+    if _recorded(x):
+        return _Undifferentiated.apply(lambda: mxfp4_linear_a4(x, weight, activation, stream),
+                                       "mxfp4_linear_a4 has no backward pass: give it x.detach()", x)
     if stream is None:
         y = _calls.linear(x, weight.codes, weight.scales, act, True)
         if y is not None:
@@ -248,7 +275,13 @@ def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dow
     gate, up [I, H], down [H, I]; with save, (y, saved) where saved (8 T I bytes and
     padding) is what gated_ffn_backward takes.  The hidden activations are rounded
     to the 16-bit type, but not for a few tokens without save, where y may so
-    differ by that rounding."""
+    differ by that rounding.  For autograd there is gated_ffn: a backward pass
+    through this y raises, and with save y has no graph, gated_ffn_backward being the
+    caller's to call."""
+    if not save and _recorded(x, gate, up, down):
+        return _Undifferentiated.apply(lambda: gated_ffn_forward(x, gate, up, down, activation, stream=stream),
+                                       "gated_ffn_forward has no backward pass of its own: use gated_ffn",
+                                       x, gate, up, down)
     if stream is None:
         out = _calls.ffn_forward(x, gate, up, down, _act(activation, gated=True), save)
         if out is not None:

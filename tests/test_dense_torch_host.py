@@ -86,3 +86,32 @@ def test_sizes_past_32_bits_are_refused(dense, monkeypatch, which):
             else:
                 dense.gated_ffn_forward(x, gate, up, down, save=which.endswith("save"))
     assert e.value.status == capi.NVFP4_ERR_UNSUPPORTED
+
+
+def test_gradients_are_not_lost_in_silence(dense, monkeypatch):
+    """Operators without a backward pass raise where one comes to them, and answer as
+    before where none is recorded."""
+    monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
+    monkeypatch.setattr(dense, "_calls", type("Calls", (), {
+        "linear": staticmethod(lambda x, *a: x.detach() + 1), "ffn_forward": staticmethod(
+            lambda x, *a: (x.detach() + 1, torch.zeros(1)) if a[-1] else x.detach() + 1)}))
+    weight = dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64)
+    x, w = torch.zeros(2, 64), torch.zeros(8, 64)
+    calls = {"mxfp4_linear ": lambda x: dense.mxfp4_linear(x, weight), "mxfp4_linear_a4": lambda x: dense.mxfp4_linear_a4(x, weight),
+             "gated_ffn": lambda x: dense.gated_ffn_forward(x, w, w, w.T)}
+    for text, call in calls.items():
+        leaf = x.clone().requires_grad_()
+        y = call(leaf)
+        assert torch.equal(y, x + 1)
+        y += 1                                   # not a view: may be changed in place
+        with pytest.raises(RuntimeError, match=text):
+            (y.sum() + leaf.sum()).backward()
+        for mode in (torch.no_grad, torch.inference_mode):
+            with mode():
+                assert not call(leaf).requires_grad
+        assert not call(x).requires_grad
+    p = torch.nn.Parameter(w)
+    with pytest.raises(RuntimeError, match="use gated_ffn"):
+        dense.gated_ffn_forward(x, p, w, w.T).sum().backward()
+    y, _ = dense.gated_ffn_forward(x, p, w, w.T, save=True)
+    assert not y.requires_grad
