@@ -7,13 +7,16 @@
 // is short or the call is refused; nothing has been enqueued then, and the caller repeats
 // the steps one by one in Python, where the error is raised.  Work goes to
 // torch's current stream of x's device; memory comes from torch's allocator on
-// that stream.
+// that stream.  The interpreter lock is released meanwhile: allocation may wait for
+// the GPU, and a launch for room in a full queue.
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
 
 #include <optional>
+#include <tuple>
+#include <type_traits>
 
 #include "../../../include/nvfp4dense.h"
 
@@ -45,6 +48,8 @@ bool matrix_ok(const Tensor& t, int64_t r, int64_t c, const Tensor& like) {
          t.scalar_type() == like.scalar_type() && t.get_device() == like.get_device();
 }
 
+using Gradients = std::tuple<std::optional<Tensor>, std::optional<Tensor>, std::optional<Tensor>, std::optional<Tensor>>;
+
 // An uninitialised tensor on like's device (at::empty without its dispatch).
 Tensor empty(at::IntArrayRef size, at::ScalarType type, const Tensor& like) {
   return at::detail::empty_cuda(size, type, like.device(), std::nullopt);
@@ -53,55 +58,55 @@ Tensor bytes(size_t n, const Tensor& like) { return empty({(int64_t)std::max<siz
 
 void* current_stream(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
 
-py::object quantize(const Tensor& x) {
+std::optional<std::tuple<Tensor, Tensor>> quantize(const Tensor& x) {
   int64_t ld;
   const int dt = dtype_of(x);
-  if (dt < 0 || !rows_ok(x, ld)) return py::none();
+  if (dt < 0 || !rows_ok(x, ld)) return std::nullopt;
   const c10::cuda::CUDAGuard guard(x.device());
   const int64_t R = x.size(0), K = x.size(1), nb = (K + 31) / 32;
   Tensor codes = empty({R, 16 * nb}, at::kByte, x), scales = empty({R, nb}, at::kByte, x);
   if (mxfp4_quantize(x.data_ptr(), dt, R, K, ld, codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(),
                      current_stream(x)) != NVFP4_OK)
-    return py::none();
-  return py::make_tuple(std::move(codes), std::move(scales));
+    return std::nullopt;
+  return std::make_tuple(std::move(codes), std::move(scales));
 }
 
 // K < 0: whole blocks
-py::object dequantize(const Tensor& codes, const Tensor& scales, int64_t K, bool bf16) {
-  if (!codes.is_cuda() || !scales.is_cuda() || scales.dim() != 2 || codes.scalar_type() != at::kByte) return py::none();
+std::optional<Tensor> dequantize(const Tensor& codes, const Tensor& scales, int64_t K, bool bf16) {
+  if (!codes.is_cuda() || !scales.is_cuda() || scales.dim() != 2 || codes.scalar_type() != at::kByte) return std::nullopt;
   const int64_t R = scales.size(0), nb = scales.size(1);
-  if (!matrix_ok(codes, R, 16 * nb, codes) || !matrix_ok(scales, R, nb, codes)) return py::none();
+  if (!matrix_ok(codes, R, 16 * nb, codes) || !matrix_ok(scales, R, nb, codes)) return std::nullopt;
   if (K < 0) K = 32 * nb;
-  if ((K + 31) / 32 != nb) return py::none();
+  if ((K + 31) / 32 != nb) return std::nullopt;
   const c10::cuda::CUDAGuard guard(codes.device());
   Tensor out = empty({R, K}, bf16 ? at::kBFloat16 : at::kFloat, codes);
   if (mxfp4_dequantize(codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(), R, K, out.data_ptr(), dtype_of(out),
                        current_stream(codes)) != NVFP4_OK)
-    return py::none();
-  return py::cast(std::move(out));
+    return std::nullopt;
+  return out;
 }
 
 // codes [N, 16 B], scales [N, B] of a weight
-py::object linear(const Tensor& x, const Tensor& codes, const Tensor& scales, int act, bool a4) {
+std::optional<Tensor> linear(const Tensor& x, const Tensor& codes, const Tensor& scales, int act, bool a4) {
   int64_t ld;
   const int dt = dtype_of(x);
-  if (dt < 0 || !rows_ok(x, ld) || scales.dim() != 2 || codes.scalar_type() != at::kByte) return py::none();
+  if (dt < 0 || !rows_ok(x, ld) || scales.dim() != 2 || codes.scalar_type() != at::kByte) return std::nullopt;
   const int64_t N = scales.size(0), nb = scales.size(1);
-  if (!matrix_ok(codes, N, 16 * nb, codes) || !matrix_ok(scales, N, nb, codes)) return py::none();
-  if (x.size(1) != 32 * nb || x.get_device() != codes.get_device()) return py::none();
-  if (x.size(0) > INT32_MAX || N > INT32_MAX || 32 * nb > INT32_MAX) return py::none();
+  if (!matrix_ok(codes, N, 16 * nb, codes) || !matrix_ok(scales, N, nb, codes)) return std::nullopt;
+  if (x.size(1) != 32 * nb || x.get_device() != codes.get_device()) return std::nullopt;
+  if (x.size(0) > INT32_MAX || N > INT32_MAX || 32 * nb > INT32_MAX) return std::nullopt;
   const mxfp4_weight weight{codes.data_ptr<uint8_t>(), scales.data_ptr<uint8_t>(), (int32_t)N, (int32_t)(32 * nb)};
   const mxfp4_weight* const w = &weight;
   const c10::cuda::CUDAGuard guard(x.device());
   const int32_t T = (int32_t)x.size(0);
   const size_t need = a4 ? mxfp4_linear_a4_workspace_bytes(T, w, act) : mxfp4_linear_workspace_bytes(T, w, act);
-  if (need == 0) return py::none();  // refused
+  if (need == 0) return std::nullopt;  // refused
   Tensor y = empty({T, act ? w->N / 2 : w->N}, x.scalar_type(), x), ws;
   if (need > 256) ws = bytes(need, x);
   void* const wp = ws.defined() ? ws.data_ptr() : nullptr;
   const auto call = a4 ? mxfp4_linear_a4 : mxfp4_linear;
-  if (call(x.data_ptr(), dt, ld, T, w, act, y.data_ptr(), wp, need, current_stream(x)) != NVFP4_OK) return py::none();
-  return py::cast(std::move(y));
+  if (call(x.data_ptr(), dt, ld, T, w, act, y.data_ptr(), wp, need, current_stream(x)) != NVFP4_OK) return std::nullopt;
+  return y;
 }
 
 bool ffn_weights(const Tensor& x, const Tensor& gate, const Tensor& up, const Tensor& down, int act, int64_t& ld,
@@ -115,34 +120,35 @@ bool ffn_weights(const Tensor& x, const Tensor& gate, const Tensor& up, const Te
   return true;
 }
 
-py::object ffn_forward(const Tensor& x, const Tensor& gate, const Tensor& up, const Tensor& down, int act, bool save) {
+// (y, what is kept: empty without `save`)
+std::optional<std::tuple<Tensor, Tensor>> ffn_forward_both(const Tensor& x, const Tensor& gate, const Tensor& up,
+                                                           const Tensor& down, int act, bool save) {
   int64_t ld;
   gated_ffn_weights f;
-  if (!ffn_weights(x, gate, up, down, act, ld, f)) return py::none();
+  if (!ffn_weights(x, gate, up, down, act, ld, f)) return std::nullopt;
   const c10::cuda::CUDAGuard guard(x.device());
   const int32_t T = (int32_t)x.size(0);
   const size_t need = save ? gated_ffn_saved_bytes(T, &f) : gated_ffn_forward_workspace_bytes(T, &f);
-  if (need == 0) return py::none();
+  if (need == 0) return std::nullopt;
   Tensor y = empty({T, f.H}, x.scalar_type(), x), ws = bytes(need, x);
   if (gated_ffn_forward(x.data_ptr(), ld, T, &f, y.data_ptr(), save ? ws.data_ptr() : nullptr,
                         save ? nullptr : ws.data_ptr(), save ? 0 : ws.numel(), current_stream(x)) != NVFP4_OK)
-    return py::none();
-  if (save) return py::make_tuple(std::move(y), std::move(ws));
-  return py::cast(std::move(y));
+    return std::nullopt;
+  return std::make_tuple(std::move(y), save ? std::move(ws) : Tensor());
 }
 
-py::object ffn_backward(const Tensor& dy, const Tensor& x, const Tensor& gate, const Tensor& up, const Tensor& down,
+std::optional<Gradients> ffn_backward(const Tensor& dy, const Tensor& x, const Tensor& gate, const Tensor& up, const Tensor& down,
                         const Tensor& saved, int act, bool need_dx, bool need_dgate, bool need_dup, bool need_ddown) {
   int64_t ld, lddy;
   gated_ffn_weights f;
-  if (!ffn_weights(x, gate, up, down, act, ld, f) || !rows_ok(dy, lddy)) return py::none();
+  if (!ffn_weights(x, gate, up, down, act, ld, f) || !rows_ok(dy, lddy)) return std::nullopt;
   const int32_t T = (int32_t)x.size(0);
   if (dy.size(0) != T || dy.size(1) != f.H || dy.scalar_type() != x.scalar_type() || dy.get_device() != x.get_device())
-    return py::none();
+    return std::nullopt;
   const size_t kept = gated_ffn_saved_bytes(T, &f), need = gated_ffn_backward_workspace_bytes(T, &f);
   if (need == 0 || !saved.is_cuda() || saved.scalar_type() != at::kByte || saved.get_device() != x.get_device() ||
       saved.dim() != 1 || !saved.is_contiguous() || saved.numel() != (int64_t)std::max<size_t>(kept, 256))
-    return py::none();
+    return std::nullopt;
   const c10::cuda::CUDAGuard guard(x.device());
   const Tensor ws = bytes(need, x);
   const Tensor* like[] = {&x, &gate, &up, &down};
@@ -156,20 +162,31 @@ py::object ffn_backward(const Tensor& dy, const Tensor& x, const Tensor& gate, c
     }
   if (gated_ffn_backward(dy.data_ptr(), lddy, x.data_ptr(), ld, saved.data_ptr(), T, &f, p[0], p[1], p[2], p[3],
                          ws.data_ptr(), ws.numel(), current_stream(x)) != NVFP4_OK)
-    return py::none();
-  return py::make_tuple(out[0], out[1], out[2], out[3]);
+    return std::nullopt;
+  return Gradients(out[0], out[1], out[2], out[3]);
 }
 
 // An allocation that fails is the Python steps' to report, with torch's own error.
-template <typename... A>
-auto guarded(py::object (*f)(A...)) {
-  return [f](A... a) -> py::object {
-    try {
-      return f(a...);
-    } catch (const c10::Error&) {
-      return py::none();
-    }
-  };
+template <typename R, typename... A>
+std::optional<R> attempt(std::optional<R> (*f)(A...), std::type_identity_t<A>... a) {
+  const py::gil_scoped_release release;
+  try {
+    return f(a...);
+  } catch (const c10::Error&) {
+    return std::nullopt;
+  }
+}
+template <typename R, typename... A>
+auto guarded(std::optional<R> (*f)(A...)) {
+  return [f](A... a) { return attempt(f, a...); };
+}
+
+// y, or (y, saved)
+py::object ffn_forward(const Tensor& x, const Tensor& gate, const Tensor& up, const Tensor& down, int act, bool save) {
+  auto out = attempt(&ffn_forward_both, x, gate, up, down, act, save);
+  if (!out) return py::none();
+  if (save) return py::cast(std::move(*out));
+  return py::cast(std::move(std::get<0>(*out)));
 }
 
 }  // namespace
@@ -178,6 +195,6 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
   m.def("quantize", guarded(&quantize));
   m.def("dequantize", guarded(&dequantize));
   m.def("linear", guarded(&linear));
-  m.def("ffn_forward", guarded(&ffn_forward));
+  m.def("ffn_forward", &ffn_forward);
   m.def("ffn_backward", guarded(&ffn_backward));
 }

@@ -48,3 +48,36 @@ def test_weight_arrays_exchanged(dev, T):
         s.synchronize()
         assert torch.equal(y, f(x, second))
     del old
+
+
+def test_other_threads_run_while_a_launch_waits(dev):
+    """Launches into a full queue wait for the GPU; the interpreter goes on."""
+    import threading
+    import time
+    x, *w = _make(3, 4, 64, 64, dev)
+    weight = lib.Mxfp4Weight.quantize(w[0])
+    lib.mxfp4_linear(x, weight)
+    torch.cuda.synchronize()
+    gaps, stop = [0.0], threading.Event()
+
+    def other():
+        last = time.monotonic()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.monotonic()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+    thread = threading.Thread(target=other)
+    thread.start()
+    # about a second of sleep on the GPU, then more launches than a queue holds
+    torch.cuda._sleep(int(1.9e9))
+    began = time.monotonic()
+    for _ in range(6000):
+        lib.mxfp4_linear(x, weight)
+    waited = time.monotonic() - began
+    stop.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert lib.device_status() == 0
+    assert waited > 0.5, "the queue never filled: the test shows nothing"
+    assert gaps[0] < waited / 2, (gaps, waited)
