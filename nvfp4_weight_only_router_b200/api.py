@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import sys
 
 import numpy as np
 import torch
@@ -441,7 +442,9 @@ def residual_rmsnorm(res: torch.Tensor, y: torch.Tensor | None, x_out: torch.Ten
 
 
 def device_status(stream=None) -> int:
-    """The first recorded device error of either library (0 if none), cleared."""
-    from . import dense_capi
-    first = capi.nvfp4_get_device_status(_stream(stream))
-    return dense_capi.nvfp4dense_get_device_status(_stream(stream)) or first
+    """A recorded device error (0 if none), cleared: of the MoE library, or where it
+    has none, of the dense one if that is loaded.  An error of the one leaves the
+    other's to the next call."""
+    status = capi.nvfp4_get_device_status(_stream(stream))
+    dense = sys.modules.get(__package__ + ".dense_capi")
+    return status if status or dense is None else dense.nvfp4dense_get_device_status(_stream(stream))

@@ -115,3 +115,36 @@ def test_gradients_are_not_lost_in_silence(dense, monkeypatch):
         dense.gated_ffn_forward(x, p, w, w.T).sum().backward()
     y, _ = dense.gated_ffn_forward(x, p, w, w.T, save=True)
     assert not y.requires_grad
+
+
+@pytest.mark.parametrize("moe,other,answers", [(0, 0, [0, 0]), (5, 0, [5, 0]), (0, 5, [5, 0]), (7, 5, [7, 5, 0])])
+def test_device_status_loses_neither_librarys_error(dense, monkeypatch, moe, other, answers):
+    import nvfp4_weight_only_router_b200 as lib
+    from nvfp4_weight_only_router_b200 import api, capi, dense_capi
+    words = {"moe": moe, "dense": other}
+
+    monkeypatch.setattr(api, "_stream", lambda s=None: 0)
+    monkeypatch.setattr(capi, "nvfp4_get_device_status", lambda s: _take(words, "moe"))
+    monkeypatch.setattr(dense_capi, "nvfp4dense_get_device_status", lambda s: _take(words, "dense"))
+    assert [lib.device_status() for _ in answers] == answers
+
+
+def _take(words, which):
+    got, words[which] = words[which], 0
+    return got
+
+
+def test_device_status_without_the_dense_library():
+    """Where the dense library was never loaded no kernel of it has run: its word is
+    not asked for, and the library need not be there."""
+    import subprocess
+    import sys
+    code = ("import sys\n"
+            "from nvfp4_weight_only_router_b200 import api, capi\n"
+            "sys.modules['nvfp4_weight_only_router_b200.dense_capi'] = None\n"      # its import fails
+            "api._stream = lambda s=None: 0\n"
+            "capi.nvfp4_get_device_status = lambda s: 3\n"
+            "assert api.device_status() == 3\n"
+            "capi.nvfp4_get_device_status = lambda s: 0\n"
+            "assert api.device_status() == 0\n")
+    subprocess.run([sys.executable, "-c", code], check=True)
