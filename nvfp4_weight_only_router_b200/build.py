@@ -1,7 +1,8 @@
 """Build the in-tree shared libraries libnvfp4moe.so (csrc/*.cu) and
 libnvfp4dense.so (csrc/dense/*.cu and the host helpers it shares) for sm_100a
 with nvcc, and _dense_calls.so (csrc/dense/torch_calls.cpp), torch's calls of
-the latter, with the host compiler.
+the latter, with g++.  The C libraries need no torch:
+where it is not installed, torch's calls are left out.
 
     python -m nvfp4_weight_only_router_b200.build [--force] [--verbose]
 
@@ -12,6 +13,7 @@ any header is newer than their object.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -55,15 +57,19 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     calls = os.path.join(CSRC, "dense", "torch_calls.cpp")
     calls_obj = os.path.join(BUILD, "dense_torch_calls.o")
     abi = max(os.path.getmtime(f) for f in [calls] + glob.glob(os.path.join(ROOT, "include", "*.h")))
+    with_torch = importlib.util.find_spec("torch") is not None
     with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
         host = None
-        if force or not os.path.exists(calls_obj) or os.path.getmtime(calls_obj) < abi:
+        if with_torch and (force or not os.path.exists(calls_obj) or os.path.getmtime(calls_obj) < abi):
             host = pool.submit(_compile_calls, calls, calls_obj, verbose)
         list(pool.map(lambda so: _compile(*so, flags, verbose), stale))
-        if host is not None:
-            host.result()
     _link(LIB, list(main.values()), force, verbose)
     _link(DENSE_LIB, list(dense.values()) + [_object(os.path.join(CSRC, n + ".cu")) for n in DENSE_SHARED], force, verbose)
+    if not with_torch:
+        print(f"torch is not installed: {os.path.basename(DENSE_CALLS)} is not built", file=sys.stderr)
+        return LIB
+    if host is not None:
+        host.result()
     if force or not os.path.exists(DENSE_CALLS) or os.path.getmtime(calls_obj) > os.path.getmtime(DENSE_CALLS):
         _link_calls(calls_obj, verbose)
     return LIB
