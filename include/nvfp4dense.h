@@ -114,8 +114,8 @@ typedef struct {
  *         per token and hidden unit, and padding: rows of 64, blocks of 32 x 16
  *         tokens x hidden units), or NULL
  * fp32 accumulation; h is rounded to the 16-bit type (without `saved`, at up to 4
- * tokens, or 16 with I <= 512: kept as two of them).  T <= 2^20.  With `saved` the
- * workspace is not used.
+ * tokens, or 16 with I <= 512 and T H I <= 140e6: kept as two of them).  T <= 2^20.
+ * With `saved` the workspace is not used.
  * ------------------------------------------------------------------------- */
 NVFP4DENSE_API size_t gated_ffn_saved_bytes(int32_t T, const gated_ffn_weights* f);
 NVFP4DENSE_API size_t gated_ffn_forward_workspace_bytes(int32_t T, const gated_ffn_weights* f);

@@ -305,7 +305,7 @@ size_t gated_ffn_saved_bytes(int32_t T, const gated_ffn_weights* f) {
 size_t gated_ffn_forward_workspace_bytes(int32_t T, const gated_ffn_weights* f) {
   // h, in two parts for few tokens
   return check_ffn(T, f) == NVFP4_OK
-             ? round_up((size_t)T * pair_pitch(f->I) * (skinny_splits_hidden(T, f->I) ? 4 : 2) + 1, 256) : 0;
+             ? round_up((size_t)T * pair_pitch(f->I) * (skinny_splits_hidden(T, f->H, f->I) ? 4 : 2) + 1, 256) : 0;
 }
 
 nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gated_ffn_weights* f, void* y, void* saved,
@@ -325,7 +325,7 @@ nvfp4_status gated_ffn_forward(const void* x, int64_t ldx, int32_t T, const gate
   int* status = device_status_ptr();
   void* const h = saved ? saved : ws;
   const bool fits = skinny_fits_ffn(T, f->H, f->I), few = fits && !saved;  // what is kept: only by the other kernel
-  const bool split = few && skinny_splits_hidden(T, f->I);
+  const bool split = few && skinny_splits_hidden(T, f->H, f->I);
   const int64_t ldh = few ? f->I : pair_pitch(f->I);
   cudaError_t e;
   if (few) {

@@ -57,7 +57,7 @@ int sms();
 // columns), or for both products of a gated block
 bool skinny_fits_mx(int T, int N, int K, bool gated, bool quant_x);
 bool skinny_fits_ffn(int T, int H, int I);
-bool skinny_splits_hidden(int T, int I);
+bool skinny_splits_hidden(int T, int H, int I);
 struct SkinnyArgs {
   const void* x;      // [T, K]
   int64_t ldx;        // elements

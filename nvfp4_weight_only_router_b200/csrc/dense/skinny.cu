@@ -357,7 +357,7 @@ bool skinny_fits_ffn(int T, int H, int I) {
   return T <= 8 || (T <= 64 && (int64_t)T * H * I <= 140000000);
 }
 
-// Whether the block keeps h in two 16-bit parts, so that y is off by its own
+// Whether the block, where it is this kernel's, keeps h in two 16-bit parts, so that y is off by its own
 // rounding alone.  Rounded once to 16 bits, h leaves y 1.4 times that far from the
 // exact one, and where few hidden units make up its sums up to 1.8 times.  Up to four
 // tokens the second parts are columns that the tensor instruction has anyway (us, one
@@ -365,7 +365,9 @@ bool skinny_fits_ffn(int T, int H, int I) {
 // x 4096 T = 4 12.5 / 13.7); for more the second product takes twice the tokens
 // (T = 8: 2816 x 512 8.4 / 7.4, 1024 x 512 4.7 / 4.9, 2816 x 2112 12.3 / 14.8; T = 16:
 // 2816 x 512 8.8 / 9.3).
-bool skinny_splits_hidden(int T, int I) { return T <= 4 || (T <= 16 && I <= 512); }
+bool skinny_splits_hidden(int T, int H, int I) {
+  return skinny_fits_ffn(T, H, I) && (T <= 4 || (T <= 16 && I <= 512));
+}
 
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
   if (a.split_x && a.split_y) return cudaErrorInvalidValue;
