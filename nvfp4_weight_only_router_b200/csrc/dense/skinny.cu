@@ -109,8 +109,10 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
   auto red = reinterpret_cast<float4(*)[NT8][32]>(xs);  // behind the last pass
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  if (!p.after) after_previous();
-  let_next();
+  if (!p.after) {
+    after_previous();
+    let_next();
+  }
 
   // this CTA's tokens
   const uint8_t* px = p.x + (size_t)blockIdx.y * (NT8 * 8) * p.ldx_bytes;
@@ -164,7 +166,10 @@ __global__ void __launch_bounds__(kSkThreads, 2) skinny_kernel(SkinnyParams p) {
         }
       }
     }
-    if (first && p.after) after_previous();
+    if (first && p.after) {
+      after_previous();
+      let_next();
+    }
     if constexpr (XS) {
       if (first && p.after) copy_x();
       asm volatile("cp.async.wait_all;" ::: "memory");

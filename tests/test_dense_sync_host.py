@@ -69,3 +69,17 @@ def test_remote_arrivals_name_their_scope():
     issue = _between("MMA issuer", "every MMA issued has completed")
     assert "if constexpr (KIND == kKindW4) ok = swait_written(sm, &sm.full[s]" in issue
     assert "mbarrier.try_wait.parity.acquire.cluster" in _between("bool try_wait_cluster", "\n}")
+
+
+def test_the_next_kernel_starts_behind_the_wait():
+    """let_next() directly follows after_previous() in every kernel: a kernel that waits
+    for its predecessor knows everything before that one complete as well."""
+    import glob
+    found = 0
+    for path in glob.glob(os.path.join(ROOT, "nvfp4_weight_only_router_b200", "csrc", "dense", "*.cu")):
+        src = open(path).read()
+        for call in re.finditer(r"\blet_next\(\);", src):
+            assert re.search(r"after_previous\(\);\s*$", src[:call.start()]), (path, src[call.start() - 80:call.end()])
+            found += 1
+        assert len(re.findall(r"\bafter_previous\(\);", src)) == len(re.findall(r"\blet_next\(\);", src)), path
+    assert found >= 7
