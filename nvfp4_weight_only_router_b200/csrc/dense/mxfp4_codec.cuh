@@ -170,9 +170,12 @@ __device__ __forceinline__ void unpack16x2(uint32_t v, bool f16, float& lo, floa
 // ---------------------------------------------------------------- activations
 // gelu_tanh and silu with their derivatives, in fp32.  With s = 1 / (1 + exp(-z)),
 // silu: z = g, gelu_tanh: z = 2 sqrt(2/pi) (g + 0.044715 g^3) (0.5 (1 + tanh(z / 2)) = s):
-// act = g s, act' = s + g s (1 - s) dz/dg.  The fast exponential and division
-// (2^-21 relative together) run once per hidden unit in epilogues that must not
-// outlast the products; exp overflow gives the limit s = 0.
+// act = g s, act' = s + g s (1 - s) dz/dg.  The fast exponential and division run
+// once per hidden unit in epilogues that must not outlast the products.  In units of
+// 2^-23, the exponential is off by 2 + 1.173 |z| relative, z's own roundings move it by up
+// to 3.3 |z|, the sum, division and product add 4: s and act are within 2^-20 (1 + 0.6 |z|)
+// relative (z < 0; above, the exponential is a small part of the sum and 2^-20 holds),
+// which 16 bits do not show.  Where exp exceeds 2^126 the division gives the limit s = 0.
 constexpr float kGeluK0 = 1.5957691216057308f, kGeluK1 = 0.044715f;  // 2 sqrt(2 / pi)
 __device__ __forceinline__ float act_fwd(float g, int act) {
   const float z = act == kActSilu ? g : kGeluK0 * (g + kGeluK1 * g * g * g);
