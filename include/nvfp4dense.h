@@ -56,8 +56,9 @@ extern "C" {
  * (a = 0: -127), scale byte X + 127, code = the E2M1 value nearest to x 2^-X,
  * ties to the even code, saturating at 6.  A block that holds a NaN or an
  * infinity gets scale 255 and codes 0, so that it reads as NaN.
- * x may be of any alignment its type has.  rows <= 2^31 - 1, K < 2^24,
- * rows * K < 2^40.
+ * x may be of any alignment its type has; rows off the 16-byte grid are read by the
+ * aligned 16-byte pieces that hold their elements, so up to 14 bytes before and behind
+ * a row too, whatever these hold.  rows <= 2^31 - 1, K < 2^24, rows * K < 2^40.
  * ------------------------------------------------------------------------- */
 NVFP4DENSE_API nvfp4_status mxfp4_quantize(const void* x_dev, int32_t dtype, int64_t rows, int64_t K, int64_t ldx,
                                            uint8_t* codes_dev, uint8_t* scales_dev, void* stream);
