@@ -21,6 +21,7 @@ import ctypes
 import dataclasses
 
 import torch
+from torch.autograd import forward_ad
 
 from . import capi
 from . import dense_capi as dc
@@ -118,6 +119,8 @@ class _Undifferentiated(torch.autograd.Function):
 
 
 def _recorded(*tensors: torch.Tensor) -> bool:
+    if forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled():   # tensors may carry tangents
+        return True
     for t in tensors:
         if t.requires_grad:
             return torch.is_grad_enabled()

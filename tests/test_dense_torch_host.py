@@ -148,3 +148,19 @@ def test_device_status_without_the_dense_library():
             "capi.nvfp4_get_device_status = lambda s: 0\n"
             "assert api.device_status() == 0\n")
     subprocess.run([sys.executable, "-c", code], check=True)
+
+
+def test_tangents_are_not_lost_in_silence(dense, monkeypatch):
+    """Forward-mode derivatives: refused, as gated_ffn refuses them."""
+    import torch.autograd.forward_ad as fw
+    monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
+    monkeypatch.setattr(dense, "_calls", type("Calls", (), {"linear": staticmethod(lambda x, *a: x.clone()),
+                                                            "ffn_forward": staticmethod(lambda x, *a: x.clone())}))
+    weight = dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64)
+    x, w = torch.zeros(2, 64), torch.zeros(8, 64)
+    for call in (lambda x: dense.mxfp4_linear(x, weight), lambda x: dense.mxfp4_linear_a4(x, weight),
+                 lambda x: dense.gated_ffn_forward(x, w, w, w.T), lambda x: dense.gated_ffn(x, w, w, w.T)):
+        with fw.dual_level():
+            assert torch.equal(call(x), x)
+            with pytest.raises(NotImplementedError, match="jvp"):
+                call(fw.make_dual(x, torch.ones_like(x)))

@@ -81,3 +81,50 @@ def test_other_threads_run_while_a_launch_waits(dev):
     assert lib.device_status() == 0
     assert waited > 0.5, "the queue never filled: the test shows nothing"
     assert gaps[0] < waited / 2, (gaps, waited)
+
+
+def _forms(dev):
+    x, *w = _make(5, 40, 64, 48, dev)
+    weight = lib.Mxfp4Weight.quantize(w[0])
+    return x, {"linear": lambda t: lib.mxfp4_linear(t, weight), "a4": lambda t: lib.mxfp4_linear_a4(t, weight),
+               "quantize": lambda t: lib.mxfp4_quantize(t)[0], "forward": lambda t: lib.gated_ffn_forward(t, *w),
+               "ffn": lambda t: lib.gated_ffn(t, *w)}
+
+
+@pytest.mark.filterwarnings("ignore")
+@pytest.mark.parametrize("name", ["linear", "a4", "quantize", "forward", "ffn"])
+def test_inside_compiled_functions(dev, name):
+    """torch.compile leaves the calls as they are (a graph break each)."""
+    x, forms = _forms(dev)
+    torch._dynamo.reset()
+
+    def f(t):
+        return forms[name](t * 2) + 1
+    assert torch.equal(torch.compile(f, backend="eager")(x), f(x))
+
+
+@pytest.mark.parametrize("name", ["linear", "a4", "quantize", "forward", "ffn"])
+def test_function_transforms_are_refused(dev, name):
+    """Tensors without memory of their own: refused, nothing is launched."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    x, forms = _forms(dev)
+    f = forms[name]
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(f)(torch.stack((x, x)))
+    if name != "quantize":
+        with pytest.raises(RuntimeError):
+            torch.func.grad(lambda t: f(t).float().sum())(x)
+    with FakeTensorMode(allow_non_fake_inputs=True) as mode, pytest.raises(RuntimeError):
+        f(mode.from_tensor(x))
+    assert lib.device_status() == 0
+
+
+def test_checkpointed_block(dev):
+    from torch.utils.checkpoint import checkpoint
+    x, *w = _make(6, 40, 64, 48, dev)
+    grads = []
+    for run in (lambda *t: lib.gated_ffn(*t), lambda *t: checkpoint(lib.gated_ffn, *t, use_reentrant=False)):
+        leaves = [t.clone().requires_grad_() for t in (x, *w)]
+        run(*leaves).float().sum().backward()
+        grads.append([t.grad for t in leaves])
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
