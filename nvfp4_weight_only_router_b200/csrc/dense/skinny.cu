@@ -353,11 +353,12 @@ bool skinny_fits_mx(int T, int N, int K, bool gated, bool quant_x) {
 
 // The gated block, both products by one kernel or both by the other (a mixture
 // is slower than either: the second then waits for the first).  T H I at the
-// crossing, in millions, for I x H: 1024 x 8192 180, 2112 x 2816 190, 2816 x 2112
-// 110, 4096 x 1024 125, 4096 x 2816 138, 5632 x 2816 150.  At T = 16: 2112 x 2816
-// 12.7 / 16.1, 1024 x 8192 21.4 / 24.0, 5632 x 2816 35.4 / 34.1.  At T = 8 the
-// few-token kernel always (8192 x 2816 40.0 / 42.4), above 64 never (1024 x 1024
-// at 96: 10.8 / 10.1).
+// crossing, in millions, for I x H (weights not in L2): 1024 x 8192 270, 2112 x 2816
+// 200, 2816 x 2112 70, 4096 x 1024 120, 4096 x 2816 130, 5632 x 2816 160; the limit is
+// off by at most 3% of the time for these.  At T = 16: 2112 x 2816 15.1 / 18.9, 2816 x
+// 2112 20.0 / 19.7, 1024 x 8192 25.4 / 29.9, 5632 x 2816 39.3 / 36.5.  At T = 8 the
+// few-token kernel always (8192 x 2816 42.9 / 44.9), above 64 never (1024 x 1024
+// at 96: 10.9 / 10.8).
 bool skinny_fits_ffn(int T, int H, int I) {
   return T <= 8 || (T <= 64 && (int64_t)T * H * I <= 140000000);
 }
@@ -366,10 +367,10 @@ bool skinny_fits_ffn(int T, int H, int I) {
 // rounding alone.  Rounded once to 16 bits, h leaves y 1.4 times that far from the
 // exact one, and where few hidden units make up its sums up to 1.8 times.  Up to four
 // tokens the second parts are columns that the tensor instruction has anyway (us, one
-// part / two, weights not in L2: 2816 x 2112 T = 1 10.6 / 10.7, T = 4 11.0 / 11.5, 1024
-// x 4096 T = 4 12.5 / 13.7); for more the second product takes twice the tokens
-// (T = 8: 2816 x 512 8.4 / 7.4, 1024 x 512 4.7 / 4.9, 2816 x 2112 12.3 / 14.8; T = 16:
-// 2816 x 512 8.8 / 9.3).
+// part / two, weights not in L2, H x I: 2816 x 2112 T = 1 10.9 / 11.0, T = 4 11.6 / 12.0,
+// 1024 x 4096 T = 4 12.8 / 14.0); for more the second product takes twice the tokens
+// (T = 8: 2816 x 512 7.3 / 7.3, 1024 x 512 4.7 / 4.9, 2816 x 2112 12.6 / 14.9; T = 16:
+// 2816 x 512 8.3 / 8.8).
 bool skinny_splits_hidden(int T, int H, int I) {
   return skinny_fits_ffn(T, H, I) && (T <= 4 || (T <= 16 && I <= 512));
 }
