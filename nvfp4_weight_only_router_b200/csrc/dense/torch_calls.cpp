@@ -3,13 +3,15 @@
 // Through ctypes the same steps take 9 to 18 us of host time, more than the
 // kernels of few tokens take on the GPU.
 //
-// Every function returns None where an argument is not as the call needs it, memory
-// is short or the call is refused; nothing has been enqueued then, and the caller repeats
+// Every function returns None where an argument is not as the call needs it, autograd
+// follows an operator without a backward pass, memory is short or the call is refused; nothing has been enqueued then, and the caller repeats
 // the steps one by one in Python, where the error is raised.  Work goes to
 // torch's current stream of x's device; memory comes from torch's allocator on
 // that stream.  The interpreter lock is released meanwhile: allocation may wait for
 // the GPU, and a launch for room in a full queue.
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -41,6 +43,12 @@ bool rows_ok(const Tensor& t, int64_t& ld) {
   if (f > 1 && t.stride(1) != 1) return false;
   ld = n <= 1 ? f : t.stride(0);
   return ld >= f;
+}
+
+// Whether autograd would follow what is computed from t: in a graph, or by a tangent.
+bool recorded(const Tensor& t) {
+  if (t.requires_grad() && c10::GradMode::is_enabled()) return true;
+  return t._fw_grad(0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode();
 }
 
 bool matrix_ok(const Tensor& t, int64_t r, int64_t c, const Tensor& like) {
@@ -90,7 +98,7 @@ std::optional<Tensor> dequantize(const Tensor& codes, const Tensor& scales, int6
 std::optional<Tensor> linear(const Tensor& x, const Tensor& codes, const Tensor& scales, int act, bool a4) {
   int64_t ld;
   const int dt = dtype_of(x);
-  if (dt < 0 || !rows_ok(x, ld) || scales.dim() != 2 || codes.scalar_type() != at::kByte) return std::nullopt;
+  if (dt < 0 || recorded(x) || !rows_ok(x, ld) || scales.dim() != 2 || codes.scalar_type() != at::kByte) return std::nullopt;
   const int64_t N = scales.size(0), nb = scales.size(1);
   if (!matrix_ok(codes, N, 16 * nb, codes) || !matrix_ok(scales, N, nb, codes)) return std::nullopt;
   if (x.size(1) != 32 * nb || x.get_device() != codes.get_device()) return std::nullopt;
@@ -126,6 +134,7 @@ std::optional<std::tuple<Tensor, Tensor>> ffn_forward_both(const Tensor& x, cons
   int64_t ld;
   gated_ffn_weights f;
   if (!ffn_weights(x, gate, up, down, act, ld, f)) return std::nullopt;
+  if (!save && (recorded(x) || recorded(gate) || recorded(up) || recorded(down))) return std::nullopt;
   const c10::cuda::CUDAGuard guard(x.device());
   const int32_t T = (int32_t)x.size(0);
   const size_t need = save ? gated_ffn_saved_bytes(T, &f) : gated_ffn_forward_workspace_bytes(T, &f);

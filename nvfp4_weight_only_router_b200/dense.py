@@ -233,26 +233,26 @@ def mxfp4_linear(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = 
     gated form y [T, N/2] = act(x Wg^T) * (x Wu^T).  Not differentiable: a backward
     pass through y raises."""
     act = _act(activation)
-    if _recorded(x):
-        return _Undifferentiated.apply(lambda: mxfp4_linear(x, weight, activation, stream),
-                                       "mxfp4_linear has no backward pass: give it x.detach()", x)
     if stream is None:
         y = _calls.linear(x, weight.codes, weight.scales, act, False)
         if y is not None:
             return y
+    if _recorded(x):
+        return _Undifferentiated.apply(lambda: mxfp4_linear(x, weight, activation, stream),
+                                       "mxfp4_linear has no backward pass: give it x.detach()", x)
     return _linear("mxfp4_linear", dc.mxfp4_linear, dc.mxfp4_linear_workspace_bytes, x, weight, act, stream)
 
 
 def mxfp4_linear_a4(x: torch.Tensor, weight: Mxfp4Weight, activation: str | None = None, stream=None) -> torch.Tensor:
     """W4A4: mxfp4_linear with x (bf16 or f16) quantised to MXFP4 on the way in."""
     act = _act(activation)
-    if _recorded(x):
-        return _Undifferentiated.apply(lambda: mxfp4_linear_a4(x, weight, activation, stream),
-                                       "mxfp4_linear_a4 has no backward pass: give it x.detach()", x)
     if stream is None:
         y = _calls.linear(x, weight.codes, weight.scales, act, True)
         if y is not None:
             return y
+    if _recorded(x):
+        return _Undifferentiated.apply(lambda: mxfp4_linear_a4(x, weight, activation, stream),
+                                       "mxfp4_linear_a4 has no backward pass: give it x.detach()", x)
     return _linear("mxfp4_linear_a4", dc.mxfp4_linear_a4, dc.mxfp4_linear_a4_workspace_bytes, x, weight, act, stream)
 
 
@@ -281,14 +281,14 @@ def gated_ffn_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, dow
     differ by that rounding.  For autograd there is gated_ffn: a backward pass
     through this y raises, and with save y has no graph, gated_ffn_backward being the
     caller's to call."""
-    if not save and _recorded(x, gate, up, down):
-        return _Undifferentiated.apply(lambda: gated_ffn_forward(x, gate, up, down, activation, stream=stream),
-                                       "gated_ffn_forward has no backward pass of its own: use gated_ffn",
-                                       x, gate, up, down)
     if stream is None:
         out = _calls.ffn_forward(x, gate, up, down, _act(activation, gated=True), save)
         if out is not None:
             return out
+    if not save and _recorded(x, gate, up, down):
+        return _Undifferentiated.apply(lambda: gated_ffn_forward(x, gate, up, down, activation, stream=stream),
+                                       "gated_ffn_forward has no backward pass of its own: use gated_ffn",
+                                       x, gate, up, down)
     f = _ffn_weights(gate, up, down, activation)
     ld = _rows(x, "x", f.H)
     _same("x and the weights", x, gate)

@@ -93,8 +93,10 @@ def test_gradients_are_not_lost_in_silence(dense, monkeypatch):
     before where none is recorded."""
     monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
     monkeypatch.setattr(dense, "_calls", type("Calls", (), {
-        "linear": staticmethod(lambda x, *a: x.detach() + 1), "ffn_forward": staticmethod(
-            lambda x, *a: (x.detach() + 1, torch.zeros(1)) if a[-1] else x.detach() + 1)}))
+        # as the C++ step: nothing where autograd follows
+        "linear": staticmethod(lambda x, *a: None if dense._recorded(x) else x.detach() + 1), "ffn_forward": staticmethod(
+            lambda x, *a: (x.detach() + 1, torch.zeros(1)) if a[-1] else
+            None if dense._recorded(x, *a[:3]) else x.detach() + 1)}))
     weight = dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64)
     x, w = torch.zeros(2, 64), torch.zeros(8, 64)
     calls = {"mxfp4_linear ": lambda x: dense.mxfp4_linear(x, weight), "mxfp4_linear_a4": lambda x: dense.mxfp4_linear_a4(x, weight),
@@ -154,8 +156,8 @@ def test_tangents_are_not_lost_in_silence(dense, monkeypatch):
     """Forward-mode derivatives: refused, as gated_ffn refuses them."""
     import torch.autograd.forward_ad as fw
     monkeypatch.setattr(dense, "_check_codes", lambda *t: None)
-    monkeypatch.setattr(dense, "_calls", type("Calls", (), {"linear": staticmethod(lambda x, *a: x.clone()),
-                                                            "ffn_forward": staticmethod(lambda x, *a: x.clone())}))
+    step = staticmethod(lambda x, *a: None if dense._recorded(x) else x.clone())   # as the C++ step
+    monkeypatch.setattr(dense, "_calls", type("Calls", (), {"linear": step, "ffn_forward": step}))
     weight = dense.Mxfp4Weight(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 2, dtype=torch.uint8), 64)
     x, w = torch.zeros(2, 64), torch.zeros(8, 64)
     for call in (lambda x: dense.mxfp4_linear(x, weight), lambda x: dense.mxfp4_linear_a4(x, weight),

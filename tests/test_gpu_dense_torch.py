@@ -128,3 +128,37 @@ def test_checkpointed_block(dev):
         run(*leaves).float().sum().backward()
         grads.append([t.grad for t in leaves])
     assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
+def test_lost_gradients_are_refused(dev):
+    """An operator without a backward pass: computed as ever, but a backward pass that
+    comes to it raises, and so do forward-mode derivatives."""
+    import torch.autograd.forward_ad as fw
+    x, *w = _make(7, 40, 64, 48, dev)
+    weight = lib.Mxfp4Weight.quantize(w[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    forms = [lambda t, **k: lib.mxfp4_linear(t, weight, **k), lambda t, **k: lib.mxfp4_linear_a4(t, weight, "silu", **k),
+             lambda t, **k: lib.gated_ffn_forward(t, *w, **k)]
+    for f in forms:
+        ref = f(x)
+        leaf = x.clone().requires_grad_()
+        for more in ({}, {"stream": s}):
+            y = f(leaf, **more)
+            s.synchronize()
+            assert torch.equal(y, ref)
+            with pytest.raises(RuntimeError, match="has no backward pass"):
+                (y.float().sum() + leaf.float().sum()).backward()
+        with torch.no_grad():
+            y = f(leaf)
+            assert torch.equal(y, ref) and not y.requires_grad
+        with fw.dual_level():
+            assert torch.equal(f(x), ref)
+            with pytest.raises(NotImplementedError):
+                f(fw.make_dual(x, torch.ones_like(x)))
+    for i in range(3):                                    # a weight that requires a gradient
+        p = [t.clone().requires_grad_(k == i) for k, t in enumerate(w)]
+        with pytest.raises(RuntimeError, match="use gated_ffn"):
+            lib.gated_ffn_forward(x, *p).float().sum().backward()
+        y, saved = lib.gated_ffn_forward(x, *p, save=True)
+        assert not y.requires_grad and lib.gated_ffn_backward(x, x, *p, saved)[i + 1].shape == p[i].shape
