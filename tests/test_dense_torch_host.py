@@ -1,4 +1,6 @@
 """The dense operators' torch side without a GPU: which steps a call takes."""
+import os
+
 import pytest
 import torch
 
@@ -149,7 +151,8 @@ def test_device_status_without_the_dense_library():
             "assert api.device_status() == 3\n"
             "capi.nvfp4_get_device_status = lambda s: 0\n"
             "assert api.device_status() == 0\n")
-    subprocess.run([sys.executable, "-c", code], check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
 
 
 def test_tangents_are_not_lost_in_silence(dense, monkeypatch):
