@@ -162,3 +162,37 @@ def test_lost_gradients_are_refused(dev):
             lib.gated_ffn_forward(x, *p).float().sum().backward()
         y, saved = lib.gated_ffn_forward(x, *p, save=True)
         assert not y.requires_grad and lib.gated_ffn_backward(x, x, *p, saved)[i + 1].shape == p[i].shape
+
+
+def test_threads_call_at_once(dev):
+    """Calls of several threads, each on a stream of its own, which the lock no longer
+    keeps apart; the first of a process among them."""
+    import threading
+    sets = [_make(20 + i, (3, 40, 300, 600)[i], 264, 200, dev) for i in range(4)]
+
+    def calls(x, gate, up, down):
+        dn = lib.Mxfp4Weight.quantize(down[:, :192].contiguous())
+        y, saved = lib.gated_ffn_forward(x, gate, up, down, save=True)
+        return (y, *lib.gated_ffn_backward(y, x, gate, up, down, saved), lib.gated_ffn_forward(x, gate, up, down),
+                lib.mxfp4_dequantize(*lib.mxfp4_quantize(x), x.shape[1]),
+                lib.mxfp4_linear(x[:, :192].contiguous(), dn), lib.mxfp4_linear_a4(x[:, :192].contiguous(), dn))
+    torch.cuda.synchronize()
+    got = [[] for _ in sets]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(40):
+                got[i].append(calls(*sets[i]))
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert lib.device_status() == 0
+    for i, s in enumerate(sets):
+        ref = calls(*s)
+        assert len(got[i]) == 40
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, ref)), i
